@@ -109,6 +109,16 @@ class gs_view_result(C.Structure):
                 ("gate_forced", C.c_int32), ("gate_score", C.c_double)]
 
 
+class gs_tensor(C.Structure):
+    _fields_ = [("data", C.c_void_p), ("rows", C.c_int64), ("cols", C.c_int64), ("stride", C.c_int64),
+                ("type", C.c_int32), ("pad", C.c_int32)]
+
+
+class gs_adam_opts(C.Structure):
+    _fields_ = [("step", C.c_int32), ("pad", C.c_int32), ("lr", C.c_double), ("beta1", C.c_double),
+                ("beta2", C.c_double), ("eps", C.c_double), ("weight_decay", C.c_double)]
+
+
 ALLOC_FN = C.CFUNCTYPE(C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p)
 FREE_FN = C.CFUNCTYPE(None, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p)
 
@@ -165,6 +175,11 @@ def load(path: str = LIB_PATH):
         "gs_export_size": (st, [vp, vp, i32, P(C.c_size_t)]),
         "gs_util_exp": (st, [vp, vp, vp, i64]),
         "gs_util_exp_falloff": (st, [vp, vp, vp, i64]),
+        "gs_embed_fwd": (st, [vp, P(gs_tensor), vp, i32, i64, C.c_float, P(gs_tensor)]),
+        "gs_embed_bwd": (st, [vp, vp, i32, i64, P(gs_tensor), C.c_float, i64, i32, P(gs_tensor)]),
+        "gs_grad_norm": (st, [vp, vp, i32, C.c_double, vp]),
+        "gs_clip_grads": (st, [vp, vp, i32, C.c_double, vp, vp]),
+        "gs_adam_tensors": (st, [vp, vp, vp, vp, vp, vp, i32, P(gs_adam_opts), vp]),
         "gs_train_view": (st, [vp, P(gs_camera), P(gs_params), vp, P(gs_view_opts), P(gs_view_result)]),
     }
     for name, (res, args) in sig.items():
@@ -462,6 +477,138 @@ def gs_adam_step(ctx: Context, proj, params: DeviceScene, m: DeviceScene, v: Dev
     ctx.check(ctx.lib.gs_adam_step(ctx.handle, proj, params.n, params.sh_degree, C.byref(params.ptrs()),
                                    C.byref(m.ptrs()), C.byref(v.ptrs()), _ptr(grad3d), int(step), float(lr),
                                    float(beta1), float(beta2), float(eps)))
+
+
+# ---------------------------------------------------------------------------- tables and tensor lists
+
+GS_F32, GS_F16, GS_BF16, GS_I32, GS_I64 = range(5)
+_type_codes = {}
+
+
+def _type_code(dtype):
+    if not _type_codes:
+        import torch
+        _type_codes.update({torch.float32: GS_F32, torch.float16: GS_F16, torch.bfloat16: GS_BF16,
+                            torch.int32: GS_I32, torch.int64: GS_I64})
+    return _type_codes.get(dtype, -1)
+
+
+def tensor_struct(t, device=None) -> gs_tensor:
+    """gs_tensor of a device tensor: a 2-D tensor with unit column stride (rows may be apart, or one row
+    broadcast), or a contiguous tensor of any other shape, taken as one row."""
+    if not t.is_cuda or (device is not None and t.device != device):
+        raise ValueError(f"a tensor on {t.device}: expected {device or 'a GPU'}")
+    code = _type_code(t.dtype)
+    if code < 0 or code > GS_BF16:
+        raise ValueError(f"element type {t.dtype}: expected float32, float16 or bfloat16")
+    if t.dim() == 2:
+        rows, cols = t.shape
+        stride, inner = t.stride()
+        if inner != 1 and cols > 1:
+            raise ValueError("the columns of a 2-D tensor must be contiguous")
+        return gs_tensor(t.data_ptr(), rows, cols, stride, code, 0)
+    if not t.is_contiguous():
+        raise ValueError("a tensor that is not 2-D must be contiguous")
+    n = t.numel()
+    return gs_tensor(t.data_ptr(), 1, n, n, code, 0)
+
+
+class TensorList:
+    """A list of device tensors described once for gs_grad_norm, gs_clip_grads and gs_adam_tensors (it keeps
+    the tensors alive).  None in the list stands for an absent tensor (a parameter without a copy)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.n = len(self.tensors)
+        self.array = (gs_tensor * max(self.n, 1))()
+        self.device = next((t.device for t in self.tensors if t is not None), None)
+        for k, t in enumerate(self.tensors):
+            if t is not None:
+                self.array[k] = tensor_struct(t, self.device)
+        self.ptr = C.cast(self.array, C.c_void_p)
+
+    def __len__(self):
+        return self.n
+
+
+def _as_list(tensors, ctx):
+    lst = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
+    if lst.device is not None and lst.device != ctx.device:
+        raise ValueError(f"tensors on {lst.device}, the context is on {ctx.device}")
+    return lst
+
+
+def _index(idx, ctx):
+    code = _type_code(idx.dtype)
+    if code < GS_I32 or idx.device != ctx.device or not idx.is_contiguous():
+        raise ValueError("indices must be a contiguous int32 or int64 tensor on the context's device")
+    return code
+
+
+def _norm_ptr(norm, ctx):
+    if norm.device != ctx.device or _type_code(norm.dtype) != GS_F32 or norm.numel() < 2 or not norm.is_contiguous():
+        raise ValueError("norm must be a float32 tensor of two values on the context's device")
+    return norm.data_ptr()
+
+
+def gs_embed_fwd(ctx: Context, table, idx, out=None, scale=1.0):
+    """out[i] = scale * table[idx[i]] (zeros where idx[i] is outside the table); idx of any shape, out
+    idx.numel() x table.shape[1] (allocated in the table's type when None)."""
+    code = _index(idx, ctx)
+    n = idx.numel()
+    if out is None:
+        with ctx.torch.cuda.stream(ctx.stream):
+            out = table.new_empty((n, table.shape[1]))
+    ctx.check(ctx.lib.gs_embed_fwd(ctx.handle, tensor_struct(table, ctx.device), idx.data_ptr(), code, n, scale,
+                                   tensor_struct(out, ctx.device)))
+    return out
+
+
+def gs_embed_bwd(ctx: Context, idx, dout, dtable, scale=1.0, padding=-1, accumulate=False):
+    """dtable[v] = scale * sum of dout[i] over idx[i] == v (added to dtable when accumulate)."""
+    code = _index(idx, ctx)
+    ctx.check(ctx.lib.gs_embed_bwd(ctx.handle, idx.data_ptr(), code, idx.numel(), tensor_struct(dout, ctx.device),
+                                   scale, padding, accumulate, tensor_struct(dtable, ctx.device)))
+    return dtable
+
+
+def gs_grad_norm(ctx: Context, grads, max_norm=float("inf"), norm=None):
+    """norm (device float32 [2], allocated when None): the global norm of grads (a TensorList or tensors)
+    and the clip factor min(1, max_norm / (norm + 1e-6))."""
+    g = _as_list(grads, ctx)
+    if norm is None:
+        with ctx.torch.cuda.stream(ctx.stream):
+            norm = ctx.torch.empty(2, dtype=ctx.torch.float32, device=ctx.device)
+    ctx.check(ctx.lib.gs_grad_norm(ctx.handle, g.ptr, g.n, max_norm, _norm_ptr(norm, ctx)))
+    return norm
+
+
+def gs_clip_grads(ctx: Context, grads, max_norm, norm=None, out=None):
+    """Scale grads by the clip factor, in place or into out (a TensorList or tensors of the same sizes and
+    types); returns norm as gs_grad_norm does."""
+    g = _as_list(grads, ctx)
+    o = None if out is None else _as_list(out, ctx)
+    if o is not None and o.n != g.n:
+        raise ValueError(f"{o.n} outputs for {g.n} gradients")
+    if norm is None:
+        with ctx.torch.cuda.stream(ctx.stream):
+            norm = ctx.torch.empty(2, dtype=ctx.torch.float32, device=ctx.device)
+    ctx.check(ctx.lib.gs_clip_grads(ctx.handle, g.ptr, g.n, max_norm, None if o is None else o.ptr,
+                                    _norm_ptr(norm, ctx)))
+    return norm
+
+
+def gs_adam_tensors(ctx: Context, params, m, v, grads, step, lr=1e-3, beta1=0.9, beta2=0.999, eps=1e-15,
+                    weight_decay=0.0, norm=None, copies=None):
+    """One Adam step over lists of tensors (TensorLists or tensors); norm: as written by gs_grad_norm, whose
+    factor scales the gradients; copies: low-precision copies of the parameters to write (None entries: none)."""
+    p, m, v, g = (_as_list(x, ctx) for x in (params, m, v, grads))
+    k = None if copies is None else _as_list(copies, ctx)
+    if not p.n == m.n == v.n == g.n or (k is not None and k.n != p.n):
+        raise ValueError("the lists have different lengths")
+    o = gs_adam_opts(step, 0, lr, beta1, beta2, eps, weight_decay)
+    ctx.check(ctx.lib.gs_adam_tensors(ctx.handle, p.ptr, m.ptr, v.ptr, g.ptr, None if k is None else k.ptr, p.n, o,
+                                      None if norm is None else _norm_ptr(norm, ctx)))
 
 
 def gs_release(ctx: Context, handle):

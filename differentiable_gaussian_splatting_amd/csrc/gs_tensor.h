@@ -1,0 +1,56 @@
+// gs_tensor.h -- device-side helpers of the tensor-list and table kernels:
+// element types and loads and stores of several values at once.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace gst {
+
+typedef _Float16 f16;
+typedef __bf16 bf16;
+
+// N values in memory, aligned to the element only: rows of odd widths, columns
+// of wider rows and views into flat buffers start anywhere.  The compiler
+// loads and stores a pack of up to 16 bytes in one instruction whatever its
+// alignment (gfx950 global memory takes any).
+template <typename T, int N>
+struct Pack {
+    T v[N];
+};
+
+template <typename T, int N>
+__device__ __forceinline__ Pack<T, N> load(const T* p)
+{
+    Pack<T, N> r;
+    __builtin_memcpy(&r, p, sizeof(r));
+    return r;
+}
+
+template <typename T, int N>
+__device__ __forceinline__ void store(T* p, const Pack<T, N>& r)
+{
+    __builtin_memcpy(p, &r, sizeof(r));
+}
+
+// x rounded to T (to nearest, ties to even).  For f16 the compiler would fuse a
+// product before the conversion into a multiply-add with +0, which turns -0
+// into +0; the empty statement keeps the two apart.
+template <typename T>
+__device__ __forceinline__ T narrow(float x)
+{
+    if constexpr (sizeof(T) == 2) asm("" : "+v"(x));
+    return (T)x;
+}
+
+// Calls f with a value of the element type (GS_F32, GS_F16, GS_BF16).
+template <typename F>
+inline void with_type(int type, F&& f)
+{
+    if (type == 0) f(float{});
+    else if (type == 1) f(f16{});
+    else f(bf16{});
+}
+
+}  // namespace gst

@@ -392,6 +392,94 @@ void gs_gate_destroy(gs_gate* gate);
 gs_status gs_gate_step(gs_gate* gate, int32_t view, double loss, gs_gate_decision* decision);
 gs_status gs_gate_get_stats(const gs_gate* gate, gs_gate_stats* stats);
 
+/* ---- tables, gradient norms and updates of tensor lists ------------------- */
+
+/* A scene may hold an attribute (its SH rows, say) in a table of V rows that
+ * its N Gaussians share, with an index per Gaussian.  A training step then
+ * looks the rows up (gs_embed_fwd), renders the view and forms its gradient
+ * rows (gs_train_view with grad3d_out), sums them into the table's gradient
+ * (gs_embed_bwd), clips the whole gradient to a global norm (gs_clip_grads, or
+ * gs_grad_norm alone) and updates every tensor (gs_adam_tensors).  The calls
+ * take any widths and the element types below, so they also serve token tables
+ * and the parameters of layers.
+ *
+ * All of them are asynchronous on the context's stream, allocate their
+ * workspace from the context's allocator before anything is launched (so an
+ * allocation failure leaves every output untouched) and copy nothing between
+ * host and device: they can be captured into a graph whose allocator serves
+ * captures.  Results do not depend on timing: the same inputs give the same
+ * bits on the same device.  A tensor written on another stream than the
+ * context's must be complete, or its stream waited for, before the call. */
+enum { GS_F32 = 0, GS_F16 = 1, GS_BF16 = 2, GS_I32 = 3, GS_I64 = 4 };
+
+/* A device matrix of rows x cols values, value (r, c) at data[r stride + c].
+ * rows, cols >= 0; no value is read where either is 0.  A tensor that is only
+ * read may have any stride >= 0 (0: one row, broadcast); one that is written
+ * needs stride >= cols unless it has at most one row.  data is aligned to its
+ * element, no more. */
+typedef struct {
+    void* data;
+    int64_t rows, cols, stride;
+    int32_t type;        /* GS_F32, GS_F16 or GS_BF16 */
+    int32_t pad;
+} gs_tensor;
+
+/* Rows of a table by index: out[i, c] = scale table[idx[i], c] in f32, rounded
+ * once to out's type (to nearest, ties to even); a row of zeros where idx[i]
+ * is outside [0, table->rows) (a masked token).  idx: device, n contiguous
+ * GS_I32 or GS_I64 values.  out: n x table->cols.  Table and out may have
+ * different types.  Errors: INVALID_ARG, OVERFLOW (n or table->rows >= 2^31,
+ * cols >= 2^31), DEVICE. */
+gs_status gs_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx, int32_t idx_type, int64_t n, float scale,
+                       const gs_tensor* out);
+
+/* Gradient of gs_embed_fwd with respect to the table: dtable[v, c] = scale
+ * times the sum of dout[i, c] over the i with idx[i] = v, plus the old
+ * dtable[v, c] when accumulate != 0.  Sums in f32, in an order that depends on
+ * idx alone (ascending i in fixed pieces), rounded once to dtable's type.
+ * Indices outside [0, dtable->rows) and those equal to padding (any value
+ * outside that range: none) add nothing, and their rows of dout are not read.
+ * Rows without an index become zero, or stay as they are when accumulating.
+ * dout: n x dtable->cols.  Errors: as gs_embed_fwd, and OOM. */
+gs_status gs_embed_bwd(gs_ctx* ctx, const void* idx, int32_t idx_type, int64_t n, const gs_tensor* dout, float scale,
+                       int64_t padding, int32_t accumulate, const gs_tensor* dtable);
+
+/* Global norm of a list of n_tensors gradients, all their values taken as one
+ * vector: norm[0] = sqrt(sum g^2) (squares and sums in f64, rounded once) and
+ * the clip factor norm[1] = min(1, max_norm / (norm + 1e-6)).  norm: device, two
+ * floats.  max_norm >= 0, +inf for the norm alone (factor 1).  A value that is
+ * not finite makes norm[0] inf or NaN and norm[1] 0 or NaN.  grads: host array
+ * of n_tensors >= 0 descriptors.  Errors: INVALID_ARG, OOM, DEVICE. */
+gs_status gs_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, double max_norm, float* norm);
+
+/* gs_grad_norm, then out[k] = norm[1] grads[k] for every tensor, in f32 and
+ * rounded once.  out: n_tensors descriptors of the same sizes and types, or
+ * NULL to scale grads in place (no value is written when the factor is 1). */
+gs_status gs_clip_grads(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, double max_norm, const gs_tensor* out,
+                        float* norm);
+
+typedef struct {
+    int32_t step;              /* >= 1: number of this step                  */
+    int32_t pad;
+    double lr, beta1, beta2, eps, weight_decay;
+} gs_adam_opts;
+
+/* One Adam step over a list of n_tensors tensors, with decoupled weight decay:
+ *   g' = c g,  m = beta1 m + (1 - beta1) g',  v = beta2 v + (1 - beta2) g'^2,
+ *   p = p (1 - lr weight_decay)
+ *       - lr / (1 - beta1^step) m / (sqrt(v / (1 - beta2^step)) + eps),
+ * c = norm[1] where norm (device, as written by gs_grad_norm) is given, else 1.
+ * When norm[0] is not finite nothing is changed: a step whose gradient
+ * overflowed is left out.  params, m, v: GS_F32; grads: any type; copies
+ * (NULL, or one per tensor; data NULL: none for that tensor): the new
+ * parameters rounded to the copy's type.  All of a tensor's descriptors have
+ * its rows and cols; params, m, v and copies are contiguous (stride = cols, or
+ * at most one row), grads may be strided.  Each parameter is updated from its
+ * own values alone.  Errors: INVALID_ARG, DEVICE. */
+gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor* m, const gs_tensor* v,
+                          const gs_tensor* grads, const gs_tensor* copies, int32_t n_tensors,
+                          const gs_adam_opts* opts, const float* norm);
+
 /* ---- one whole view ---------------------------------------------------- */
 
 typedef struct {
