@@ -10,6 +10,9 @@
 #include "gs_internal.h"
 #include "gs_tensor.h"
 
+#include <algorithm>
+#include <type_traits>
+
 namespace {
 
 using gst::narrow;
@@ -39,38 +42,332 @@ __global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, 
     }
 }
 
+// ---------------------------------------------------------------------------
+// The backward: (1) the positions sorted by (row, position); (2) sums over
+// chunks of sorted positions; (3) the runs that cross blocks joined.
+//
+// (1) and, beside it in the same launch, the zero rows: blocks past `sorters`
+// write zeros over all of dtable (not when accumulating), and (2) and (3)
+// overwrite the rows that have positions.
+
+struct ZeroJob {
+    char* p;            // null: nothing to clear
+    int64_t rows;       // rows of `bytes` bytes, `stride` bytes apart
+    int64_t bytes, stride;
+};
+
+__device__ __forceinline__ void clear_rows(const ZeroJob& z, int64_t blk, int64_t nblk)
+{
+    const gst::Pack<uint16_t, 8> zero{};
+    const int64_t step = nblk * blockDim.x * 16, lane0 = (blk * blockDim.x + threadIdx.x) * 16;
+    if (z.rows == 1) {
+        for (int64_t b = lane0; b < z.bytes; b += step) {
+            if (b + 16 <= z.bytes) gst::store(reinterpret_cast<uint16_t*>(z.p + b), zero);
+            else
+                for (int64_t q = b; q < z.bytes; q += 2) *reinterpret_cast<uint16_t*>(z.p + q) = 0;
+        }
+        return;
+    }
+    for (int64_t r = blk; r < z.rows; r += nblk) {
+        char* row = z.p + r * z.stride;
+        for (int64_t q = 2 * (int64_t)threadIdx.x; q < z.bytes; q += 2 * blockDim.x)
+            *reinterpret_cast<uint16_t*>(row + q) = 0;
+    }
+}
+
 template <typename I>
 __global__ __launch_bounds__(256) void k_embed_keys(const I* __restrict__ idx, int64_t n, uint32_t rows, int64_t skip,
-                                                    uint32_t* __restrict__ keys, uint32_t* __restrict__ pos)
+                                                    uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
+                                                    uint32_t sorters, ZeroJob zero)
 {
+    if (blockIdx.x >= sorters) {
+        clear_rows(zero, blockIdx.x - sorters, gridDim.x - sorters);
+        return;
+    }
     const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     if (i >= n) return;
     keys[i] = row_of(idx, i, rows, skip);
     pos[i] = (uint32_t)i;
 }
 
-// one thread per value of dtable: the sum over its row's positions
-template <typename T, typename O>
-__global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride,
-                                                   const uint64_t* __restrict__ first, const uint32_t* __restrict__ pos,
-                                                   uint32_t rows, uint32_t cols, float scale, int accumulate,
-                                                   O* __restrict__ dtable, int64_t ostride)
+// Sort of few positions by counting: position i goes to the place
+//   #{j : key_j < key_i} + #{j < i : key_j = key_i} = #{j < i : key_j < key_i + 1} + #{j > i : key_j < key_i},
+// one compare and one add per pair.  A block ranks 64 positions (one per
+// lane), its 16 wavefronts each count a sixteenth of the keys, which are
+// staged in LDS and read four at a time by all lanes from one address.
+constexpr int kRankThreads = 1024;
+template <typename I>
+__global__ __launch_bounds__(kRankThreads) void k_embed_rank(const I* __restrict__ idx, int n, uint32_t rows,
+                                                             int64_t skip, uint32_t* __restrict__ keys,
+                                                             uint32_t* __restrict__ pos, uint32_t sorters,
+                                                             ZeroJob zero)
 {
-    const int64_t total = (int64_t)rows * cols, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < total; k += step) {
-        const int64_t v = k / cols;
-        const uint32_t c = (uint32_t)(k - v * cols);
-        const uint64_t a = first[v], b = first[v + 1];
-        O* o = dtable + v * ostride + c;
-        if (a == b) {
-            if (!accumulate) *o = (O)0.0f;
-            continue;
+    extern __shared__ uint4 sk4[];
+    __shared__ uint32_t cnt[kRankThreads / 64][64];
+    if (blockIdx.x >= sorters) {
+        clear_rows(zero, blockIdx.x - sorters, gridDim.x - sorters);
+        return;
+    }
+    uint32_t* sk = reinterpret_cast<uint32_t*>(sk4);
+    const int n4 = (n + 3) / 4;
+    for (int j = threadIdx.x; j < 4 * n4; j += kRankThreads) sk[j] = j < n ? row_of(idx, j, rows, skip) : 0xFFFFFFFFu;
+    __syncthreads();
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int i0 = blockIdx.x * 64, i = i0 + lane;
+    const uint32_t ki = i < n ? sk[i] : 0u;
+    const int per = (n4 + kRankThreads / 64 - 1) / (kRankThreads / 64);
+    const int q0 = wave * per, q1 = min(n4, q0 + per);
+    const int b0 = i0 / 4, b1 = b0 + 16;   // the block's own positions, in fours
+    uint32_t c = 0;
+    auto count = [&](int qa, int qb, uint32_t thr) {
+#pragma unroll 4
+        for (int q = qa; q < qb; ++q) {
+            const uint4 k = sk4[q];
+            c += (k.x < thr ? 1u : 0u) + (k.y < thr ? 1u : 0u) + (k.z < thr ? 1u : 0u) + (k.w < thr ? 1u : 0u);
         }
-        float s = 0.0f;
-        for (uint64_t j = a; j < b; ++j) s += (float)dout[(int64_t)pos[j] * dstride + c];
-        *o = narrow<O>(accumulate ? (float)*o + scale * s : scale * s);
+    };
+    count(q0, min(q1, b0), ki + 1u);
+    for (int q = max(q0, b0); q < min(q1, b1); ++q)
+        for (int e = 0; e < 4; ++e) c += sk[4 * q + e] < ki + (4 * q + e < i ? 1u : 0u) ? 1u : 0u;
+    count(max(q0, b1), q1, ki);
+    cnt[wave][lane] = c;
+    __syncthreads();
+    if (wave == 0 && i < n) {
+        uint32_t r = 0;
+        for (int w = 0; w < kRankThreads / 64; ++w) r += cnt[w][lane];
+        keys[r] = ki;
+        pos[r] = (uint32_t)i;
     }
 }
+
+// How (2) and (3) split the sorted positions and the columns.  A team of
+// `1 << lg` lanes, each holding VEC neighbouring columns (16 bytes), adds up
+// the rows of `chunk` positions; a block's 256 >> lg teams take neighbouring
+// chunks.
+struct SumShape {
+    const uint32_t* keys;   // [n] rows in ascending order, `rows` for what is left out
+    const uint32_t* pos;    // [n] positions, ascending within a row
+    int64_t n;
+    uint32_t rows, cols;
+    int lg;
+    int chunk;              // a multiple of 8
+    int64_t per_block;      // chunk * teams
+    float* head;            // [blocks][cols] sum of the run that reaches a block from before
+    float* tail;            // [blocks][cols] sum of the run that starts in a block and goes on after it
+};
+
+struct Dest {
+    void* p;
+    int64_t stride;
+    int type, accumulate;
+    float scale;
+};
+
+// the columns [c0, c1) of row v: scale s (+ old), rounded once
+template <int VEC>
+__device__ __forceinline__ void put_row(const Dest& d, uint32_t v, uint32_t c0, uint32_t cb, uint32_t cols,
+                                        const float* s)
+{
+    auto put = [&](auto* base) {
+        using O = std::remove_pointer_t<decltype(base)>;
+        O* o = base + (int64_t)v * d.stride;
+        if (cb == c0) {
+            gst::Pack<O, VEC> r;
+            if (d.accumulate) r = gst::load<O, VEC>(o + c0);
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                r.v[e] = narrow<O>(d.accumulate ? (float)r.v[e] + d.scale * s[e] : d.scale * s[e]);
+            gst::store<O, VEC>(o + c0, r);
+        } else {   // the last lane of a row whose width is no multiple of VEC: its own columns only
+#pragma unroll
+            for (int e = 0; e < VEC; ++e)
+                if (cb + e >= c0) {
+                    const float x = d.scale * s[e];
+                    o[cb + e] = narrow<O>(d.accumulate ? (float)o[cb + e] + x : x);
+                }
+        }
+    };
+    if (d.type == GS_F32) put((float*)d.p);
+    else if (d.type == GS_F16) put((gst::f16*)d.p);
+    else put((gst::bf16*)d.p);
+}
+
+// the same columns of a row of f32 partials
+template <int VEC>
+__device__ __forceinline__ void put_part(float* row, uint32_t c0, uint32_t cb, const float* s)
+{
+    if (cb == c0) {
+        gst::Pack<float, VEC> r;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) r.v[e] = s[e];
+        gst::store<float, VEC>(row + c0, r);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (cb + e >= c0) row[cb + e] = s[e];
+    }
+}
+
+// (2) Each team walks its chunk in fours of positions, eight rows in flight,
+// and adds rows while the table row stays the same.  A run inside the chunk is
+// written at once.  The chunk's first run, if it began before, and its last,
+// if it goes on, are left in LDS; after the block's teams are done, the team
+// in which a run begins adds the pieces of the teams after it, in order, and
+// writes the row, or the block's piece of it (head / tail) if the run leaves
+// the block.
+constexpr int kBatch = 8;
+template <typename T, int VEC>
+__global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride, SumShape sh, Dest d)
+{
+    __shared__ float head[256 * VEC], tail[256 * VEC];
+    __shared__ uint32_t flags[256];   // per team: 1 head, 2 tail, 4 one run from before to after the chunk
+    __shared__ uint32_t hrow[256], trow[256];
+    const int lanes = 1 << sh.lg, teams = 256 >> sh.lg;
+    const int team = threadIdx.x >> sh.lg, lane = threadIdx.x & (lanes - 1);
+    const uint32_t c0 = ((uint32_t)blockIdx.y * lanes + lane) * VEC;
+    const bool on = c0 < sh.cols;                                  // this lane has columns
+    const uint32_t cb = min(c0, sh.cols - VEC);                    // where it loads them (cols >= VEC)
+    const int64_t s = (int64_t)blockIdx.x * sh.per_block + (int64_t)team * sh.chunk;
+    const int64_t e = min(sh.n, s + sh.chunk);
+    float acc[VEC];
+    uint32_t fl = 0;
+    if (s < e) {
+        uint32_t cur = sh.keys[s];
+        const uint32_t first = cur;
+        const bool from = s > 0 && sh.keys[s - 1] == cur && cur < sh.rows;
+        bool in_first = true;
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
+        const T* col = dout + cb;
+        for (int64_t j = s; j < e; j += kBatch) {
+            const auto k = gst::load<uint32_t, kBatch>(sh.keys + j);   // arrays padded to whole batches
+            const auto p = gst::load<uint32_t, kBatch>(sh.pos + j);
+            gst::Pack<T, VEC> x[kBatch];
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b)
+                if (on && j + b < e && k.v[b] < sh.rows) x[b] = gst::load<T, VEC>(col + (int64_t)p.v[b] * dstride);
+#pragma unroll
+            for (int b = 0; b < kBatch; ++b) {
+                if (j + b >= e || k.v[b] >= sh.rows) continue;
+                if (k.v[b] != cur) {
+                    // the run of `cur` ends here
+                    if (in_first && from) {
+                        fl |= 1;
+                        if (on) {
+#pragma unroll
+                            for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+                        }
+                    } else if (on) {
+                        put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+                    }
+                    in_first = false;
+                    cur = k.v[b];
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
+                }
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] += (float)x[b].v[q];
+            }
+        }
+        if (cur < sh.rows) {
+            const bool on_after = e < sh.n && sh.keys[e] == cur;
+            if (in_first && from) {
+                fl |= on_after ? 5 : 1;
+                if (on) {
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+                }
+            } else if (on_after) {
+                fl |= 2;
+                if (on) {
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) tail[threadIdx.x * VEC + q] = acc[q];
+                }
+            } else if (on) {
+                put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+            }
+        }
+        if (lane == 0) {
+            hrow[team] = first;
+            trow[team] = cur;
+        }
+    }
+    if (lane == 0) flags[team] = fl;
+    __syncthreads();
+    if (!on) return;
+    // runs that begin in this team and go on, and (team 0) the block's first run if it began before
+    auto follow = [&](const float* piece, bool goes_on, bool from_before, uint32_t row) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] = piece[threadIdx.x * VEC + q];
+        int t = team;
+        while (goes_on && ++t < teams) {
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += head[((t << sh.lg) + lane) * VEC + q];
+            goes_on = (flags[t] & 4) != 0;
+        }
+        if (from_before) put_part<VEC>(sh.head + (int64_t)blockIdx.x * sh.cols, c0, cb, acc);
+        else if (goes_on) put_part<VEC>(sh.tail + (int64_t)blockIdx.x * sh.cols, c0, cb, acc);
+        else put_row<VEC>(d, row, c0, cb, sh.cols, acc);
+    };
+    if (team == 0 && (fl & 1)) follow(head, (fl & 4) != 0, true, hrow[0]);
+    if (fl & 2) follow(tail, true, false, trow[team]);
+}
+
+// (3) One block per border between blocks of (2): if a run begins in the block
+// before it and crosses the border, its tail and the heads of the blocks after
+// it are added, the teams taking every teams-th piece, their sums in order.
+template <int VEC>
+__global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
+{
+    __shared__ float part[256 * VEC];
+    __shared__ uint32_t more[4];
+    const int64_t b = blockIdx.x, end = (b + 1) * sh.per_block;
+    const uint32_t row = sh.keys[end];   // end < n: only inner borders are launched
+    if (row >= sh.rows || sh.keys[end - 1] != row) return;
+    if (b > 0 && sh.keys[b * sh.per_block - 1] == row) return;   // it began earlier
+    // blocks b + 1 .. b + m hold its heads: block t does if the key at its start is row
+    const int64_t blocks = gridDim.x + 1;
+    int64_t m = 0;
+    for (;;) {
+        const int64_t t = b + 1 + m + threadIdx.x;
+        const uint64_t yes = gsd::ballot(t < blocks && sh.keys[t * sh.per_block] == row);
+        if ((threadIdx.x & 63) == 0) more[threadIdx.x >> 6] = (uint32_t)__popcll(yes);
+        __syncthreads();
+        const uint32_t got = more[0] + more[1] + more[2] + more[3];
+        __syncthreads();
+        m += got;
+        if (got < 256) break;
+    }
+    const int lanes = 1 << sh.lg, teams = 256 >> sh.lg;
+    const int team = threadIdx.x >> sh.lg, lane = threadIdx.x & (lanes - 1);
+    const uint32_t c0 = ((uint32_t)blockIdx.y * lanes + lane) * VEC;
+    const bool on = c0 < sh.cols;
+    const uint32_t cb = min(c0, sh.cols - VEC);
+    float acc[VEC];
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
+    if (on) {
+#pragma unroll 4
+        for (int64_t t = team; t <= m; t += teams) {   // piece 0: the tail
+            const float* src = t == 0 ? sh.tail + b * sh.cols : sh.head + (b + t) * sh.cols;
+            const auto x = gst::load<float, VEC>(src + cb);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += x.v[q];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) part[threadIdx.x * VEC + q] = acc[q];
+    __syncthreads();
+    if (!on || team != 0) return;
+    for (int t = 1; t < teams && t <= m; ++t) {
+#pragma unroll
+        for (int q = 0; q < VEC; ++q) acc[q] += part[((t << sh.lg) + lane) * VEC + q];
+    }
+    put_row<VEC>(d, row, c0, cb, sh.cols, acc);
+}
+
+// positions up to which the sort counts instead of distributing by digits
+constexpr int64_t kRankMax = 12288;
 
 unsigned flat_grid(int64_t total) { return (unsigned)std::min<int64_t>(std::max<int64_t>(ceil_div(total, 256), 1), 1 << 20); }
 
@@ -103,39 +400,102 @@ gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx,
 gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n, const gs_tensor* dout, float scale,
                            int64_t padding, int accumulate, const gs_tensor* dtable, std::vector<GsAlloc>* tmp)
 {
-    const int64_t rows = dtable->rows;
-    if (rows == 0 || dtable->cols == 0) return GS_OK;
-    const int64_t m = std::max<int64_t>(n, 1);
+    const int64_t rows = dtable->rows, cols = dtable->cols;
+    if (rows == 0 || cols == 0 || (n == 0 && accumulate)) return GS_OK;
+    const int64_t esize = dtable->type == GS_F32 ? 4 : 2;
+    const bool dense = rows == 1 || dtable->stride == cols;
+    const ZeroJob zero = accumulate ? ZeroJob{} : ZeroJob{(char*)dtable->data, dense ? 1 : rows,
+                                                          (dense ? rows : 1) * cols * esize, dtable->stride * esize};
+
+    // the split: columns per lane (16 bytes of dout, or fewer in narrow
+    // rows), lanes per team, positions per team
+    const int most = dout->type == GS_F32 ? 4 : 8;
+    int vec = 1;
+    while (2 * vec <= most && 2 * vec <= cols) vec *= 2;
+    int lg = 0;
+    while (lg < 6 && (int64_t)vec << lg < cols) ++lg;
+    const int64_t slabs = ceil_div(cols, (int64_t)vec << lg);
+    // sixteen wavefronts for each compute unit, in chunks of 8 to 256 positions
+    const int64_t want = (n * slabs << lg) / (64 * 16 * (int64_t)ctx->num_cu);
+    SumShape sh{};
+    sh.n = n;
+    sh.rows = (uint32_t)rows;
+    sh.cols = (uint32_t)cols;
+    sh.lg = lg;
+    sh.chunk = (int)std::min<int64_t>(256, std::max<int64_t>(kBatch, want / kBatch * kBatch));
+    sh.per_block = (int64_t)sh.chunk * (256 >> lg);
+    const int64_t blocks = ceil_div(n, sh.per_block);
+    if (slabs > 65535) return gs_fail(ctx, GS_ERR_OVERFLOW, "rows of %lld values", (long long)cols);
+
+    const int64_t m = ceil_div(std::max<int64_t>(n, 1), kBatch) * kBatch;
+    const bool rank = n <= kRankMax;
     uint32_t* k0 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
     uint32_t* v0 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-    uint32_t* k1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-    uint32_t* v1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-    uint32_t* scratch = (uint32_t*)gs_malloc(ctx, 4 * radix_scratch_words(m), GS_MEM_SCRATCH, tmp);
-    uint64_t* first = (uint64_t*)gs_malloc(ctx, 8 * (rows + 2), GS_MEM_SCRATCH, tmp);
-    if (!k0 || !v0 || !k1 || !v1 || !scratch || !first) return GS_ERR_OOM;
-    if (n > 0) {
-        GsTimerScope ts(ctx, "embed_bwd");
-        const dim3 grid((unsigned)ceil_div(n, 256));
-        if (idx_type == GS_I32)
-            hipLaunchKernelGGL((k_embed_keys<int32_t>), grid, dim3(256), 0, ctx->stream, (const int32_t*)idx, n,
-                               (uint32_t)rows, padding, k0, v0);
-        else
-            hipLaunchKernelGGL((k_embed_keys<int64_t>), grid, dim3(256), 0, ctx->stream, (const int64_t*)idx, n,
-                               (uint32_t)rows, padding, k0, v0);
+    uint32_t *k1 = nullptr, *v1 = nullptr, *scratch = nullptr;
+    bool ok = k0 && v0;
+    if (!rank) {
+        k1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
+        v1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
+        scratch = (uint32_t*)gs_malloc(ctx, 4 * radix_scratch_words(m), GS_MEM_SCRATCH, tmp);
+        ok = ok && k1 && v1 && scratch;
+    }
+    if (blocks > 1) {
+        sh.head = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
+        sh.tail = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
+        ok = ok && sh.head && sh.tail;
+    }
+    if (!ok) return GS_ERR_OOM;
+
+    {
+        GsTimerScope ts(ctx, "embed_sort");
+        const int threads = rank ? kRankThreads : 256;
+        const uint32_t sorters = (uint32_t)ceil_div(n, rank ? 64 : 256);
+        const int64_t clear = zero.p ? std::min<int64_t>(ceil_div(zero.rows * zero.bytes, 16 * threads), 8 * ctx->num_cu)
+                                     : 0;
+        const dim3 grid(sorters + (uint32_t)clear);
+        const size_t lds = rank ? 16 * (size_t)ceil_div(n, 4) : 0;
+        auto go = [&](auto i) {
+            using I = decltype(i);
+            if (rank)
+                hipLaunchKernelGGL((k_embed_rank<I>), grid, dim3(threads), lds, ctx->stream, (const I*)idx, (int)n,
+                                   (uint32_t)rows, padding, k0, v0, sorters, zero);
+            else
+                hipLaunchKernelGGL((k_embed_keys<I>), grid, dim3(threads), 0, ctx->stream, (const I*)idx, n,
+                                   (uint32_t)rows, padding, k0, v0, sorters, zero);
+        };
+        if (grid.x > 0) {
+            if (idx_type == GS_I32) go(int32_t{});
+            else go(int64_t{});
+        }
+    }
+    if (n == 0) {
+        GS_HIP(ctx, hipGetLastError());
+        return GS_OK;
     }
     bool second = false;
-    gs_status st = launch_radix_sort(ctx, k0, v0, k1, v1, n, bits_for(rows + 1), &second, nullptr, 0, nullptr, scratch);
-    if (st == GS_OK) st = launch_seg_offsets(ctx, second ? k1 : k0, n, rows + 1, 0xFFFFFFFFu, first);
-    if (st != GS_OK) return st;
-    GsTimerScope ts(ctx, "embed_bwd");
+    if (!rank) {
+        const gs_status st = launch_radix_sort(ctx, k0, v0, k1, v1, n, bits_for(rows + 1), &second, nullptr, 0,
+                                               nullptr, scratch);
+        if (st != GS_OK) return st;
+    }
+    sh.keys = second ? k1 : k0;
+    sh.pos = second ? v1 : v0;
+    const Dest d{dtable->data, dtable->stride, dtable->type, accumulate, scale};
+    GsTimerScope ts(ctx, "embed_sum");
+    auto sum = [&](auto t, auto v) {
+        using T = decltype(t);
+        constexpr int VEC = decltype(v)::value;
+        hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3((unsigned)blocks, (unsigned)slabs), dim3(256), 0, ctx->stream,
+                           (const T*)dout->data, dout->stride, sh, d);
+        if (blocks > 1)
+            hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)(blocks - 1), (unsigned)slabs), dim3(256), 0,
+                               ctx->stream, sh, d);
+    };
     with_type(dout->type, [&](auto t) {
-        with_type(dtable->type, [&](auto o) {
-            using T = decltype(t);
-            using O = decltype(o);
-            hipLaunchKernelGGL((k_embed_sum<T, O>), dim3(flat_grid(rows * dtable->cols)), dim3(256), 0, ctx->stream,
-                               (const T*)dout->data, dout->stride, first, second ? v1 : v0, (uint32_t)rows,
-                               (uint32_t)dtable->cols, scale, accumulate, (O*)dtable->data, dtable->stride);
-        });
+        if (vec == 1) sum(t, std::integral_constant<int, 1>{});
+        else if (vec == 2) sum(t, std::integral_constant<int, 2>{});
+        else if (vec == 4) sum(t, std::integral_constant<int, 4>{});
+        else if constexpr (sizeof(t) == 2) sum(t, std::integral_constant<int, 8>{});
     });
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;
