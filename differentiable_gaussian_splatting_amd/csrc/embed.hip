@@ -27,18 +27,57 @@ __device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i,
     return v >= 0 && v < (int64_t)rows && v != skip ? (uint32_t)v : rows;
 }
 
-// one thread per value of out
-template <typename T, typename O, typename I>
-__global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, int64_t tstride, uint32_t rows,
-                                                   const I* __restrict__ idx, int64_t n, uint32_t cols, float scale,
-                                                   O* __restrict__ out, int64_t ostride)
+// The rows of out are cut into packs of VEC values (16 bytes of the wider
+// type); the last pack of a row whose width is no multiple of VEC starts
+// earlier and repeats some of the values before it.  A thread looks up U
+// packs, 256 apart, so that a wavefront writes 1 KB of neighbouring packs and
+// has its U indices, then its U table packs, in flight together.  Pack k of a
+// block is in row (rem + k) / per_row from the block's first row: a product
+// with `magic` (floor(2^32 / per_row) + 1, exact for k per_row < 2^32) where
+// 1 < per_row < 1024, else a compare (a block then meets at most two rows).
+struct FwdShape {
+    int64_t n, packs;      // rows of out; packs in all
+    uint32_t rows, cols;
+    uint32_t per_row, magic;
+    int64_t tstride, ostride;
+    float scale;
+};
+
+template <typename T, typename O, typename I, int VEC, int U>
+__global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, const I* __restrict__ idx,
+                                                   O* __restrict__ out, FwdShape sh)
 {
-    const int64_t total = n * cols, step = (int64_t)gridDim.x * blockDim.x;
-    for (int64_t k = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; k < total; k += step) {
-        const int64_t i = k / cols;
-        const uint32_t c = (uint32_t)(k - i * cols);
-        const uint32_t r = row_of(idx, i, rows, -1);
-        out[i * ostride + c] = r < rows ? narrow<O>(scale * (float)table[r * tstride + c]) : (O)0.0f;
+    const int64_t base = (int64_t)blockIdx.x * (256 * U);
+    const int64_t row0 = base / sh.per_row;
+    const uint32_t rem = (uint32_t)(base - row0 * sh.per_row);
+    int64_t row[U];
+    uint32_t col[U], src[U];
+    gst::Pack<T, VEC> x[U];
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        const uint32_t k = rem + threadIdx.x + 256 * q;
+        const uint32_t r = sh.per_row == 1     ? k
+                           : sh.per_row < 1024 ? __umulhi(k, sh.magic)
+                                               : (k >= sh.per_row ? 1u : 0u);
+        row[q] = row0 + r;
+        col[q] = min((k - r * sh.per_row) * VEC, sh.cols - VEC);
+        src[q] = row[q] < sh.n ? row_of(idx, row[q], sh.rows, -1) : sh.rows;
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        if (src[q] < sh.rows) x[q] = gst::load<T, VEC>(table + (int64_t)src[q] * sh.tstride + col[q]);
+        else {
+#pragma unroll
+            for (int e = 0; e < VEC; ++e) x[q].v[e] = (T)0.0f;
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < U; ++q) {
+        if (row[q] >= sh.n) continue;
+        gst::Pack<O, VEC> y;
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y.v[e] = src[q] < sh.rows ? narrow<O>(sh.scale * (float)x[q].v[e]) : (O)0.0f;
+        gst::store<O, VEC>(out + row[q] * sh.ostride + col[q], y);
     }
 }
 
@@ -96,6 +135,7 @@ __global__ __launch_bounds__(256) void k_embed_keys(const I* __restrict__ idx, i
 // lane), its 16 wavefronts each count a sixteenth of the keys, which are
 // staged in LDS and read four at a time by all lanes from one address.
 constexpr int kRankThreads = 1024;
+constexpr int64_t kRankMax = 12288;   // positions up to which it is used
 template <typename I>
 __global__ __launch_bounds__(kRankThreads) void k_embed_rank(const I* __restrict__ idx, int n, uint32_t rows,
                                                              int64_t skip, uint32_t* __restrict__ keys,
@@ -366,31 +406,53 @@ __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
     put_row<VEC>(d, row, c0, cb, sh.cols, acc);
 }
 
-// positions up to which the sort counts instead of distributing by digits
-constexpr int64_t kRankMax = 12288;
-
-unsigned flat_grid(int64_t total) { return (unsigned)std::min<int64_t>(std::max<int64_t>(ceil_div(total, 256), 1), 1 << 20); }
-
 }  // namespace
 
 gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx, int idx_type, int64_t n, float scale,
                            const gs_tensor* out)
 {
-    if (n == 0 || table->cols == 0) return GS_OK;
+    const int64_t cols = table->cols;
+    if (n == 0 || cols == 0) return GS_OK;
+    const int most = table->type == GS_F32 || out->type == GS_F32 ? 4 : 8;
+    int vec = 1;
+    while (2 * vec <= most && 2 * vec <= cols) vec *= 2;
+    FwdShape sh{};
+    sh.n = n;
+    sh.rows = (uint32_t)table->rows;
+    sh.cols = (uint32_t)cols;
+    sh.per_row = (uint32_t)ceil_div(cols, vec);
+    sh.magic = sh.per_row > 1 ? (uint32_t)((1ull << 32) / sh.per_row) + 1u : 0u;
+    sh.packs = n * sh.per_row;
+    sh.tstride = table->stride;
+    sh.ostride = out->stride;
+    sh.scale = scale;
+    // one pack per thread until every compute unit has eight blocks
+    const bool one = sh.packs <= (int64_t)ctx->num_cu * 8 * 256;
+    const int64_t blocks = ceil_div(sh.packs, one ? 256 : 1024);
+    if (blocks > 0x7FFFFFFF) return gs_fail(ctx, GS_ERR_OVERFLOW, "lookup of %lld x %lld values", (long long)n,
+                                            (long long)cols);
     GsTimerScope ts(ctx, "embed_fwd");
+    auto go = [&](auto t, auto o, auto i, auto v, auto u) {
+        using T = decltype(t);
+        using O = decltype(o);
+        using I = decltype(i);
+        hipLaunchKernelGGL((k_embed_fwd<T, O, I, decltype(v)::value, decltype(u)::value>), dim3((unsigned)blocks),
+                           dim3(256), 0, ctx->stream, (const T*)table->data, (const I*)idx, (O*)out->data, sh);
+    };
     with_type(table->type, [&](auto t) {
         with_type(out->type, [&](auto o) {
-            using T = decltype(t);
-            using O = decltype(o);
-            const dim3 grid(flat_grid(n * table->cols));
-            if (idx_type == GS_I32)
-                hipLaunchKernelGGL((k_embed_fwd<T, O, int32_t>), grid, dim3(256), 0, ctx->stream,
-                                   (const T*)table->data, table->stride, (uint32_t)table->rows, (const int32_t*)idx, n,
-                                   (uint32_t)table->cols, scale, (O*)out->data, out->stride);
-            else
-                hipLaunchKernelGGL((k_embed_fwd<T, O, int64_t>), grid, dim3(256), 0, ctx->stream,
-                                   (const T*)table->data, table->stride, (uint32_t)table->rows, (const int64_t*)idx, n,
-                                   (uint32_t)table->cols, scale, (O*)out->data, out->stride);
+            auto sized = [&](auto v) {
+                auto unrolled = [&](auto u) {
+                    if (idx_type == GS_I32) go(t, o, int32_t{}, v, u);
+                    else go(t, o, int64_t{}, v, u);
+                };
+                if (one) unrolled(std::integral_constant<int, 1>{});
+                else unrolled(std::integral_constant<int, 4>{});
+            };
+            if (vec == 1) sized(std::integral_constant<int, 1>{});
+            else if (vec == 2) sized(std::integral_constant<int, 2>{});
+            else if (vec == 4) sized(std::integral_constant<int, 4>{});
+            else if constexpr (sizeof(t) == 2 && sizeof(o) == 2) sized(std::integral_constant<int, 8>{});
         });
     });
     GS_HIP(ctx, hipGetLastError());
