@@ -29,56 +29,43 @@ __device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i,
 
 // The rows of out are cut into packs of VEC values (16 bytes of the wider
 // type); the last pack of a row whose width is no multiple of VEC starts
-// earlier and repeats some of the values before it.  A thread looks up U
-// packs, 256 apart, so that a wavefront writes 1 KB of neighbouring packs and
-// has its U indices, then its U table packs, in flight together.  Pack k of a
+// earlier and repeats some of the values before it.  A thread looks up one
+// pack, so that a wavefront writes 1 KB of neighbouring packs.  Pack k of a
 // block is in row (rem + k) / per_row from the block's first row: a product
 // with `magic` (floor(2^32 / per_row) + 1, exact for k per_row < 2^32) where
 // 1 < per_row < 1024, else a compare (a block then meets at most two rows).
 struct FwdShape {
-    int64_t n, packs;      // rows of out; packs in all
+    int64_t n;             // rows of out
     uint32_t rows, cols;
     uint32_t per_row, magic;
     int64_t tstride, ostride;
     float scale;
 };
 
-template <typename T, typename O, typename I, int VEC, int U>
+template <typename T, typename O, typename I, int VEC>
 __global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, const I* __restrict__ idx,
                                                    O* __restrict__ out, FwdShape sh)
 {
-    const int64_t base = (int64_t)blockIdx.x * (256 * U);
+    const int64_t base = (int64_t)blockIdx.x * 256;
     const int64_t row0 = base / sh.per_row;
-    const uint32_t rem = (uint32_t)(base - row0 * sh.per_row);
-    int64_t row[U];
-    uint32_t col[U], src[U];
-    gst::Pack<T, VEC> x[U];
+    const uint32_t k = (uint32_t)(base - row0 * sh.per_row) + threadIdx.x;
+    const uint32_t r = sh.per_row == 1     ? k
+                       : sh.per_row < 1024 ? __umulhi(k, sh.magic)
+                                           : (k >= sh.per_row ? 1u : 0u);
+    const int64_t row = row0 + r;
+    if (row >= sh.n) return;
+    const uint32_t col = min((k - r * sh.per_row) * VEC, sh.cols - VEC);
+    const uint32_t src = row_of(idx, row, sh.rows, -1);
+    gst::Pack<O, VEC> y;
+    if (src < sh.rows) {
+        const auto x = gst::load<T, VEC>(table + (int64_t)src * sh.tstride + col);
 #pragma unroll
-    for (int q = 0; q < U; ++q) {
-        const uint32_t k = rem + threadIdx.x + 256 * q;
-        const uint32_t r = sh.per_row == 1     ? k
-                           : sh.per_row < 1024 ? __umulhi(k, sh.magic)
-                                               : (k >= sh.per_row ? 1u : 0u);
-        row[q] = row0 + r;
-        col[q] = min((k - r * sh.per_row) * VEC, sh.cols - VEC);
-        src[q] = row[q] < sh.n ? row_of(idx, row[q], sh.rows, -1) : sh.rows;
+        for (int e = 0; e < VEC; ++e) y.v[e] = narrow<O>(sh.scale * (float)x.v[e]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e) y.v[e] = (O)0.0f;
     }
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-        if (src[q] < sh.rows) x[q] = gst::load<T, VEC>(table + (int64_t)src[q] * sh.tstride + col[q]);
-        else {
-#pragma unroll
-            for (int e = 0; e < VEC; ++e) x[q].v[e] = (T)0.0f;
-        }
-    }
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-        if (row[q] >= sh.n) continue;
-        gst::Pack<O, VEC> y;
-#pragma unroll
-        for (int e = 0; e < VEC; ++e) y.v[e] = src[q] < sh.rows ? narrow<O>(sh.scale * (float)x[q].v[e]) : (O)0.0f;
-        gst::store<O, VEC>(out + row[q] * sh.ostride + col[q], y);
-    }
+    gst::store_once<O, VEC>(out + row * sh.ostride + col, y);
 }
 
 // ---------------------------------------------------------------------------
@@ -422,32 +409,25 @@ gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx,
     sh.cols = (uint32_t)cols;
     sh.per_row = (uint32_t)ceil_div(cols, vec);
     sh.magic = sh.per_row > 1 ? (uint32_t)((1ull << 32) / sh.per_row) + 1u : 0u;
-    sh.packs = n * sh.per_row;
+    const int64_t packs = n * sh.per_row, blocks = ceil_div(packs, 256);
     sh.tstride = table->stride;
     sh.ostride = out->stride;
     sh.scale = scale;
-    // one pack per thread until every compute unit has eight blocks
-    const bool one = sh.packs <= (int64_t)ctx->num_cu * 8 * 256;
-    const int64_t blocks = ceil_div(sh.packs, one ? 256 : 1024);
     if (blocks > 0x7FFFFFFF) return gs_fail(ctx, GS_ERR_OVERFLOW, "lookup of %lld x %lld values", (long long)n,
                                             (long long)cols);
     GsTimerScope ts(ctx, "embed_fwd");
-    auto go = [&](auto t, auto o, auto i, auto v, auto u) {
+    auto go = [&](auto t, auto o, auto i, auto v) {
         using T = decltype(t);
         using O = decltype(o);
         using I = decltype(i);
-        hipLaunchKernelGGL((k_embed_fwd<T, O, I, decltype(v)::value, decltype(u)::value>), dim3((unsigned)blocks),
+        hipLaunchKernelGGL((k_embed_fwd<T, O, I, decltype(v)::value>), dim3((unsigned)blocks),
                            dim3(256), 0, ctx->stream, (const T*)table->data, (const I*)idx, (O*)out->data, sh);
     };
     with_type(table->type, [&](auto t) {
         with_type(out->type, [&](auto o) {
             auto sized = [&](auto v) {
-                auto unrolled = [&](auto u) {
-                    if (idx_type == GS_I32) go(t, o, int32_t{}, v, u);
-                    else go(t, o, int64_t{}, v, u);
-                };
-                if (one) unrolled(std::integral_constant<int, 1>{});
-                else unrolled(std::integral_constant<int, 4>{});
+                if (idx_type == GS_I32) go(t, o, int32_t{}, v);
+                else go(t, o, int64_t{}, v);
             };
             if (vec == 1) sized(std::integral_constant<int, 1>{});
             else if (vec == 2) sized(std::integral_constant<int, 2>{});

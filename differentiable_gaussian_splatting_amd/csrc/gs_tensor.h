@@ -34,6 +34,17 @@ __device__ __forceinline__ void store(T* p, const Pack<T, N>& r)
     __builtin_memcpy(p, &r, sizeof(r));
 }
 
+// store of values that are not read again soon
+template <typename T, int N>
+__device__ __forceinline__ void store_once(T* p, const Pack<T, N>& r)
+{
+    typedef uint32_t v4 __attribute__((ext_vector_type(4), aligned(2)));
+    typedef uint32_t v2 __attribute__((ext_vector_type(2), aligned(2)));
+    if constexpr (sizeof(r) == 16) __builtin_nontemporal_store(__builtin_bit_cast(v4, r), reinterpret_cast<v4*>(p));
+    else if constexpr (sizeof(r) == 8) __builtin_nontemporal_store(__builtin_bit_cast(v2, r), reinterpret_cast<v2*>(p));
+    else store(p, r);
+}
+
 // x rounded to T (to nearest, ties to even).  For f16 the compiler would fuse a
 // product before the conversion into a multiply-add with +0, which turns -0
 // into +0; the empty statement keeps the two apart.
