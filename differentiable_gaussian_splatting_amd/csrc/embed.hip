@@ -69,103 +69,9 @@ __global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, 
 }
 
 // ---------------------------------------------------------------------------
-// The backward: (1) the positions sorted by (row, position); (2) sums over
-// chunks of sorted positions; (3) the runs that cross blocks joined.
-//
-// (1) and, beside it in the same launch, the zero rows: blocks past `sorters`
-// write zeros over all of dtable (not when accumulating), and (2) and (3)
-// overwrite the rows that have positions.
-
-struct ZeroJob {
-    char* p;            // null: nothing to clear
-    int64_t rows;       // rows of `bytes` bytes, `stride` bytes apart
-    int64_t bytes, stride;
-};
-
-__device__ __forceinline__ void clear_rows(const ZeroJob& z, int64_t blk, int64_t nblk)
-{
-    const gst::Pack<uint16_t, 8> zero{};
-    const int64_t step = nblk * blockDim.x * 16, lane0 = (blk * blockDim.x + threadIdx.x) * 16;
-    if (z.rows == 1) {
-        for (int64_t b = lane0; b < z.bytes; b += step) {
-            if (b + 16 <= z.bytes) gst::store(reinterpret_cast<uint16_t*>(z.p + b), zero);
-            else
-                for (int64_t q = b; q < z.bytes; q += 2) *reinterpret_cast<uint16_t*>(z.p + q) = 0;
-        }
-        return;
-    }
-    for (int64_t r = blk; r < z.rows; r += nblk) {
-        char* row = z.p + r * z.stride;
-        for (int64_t q = 2 * (int64_t)threadIdx.x; q < z.bytes; q += 2 * blockDim.x)
-            *reinterpret_cast<uint16_t*>(row + q) = 0;
-    }
-}
-
-template <typename I>
-__global__ __launch_bounds__(256) void k_embed_keys(const I* __restrict__ idx, int64_t n, uint32_t rows, int64_t skip,
-                                                    uint32_t* __restrict__ keys, uint32_t* __restrict__ pos,
-                                                    uint32_t sorters, ZeroJob zero)
-{
-    if (blockIdx.x >= sorters) {
-        clear_rows(zero, blockIdx.x - sorters, gridDim.x - sorters);
-        return;
-    }
-    const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-    if (i >= n) return;
-    keys[i] = row_of(idx, i, rows, skip);
-    pos[i] = (uint32_t)i;
-}
-
-// Sort of few positions by counting: position i goes to the place
-//   #{j : key_j < key_i} + #{j < i : key_j = key_i} = #{j < i : key_j < key_i + 1} + #{j > i : key_j < key_i},
-// one compare and one add per pair.  A block ranks 64 positions (one per
-// lane), its 16 wavefronts each count a sixteenth of the keys, which are
-// staged in LDS and read four at a time by all lanes from one address.
-constexpr int kRankThreads = 1024;
-constexpr int64_t kRankMax = 12288;   // positions up to which it is used
-template <typename I>
-__global__ __launch_bounds__(kRankThreads) void k_embed_rank(const I* __restrict__ idx, int n, uint32_t rows,
-                                                             int64_t skip, uint32_t* __restrict__ keys,
-                                                             uint32_t* __restrict__ pos, uint32_t sorters,
-                                                             ZeroJob zero)
-{
-    extern __shared__ uint4 sk4[];
-    __shared__ uint32_t cnt[kRankThreads / 64][64];
-    if (blockIdx.x >= sorters) {
-        clear_rows(zero, blockIdx.x - sorters, gridDim.x - sorters);
-        return;
-    }
-    uint32_t* sk = reinterpret_cast<uint32_t*>(sk4);
-    const int n4 = (n + 3) / 4;
-    for (int j = threadIdx.x; j < 4 * n4; j += kRankThreads) sk[j] = j < n ? row_of(idx, j, rows, skip) : 0xFFFFFFFFu;
-    __syncthreads();
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int i0 = blockIdx.x * 64, i = i0 + lane;
-    const uint32_t ki = i < n ? sk[i] : 0u;
-    const int per = (n4 + kRankThreads / 64 - 1) / (kRankThreads / 64);
-    const int q0 = wave * per, q1 = min(n4, q0 + per);
-    const int b0 = i0 / 4, b1 = b0 + 16;   // the block's own positions, in fours
-    uint32_t c = 0;
-    auto count = [&](int qa, int qb, uint32_t thr) {
-#pragma unroll 4
-        for (int q = qa; q < qb; ++q) {
-            const uint4 k = sk4[q];
-            c += (k.x < thr ? 1u : 0u) + (k.y < thr ? 1u : 0u) + (k.z < thr ? 1u : 0u) + (k.w < thr ? 1u : 0u);
-        }
-    };
-    count(q0, min(q1, b0), ki + 1u);
-    for (int q = max(q0, b0); q < min(q1, b1); ++q)
-        for (int e = 0; e < 4; ++e) c += sk[4 * q + e] < ki + (4 * q + e < i ? 1u : 0u) ? 1u : 0u;
-    count(max(q0, b1), q1, ki);
-    cnt[wave][lane] = c;
-    __syncthreads();
-    if (wave == 0 && i < n) {
-        uint32_t r = 0;
-        for (int w = 0; w < kRankThreads / 64; ++w) r += cnt[w][lane];
-        keys[r] = ki;
-        pos[r] = (uint32_t)i;
-    }
-}
+// The backward: (1) the positions sorted by (row, position), group.hip; (2)
+// sums over chunks of sorted positions, and zeros in the rows without a
+// position; (3) the runs that cross blocks joined.
 
 // How (2) and (3) split the sorted positions and the columns.  A team of
 // `1 << lg` lanes, each holding VEC neighbouring columns (16 bytes), adds up
@@ -179,6 +85,9 @@ struct SumShape {
     int lg;
     int chunk;              // a multiple of 8
     int64_t per_block;      // chunk * teams
+    uint32_t blocks;        // blocks of positions
+    uint32_t slabs;         // column ranges of (1 << lg) VEC columns
+    int zero_rows;          // table rows that a wavefront clears where they have no position
     float* head;            // [blocks][cols] sum of the run that reaches a block from before
     float* tail;            // [blocks][cols] sum of the run that starts in a block and goes on after it
 };
@@ -235,95 +144,148 @@ __device__ __forceinline__ void put_part(float* row, uint32_t c0, uint32_t cb, c
     }
 }
 
-// (2) Each team walks its chunk in fours of positions, eight rows in flight,
+// Rows [v0, v0 + zero_rows) of dtable, cleared by one wavefront where no
+// position names them: each lane looks one of the rows up in the sorted keys.
+__device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, int64_t v0)
+{
+    const int lane = threadIdx.x & 63;
+    const int64_t v = v0 + lane;
+    bool unused = lane < sh.zero_rows && v < (int64_t)sh.rows;
+    if (unused) {
+        int64_t lo = 0, hi = sh.n;
+        while (lo < hi) {
+            const int64_t mid = (lo + hi) >> 1;
+            if (sh.keys[mid] < (uint32_t)v) lo = mid + 1;
+            else hi = mid;
+        }
+        unused = lo == sh.n || sh.keys[lo] != (uint32_t)v;
+    }
+    uint64_t left = gsd::ballot(unused);
+    const gst::Pack<uint16_t, 8> zero{};
+    const int esize = d.type == GS_F32 ? 4 : 2;
+    const int64_t bytes = (int64_t)sh.cols * esize;
+    // teams of 1 << zlg lanes, 16 bytes a lane, take the rows in turn
+    int zlg = 0;
+    while (zlg < 6 && (16ll << zlg) < bytes) ++zlg;
+    const int zteam = lane >> zlg, zlane = lane & ((1 << zlg) - 1), zteams = 64 >> zlg;
+    for (int r = zteam; r < sh.zero_rows; r += zteams) {
+        if (!((left >> r) & 1ull)) continue;
+        char* row = (char*)d.p + (v0 + r) * d.stride * esize;
+        for (int64_t q = 16 * zlane; q < bytes; q += 16 << zlg) {
+            if (q + 16 <= bytes) gst::store_once(reinterpret_cast<uint16_t*>(row + q), zero);
+            else
+                for (int64_t e = q; e < bytes; e += 2) *reinterpret_cast<uint16_t*>(row + e) = 0;
+        }
+    }
+}
+
+// (2) Each team walks its chunk in batches of positions, eight rows in flight,
 // and adds rows while the table row stays the same.  A run inside the chunk is
 // written at once.  The chunk's first run, if it began before, and its last,
 // if it goes on, are left in LDS; after the block's teams are done, the team
 // in which a run begins adds the pieces of the teams after it, in order, and
 // writes the row, or the block's piece of it (head / tail) if the run leaves
-// the block.
+// the block.  Blocks after those of the positions clear the unused rows, in
+// the same launch so that their stores run beside the loads.
 constexpr int kBatch = 8;
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride, SumShape sh, Dest d)
 {
     __shared__ float head[256 * VEC], tail[256 * VEC];
     __shared__ uint32_t flags[256];   // per team: 1 head, 2 tail, 4 one run from before to after the chunk
-    __shared__ uint32_t hrow[256], trow[256];
+    const uint32_t sums = sh.blocks * sh.slabs;
+    if (blockIdx.x >= sums) {
+        clear_unused(sh, d, ((int64_t)(blockIdx.x - sums) * 4 + (threadIdx.x >> 6)) * sh.zero_rows);
+        return;
+    }
+    const uint32_t blk = blockIdx.x / sh.slabs, slab = blockIdx.x - blk * sh.slabs;
     const int lanes = 1 << sh.lg, teams = 256 >> sh.lg;
     const int team = threadIdx.x >> sh.lg, lane = threadIdx.x & (lanes - 1);
-    const uint32_t c0 = ((uint32_t)blockIdx.y * lanes + lane) * VEC;
+    const uint32_t c0 = (slab * lanes + lane) * VEC;
     const bool on = c0 < sh.cols;                                  // this lane has columns
     const uint32_t cb = min(c0, sh.cols - VEC);                    // where it loads them (cols >= VEC)
-    const int64_t s = (int64_t)blockIdx.x * sh.per_block + (int64_t)team * sh.chunk;
+    const int64_t s = (int64_t)blk * sh.per_block + (int64_t)team * sh.chunk;
     const int64_t e = min(sh.n, s + sh.chunk);
     float acc[VEC];
-    uint32_t fl = 0;
+    uint32_t fl = 0, cur = sh.rows;
     if (s < e) {
-        uint32_t cur = sh.keys[s];
-        const uint32_t first = cur;
-        const bool from = s > 0 && sh.keys[s - 1] == cur && cur < sh.rows;
+        // the lists are padded to whole batches
+        auto k = gst::load<uint32_t, kBatch>(sh.keys + s);
+        auto p = gst::load<uint32_t, kBatch>(sh.pos + s);
+        const uint32_t before = s > 0 ? sh.keys[s - 1] : sh.rows, after = e < sh.n ? sh.keys[e] : sh.rows;
+        cur = k.v[0];
+        const bool from = before == cur;
         bool in_first = true;
 #pragma unroll
         for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
         const T* col = dout + cb;
-        for (int64_t j = s; j < e; j += kBatch) {
-            const auto k = gst::load<uint32_t, kBatch>(sh.keys + j);   // arrays padded to whole batches
-            const auto p = gst::load<uint32_t, kBatch>(sh.pos + j);
+        for (int64_t j = s; j < e && cur < sh.rows; j += kBatch) {
+            // a place past the chunk or without a row reads row 0, and its
+            // value is left out below: loads without branches, so that all
+            // eight are in flight
             gst::Pack<T, VEC> x[kBatch];
-#pragma unroll
-            for (int b = 0; b < kBatch; ++b)
-                if (on && j + b < e && k.v[b] < sh.rows) x[b] = gst::load<T, VEC>(col + (int64_t)p.v[b] * dstride);
+            uint32_t kk[kBatch];
 #pragma unroll
             for (int b = 0; b < kBatch; ++b) {
-                if (j + b >= e || k.v[b] >= sh.rows) continue;
-                if (k.v[b] != cur) {
-                    // the run of `cur` ends here
-                    if (in_first && from) {
-                        fl |= 1;
-                        if (on) {
+                kk[b] = j + b < e ? k.v[b] : sh.rows;
+                const uint32_t r = kk[b] < sh.rows ? p.v[b] : 0u;
+                x[b] = gst::load<T, VEC>(col + (int64_t)r * dstride);
+            }
+            const int64_t jn = min(j + kBatch, (e - 1) / kBatch * kBatch);   // the last batch again at the end
+            k = gst::load<uint32_t, kBatch>(sh.keys + jn);
+            p = gst::load<uint32_t, kBatch>(sh.pos + jn);
+            if (kk[kBatch - 1] == cur) {   // keys ascend: all of the batch
 #pragma unroll
-                            for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
-                        }
-                    } else if (on) {
-                        put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
-                    }
-                    in_first = false;
-                    cur = k.v[b];
+                for (int b = 0; b < kBatch; ++b) {
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
+                    for (int q = 0; q < VEC; ++q) acc[q] += (float)x[b].v[q];
                 }
+                continue;
+            }
+            // one run of the batch after the other
+            for (;;) {
+                uint32_t next = sh.rows;
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) acc[q] += (float)x[b].v[q];
+                for (int b = 0; b < kBatch; ++b) {
+                    const bool take = kk[b] == cur;
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] += take ? (float)x[b].v[q] : 0.0f;
+                    next = min(next, kk[b] > cur ? kk[b] : sh.rows);
+                }
+                if (next == sh.rows) break;
+                if (in_first && from) {
+                    fl |= 1;
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+                } else if (on) {
+                    put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+                }
+                in_first = false;
+                cur = next;
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
             }
         }
         if (cur < sh.rows) {
-            const bool on_after = e < sh.n && sh.keys[e] == cur;
             if (in_first && from) {
-                fl |= on_after ? 5 : 1;
-                if (on) {
+                fl |= after == cur ? 5 : 1;
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
-                }
-            } else if (on_after) {
+                for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+            } else if (after == cur) {
                 fl |= 2;
-                if (on) {
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) tail[threadIdx.x * VEC + q] = acc[q];
-                }
+                for (int q = 0; q < VEC; ++q) tail[threadIdx.x * VEC + q] = acc[q];
             } else if (on) {
                 put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
             }
-        }
-        if (lane == 0) {
-            hrow[team] = first;
-            trow[team] = cur;
         }
     }
     if (lane == 0) flags[team] = fl;
     __syncthreads();
     if (!on) return;
-    // runs that begin in this team and go on, and (team 0) the block's first run if it began before
-    auto follow = [&](const float* piece, bool goes_on, bool from_before, uint32_t row) {
+    // the run that begins in this team and goes on, and (team 0) the block's
+    // first run if it began before
+    auto follow = [&](const float* piece, bool goes_on, bool from_before) {
 #pragma unroll
         for (int q = 0; q < VEC; ++q) acc[q] = piece[threadIdx.x * VEC + q];
         int t = team;
@@ -332,12 +294,12 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
             for (int q = 0; q < VEC; ++q) acc[q] += head[((t << sh.lg) + lane) * VEC + q];
             goes_on = (flags[t] & 4) != 0;
         }
-        if (from_before) put_part<VEC>(sh.head + (int64_t)blockIdx.x * sh.cols, c0, cb, acc);
-        else if (goes_on) put_part<VEC>(sh.tail + (int64_t)blockIdx.x * sh.cols, c0, cb, acc);
-        else put_row<VEC>(d, row, c0, cb, sh.cols, acc);
+        if (from_before) put_part<VEC>(sh.head + (int64_t)blk * sh.cols, c0, cb, acc);
+        else if (goes_on) put_part<VEC>(sh.tail + (int64_t)blk * sh.cols, c0, cb, acc);
+        else put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
     };
-    if (team == 0 && (fl & 1)) follow(head, (fl & 4) != 0, true, hrow[0]);
-    if (fl & 2) follow(tail, true, false, trow[team]);
+    if (team == 0 && (fl & 1)) follow(head, (fl & 4) != 0, true);
+    if (fl & 2) follow(tail, true, false);
 }
 
 // (3) One block per border between blocks of (2): if a run begins in the block
@@ -444,11 +406,6 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
 {
     const int64_t rows = dtable->rows, cols = dtable->cols;
     if (rows == 0 || cols == 0 || (n == 0 && accumulate)) return GS_OK;
-    const int64_t esize = dtable->type == GS_F32 ? 4 : 2;
-    const bool dense = rows == 1 || dtable->stride == cols;
-    const ZeroJob zero = accumulate ? ZeroJob{} : ZeroJob{(char*)dtable->data, dense ? 1 : rows,
-                                                          (dense ? rows : 1) * cols * esize, dtable->stride * esize};
-
     // the split: columns per lane (16 bytes of dout, or fewer in narrow
     // rows), lanes per team, positions per team
     const int most = dout->type == GS_F32 ? 4 : 8;
@@ -467,67 +424,34 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     sh.chunk = (int)std::min<int64_t>(256, std::max<int64_t>(kBatch, want / kBatch * kBatch));
     sh.per_block = (int64_t)sh.chunk * (256 >> lg);
     const int64_t blocks = ceil_div(n, sh.per_block);
-    if (slabs > 65535) return gs_fail(ctx, GS_ERR_OVERFLOW, "rows of %lld values", (long long)cols);
+    // a wavefront clears about 64 KB
+    const int64_t row_bytes = cols * (dtable->type == GS_F32 ? 4 : 2);
+    sh.zero_rows = (int)std::min<int64_t>(64, std::max<int64_t>(1, 65536 / row_bytes));
+    const int64_t clear = accumulate ? 0 : ceil_div(rows, 4 * (int64_t)sh.zero_rows);
+    if (blocks * slabs + clear > 0x7FFFFFFF || slabs > 65535)
+        return gs_fail(ctx, GS_ERR_OVERFLOW, "table gradient of %lld rows of %lld values", (long long)rows,
+                       (long long)cols);
+    sh.blocks = (uint32_t)blocks;
+    sh.slabs = (uint32_t)slabs;
 
-    const int64_t m = ceil_div(std::max<int64_t>(n, 1), kBatch) * kBatch;
-    const bool rank = n <= kRankMax;
-    uint32_t* k0 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-    uint32_t* v0 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-    uint32_t *k1 = nullptr, *v1 = nullptr, *scratch = nullptr;
-    bool ok = k0 && v0;
-    if (!rank) {
-        k1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-        v1 = (uint32_t*)gs_malloc(ctx, 4 * m, GS_MEM_SCRATCH, tmp);
-        scratch = (uint32_t*)gs_malloc(ctx, 4 * radix_scratch_words(m), GS_MEM_SCRATCH, tmp);
-        ok = ok && k1 && v1 && scratch;
-    }
+    GsGroups groups;
+    gs_status st = launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, true);
+    if (st != GS_OK) return st;
     if (blocks > 1) {
         sh.head = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
         sh.tail = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
-        ok = ok && sh.head && sh.tail;
+        if (!sh.head || !sh.tail) return GS_ERR_OOM;
     }
-    if (!ok) return GS_ERR_OOM;
-
-    {
-        GsTimerScope ts(ctx, "embed_sort");
-        const int threads = rank ? kRankThreads : 256;
-        const uint32_t sorters = (uint32_t)ceil_div(n, rank ? 64 : 256);
-        const int64_t clear = zero.p ? std::min<int64_t>(ceil_div(zero.rows * zero.bytes, 16 * threads), 8 * ctx->num_cu)
-                                     : 0;
-        const dim3 grid(sorters + (uint32_t)clear);
-        const size_t lds = rank ? 16 * (size_t)ceil_div(n, 4) : 0;
-        auto go = [&](auto i) {
-            using I = decltype(i);
-            if (rank)
-                hipLaunchKernelGGL((k_embed_rank<I>), grid, dim3(threads), lds, ctx->stream, (const I*)idx, (int)n,
-                                   (uint32_t)rows, padding, k0, v0, sorters, zero);
-            else
-                hipLaunchKernelGGL((k_embed_keys<I>), grid, dim3(threads), 0, ctx->stream, (const I*)idx, n,
-                                   (uint32_t)rows, padding, k0, v0, sorters, zero);
-        };
-        if (grid.x > 0) {
-            if (idx_type == GS_I32) go(int32_t{});
-            else go(int64_t{});
-        }
-    }
-    if (n == 0) {
-        GS_HIP(ctx, hipGetLastError());
-        return GS_OK;
-    }
-    bool second = false;
-    if (!rank) {
-        const gs_status st = launch_radix_sort(ctx, k0, v0, k1, v1, n, bits_for(rows + 1), &second, nullptr, 0,
-                                               nullptr, scratch);
-        if (st != GS_OK) return st;
-    }
-    sh.keys = second ? k1 : k0;
-    sh.pos = second ? v1 : v0;
+    st = launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, false);
+    if (st != GS_OK) return st;
+    sh.keys = groups.keys;
+    sh.pos = groups.pos;
     const Dest d{dtable->data, dtable->stride, dtable->type, accumulate, scale};
     GsTimerScope ts(ctx, "embed_sum");
     auto sum = [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int VEC = decltype(v)::value;
-        hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3((unsigned)blocks, (unsigned)slabs), dim3(256), 0, ctx->stream,
+        hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3((unsigned)(blocks * slabs + clear)), dim3(256), 0, ctx->stream,
                            (const T*)dout->data, dout->stride, sh, d);
         if (blocks > 1)
             hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)(blocks - 1), (unsigned)slabs), dim3(256), 0,

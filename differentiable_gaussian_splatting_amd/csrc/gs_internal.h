@@ -353,6 +353,17 @@ gs_status launch_bwd_adam(gs_ctx* ctx, const gs_camera* cam, const gs_params* p,
                           const float* grad2d, const gs_param_ptrs* pr, const gs_param_ptrs* m, const gs_param_ptrs* v,
                           int32_t step, float lr, float b1, float b2, float eps);
 
+// group.hip: the positions [0, n) of an index list sorted by (row, position);
+// positions whose index is outside [0, rows) or equal to skip come last, with
+// the key `rows`.  Called twice: with allocate, to take the lists from tmp
+// (GS_ERR_OOM), then to sort; keys and pos then hold the result, padded to a
+// multiple of 8 entries.
+struct GsGroups {
+    uint32_t *keys = nullptr, *pos = nullptr;
+    uint32_t *keys2 = nullptr, *pos2 = nullptr, *hist = nullptr;   // work space of the passes
+};
+gs_status launch_group(gs_ctx* ctx, const void* idx, int idx_type, int64_t n, int64_t rows, int64_t skip,
+                       std::vector<GsAlloc>* tmp, GsGroups* out, bool allocate);
 // embed.hip: rows of a table by index, and the table's gradient (workspaces
 // go to tmp; the caller releases it)
 gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx, int idx_type, int64_t n, float scale,

@@ -438,7 +438,7 @@ gs_status gs_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx, int
  * dtable[v, c] when accumulate != 0.  Sums in f32, in an order that depends on
  * idx alone (ascending i in fixed pieces), rounded once to dtable's type.
  * Indices outside [0, dtable->rows) and those equal to padding (any value
- * outside that range: none) add nothing, and their rows of dout are not read.
+ * outside that range: none) add nothing, whatever their rows of dout hold.
  * Rows without an index become zero, or stay as they are when accumulating.
  * dout: n x dtable->cols.  Errors: as gs_embed_fwd, and OOM. */
 gs_status gs_embed_bwd(gs_ctx* ctx, const void* idx, int32_t idx_type, int64_t n, const gs_tensor* dout, float scale,
