@@ -181,18 +181,18 @@ __device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, 
 
 // (2) Each team walks its chunk in batches of positions, eight rows in flight,
 // and adds rows while the table row stays the same.  A run inside the chunk is
-// written at once.  The chunk's first run, if it began before, and its last,
-// if it goes on, are left in LDS; after the block's teams are done, the team
-// in which a run begins adds the pieces of the teams after it, in order, and
-// writes the row, or the block's piece of it (head / tail) if the run leaves
-// the block.  Blocks after those of the positions clear the unused rows, in
+// written at once.  A chunk's first run, if it began before, is its head, and
+// its last, if it goes on, its tail.  After the block's teams are done, the
+// heads that belong to one run are added over the teams by doubling steps, and
+// the team in which the run begins adds its tail and writes the row, or the
+// block's piece of it (head / tail) if the run leaves the block.  Blocks after those of the positions clear the unused rows, in
 // the same launch so that their stores run beside the loads.
 constexpr int kBatch = 8;
 template <typename T, int VEC>
 __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride, SumShape sh, Dest d)
 {
-    __shared__ float head[256 * VEC], tail[256 * VEC];
-    __shared__ uint32_t flags[256];   // per team: 1 head, 2 tail, 4 one run from before to after the chunk
+    __shared__ float heads[256 * VEC];
+    __shared__ uint8_t on_from[256];   // per team: its head's run goes on behind what is added so far
     const uint32_t sums = sh.blocks * sh.slabs;
     if (blockIdx.x >= sums) {
         clear_unused(sh, d, ((int64_t)(blockIdx.x - sums) * 4 + (threadIdx.x >> 6)) * sh.zero_rows);
@@ -206,8 +206,11 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
     const uint32_t cb = min(c0, sh.cols - VEC);                    // where it loads them (cols >= VEC)
     const int64_t s = (int64_t)blk * sh.per_block + (int64_t)team * sh.chunk;
     const int64_t e = min(sh.n, s + sh.chunk);
-    float acc[VEC];
-    uint32_t fl = 0, cur = sh.rows;
+    float acc[VEC], head[VEC];
+    bool has_head = false, has_tail = false, through = false;   // through: the head is all of the chunk, and goes on
+    uint32_t cur = sh.rows;
+#pragma unroll
+    for (int q = 0; q < VEC; ++q) head[q] = 0.0f;
     if (s < e) {
         // the lists are padded to whole batches
         auto k = gst::load<uint32_t, kBatch>(sh.keys + s);
@@ -254,9 +257,9 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
                 }
                 if (next == sh.rows) break;
                 if (in_first && from) {
-                    fl |= 1;
+                    has_head = true;
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+                    for (int q = 0; q < VEC; ++q) head[q] = acc[q];
                 } else if (on) {
                     put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
                 }
@@ -268,38 +271,51 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
         }
         if (cur < sh.rows) {
             if (in_first && from) {
-                fl |= after == cur ? 5 : 1;
+                has_head = true;
+                through = after == cur;
 #pragma unroll
-                for (int q = 0; q < VEC; ++q) head[threadIdx.x * VEC + q] = acc[q];
+                for (int q = 0; q < VEC; ++q) head[q] = acc[q];
             } else if (after == cur) {
-                fl |= 2;
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) tail[threadIdx.x * VEC + q] = acc[q];
+                has_tail = true;
             } else if (on) {
                 put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
             }
         }
     }
-    if (lane == 0) flags[team] = fl;
-    __syncthreads();
-    if (!on) return;
-    // the run that begins in this team and goes on, and (team 0) the block's
-    // first run if it began before
-    auto follow = [&](const float* piece, bool goes_on, bool from_before) {
+    // heads of one run, added over the teams t .. t + 2 step - 1 while it goes on
+    bool goes = through;
+    auto publish = [&]() {
 #pragma unroll
-        for (int q = 0; q < VEC; ++q) acc[q] = piece[threadIdx.x * VEC + q];
-        int t = team;
-        while (goes_on && ++t < teams) {
-#pragma unroll
-            for (int q = 0; q < VEC; ++q) acc[q] += head[((t << sh.lg) + lane) * VEC + q];
-            goes_on = (flags[t] & 4) != 0;
-        }
-        if (from_before) put_part<VEC>(sh.head + (int64_t)blk * sh.cols, c0, cb, acc);
-        else if (goes_on) put_part<VEC>(sh.tail + (int64_t)blk * sh.cols, c0, cb, acc);
-        else put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+        for (int q = 0; q < VEC; ++q) heads[threadIdx.x * VEC + q] = head[q];
+        if (lane == 0) on_from[team] = goes;
+        __syncthreads();
     };
-    if (team == 0 && (fl & 1)) follow(head, (fl & 4) != 0, true);
-    if (fl & 2) follow(tail, true, false);
+    if (__syncthreads_or(through)) {
+        for (int step = 1; step < teams; step <<= 1) {
+            publish();
+            if (goes && team + step < teams) {
+                const float* h = heads + (threadIdx.x + (step << sh.lg)) * VEC;
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) head[q] += h[q];
+                goes = on_from[team + step];
+            }
+            __syncthreads();
+        }
+    }
+    publish();
+    if (!on) return;
+    if (team == 0 && has_head) put_part<VEC>(sh.head + (int64_t)blk * sh.cols, c0, cb, head);
+    if (has_tail) {
+        bool leaves = true;
+        if (team + 1 < teams) {
+            const float* h = heads + (threadIdx.x + (1 << sh.lg)) * VEC;
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] += h[q];
+            leaves = on_from[team + 1];
+        }
+        if (leaves) put_part<VEC>(sh.tail + (int64_t)blk * sh.cols, c0, cb, acc);
+        else put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+    }
 }
 
 // (3) One block per border between blocks of (2): if a run begins in the block

@@ -59,8 +59,11 @@ __global__ __launch_bounds__(kRankThreads) void k_group_rank(const I* __restrict
     const int q0 = min(m4, wave * per), q1 = min(m4, q0 + per);
     const int b0 = i0 / 4, b1 = b0 + 16;   // the block's own
     count(q0, min(q1, b0), ki + 1u);
-    for (int q = max(q0, b0); q < min(q1, b1); ++q)
-        for (int e = 0; e < 4; ++e) c += sk[4 * q + e] < ki + (4 * q + e < i ? 1u : 0u) ? 1u : 0u;
+    for (int q = max(q0, b0); q < min(q1, b1); ++q) {
+        const uint4 k = sk4[q];
+        c += (k.x < ki + (4 * q < i ? 1u : 0u) ? 1u : 0u) + (k.y < ki + (4 * q + 1 < i ? 1u : 0u) ? 1u : 0u) +
+             (k.z < ki + (4 * q + 2 < i ? 1u : 0u) ? 1u : 0u) + (k.w < ki + (4 * q + 3 < i ? 1u : 0u) ? 1u : 0u);
+    }
     count(max(q0, b1), q1, ki);
     cnt[wave][lane] = c;
     __syncthreads();
@@ -94,11 +97,20 @@ __global__ __launch_bounds__(64 * kMergeWaves) void k_group_merge(const uint32_t
         const uint32_t thr = ki + (t < own ? 1u : 0u);   // count the keys < thr
         const uint32_t* k = kin + t * kRankTile;
         const int m = min(kRankTile, n - t * kRankTile);
-        int lo = 0;
-        for (int step = kRankTile; step > 0; step >>= 1) {
-            const int at = lo + step;
-            if (at <= m && k[min(at, m) - 1] < thr) lo = at;
-        }
+        // lane l holds the last key of the tile's l-th part: a bisection over
+        // the lanes finds the part, one in memory the place in it
+        constexpr int kPart = kRankTile / 64;
+        const uint32_t last = lane * kPart + kPart <= m ? k[lane * kPart + kPart - 1] : 0xFFFFFFFFu;
+        int part = 0;
+#pragma unroll
+        for (int step = 32; step > 0; step >>= 1)
+            if ((uint32_t)__shfl((int)last, part + step - 1, 64) < thr) part += step;
+        // part <= 63, and all keys of parts before it are < thr; if the last
+        // lane's is too, every key is
+        int lo = part * kPart;
+#pragma unroll
+        for (int step = kPart; step > 0; step >>= 1)
+            if (lo + step <= m && k[min(lo + step, m) - 1] < thr) lo += step;
         c += (uint32_t)lo;
     }
     cnt[wave][lane] = c;
