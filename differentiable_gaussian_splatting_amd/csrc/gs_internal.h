@@ -370,10 +370,11 @@ gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx,
                            const gs_tensor* out);
 gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n, const gs_tensor* dout, float scale,
                            int64_t padding, int accumulate, const gs_tensor* dtable, std::vector<GsAlloc>* tmp);
-// lists.hip: norm and clip factor of a list, out = factor * in, Adam
+// lists.hip: norm and clip factor of a list; that, and out = factor * in; Adam
 gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n, double max_norm, float* norm,
                            std::vector<GsAlloc>* tmp);
-gs_status launch_scale_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, const float* norm);
+gs_status launch_clip(gs_ctx* ctx, const gs_tensor* in, int32_t n, double max_norm, const gs_tensor* out, float* norm,
+                      std::vector<GsAlloc>* tmp);
 gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, const gs_tensor* v, const gs_tensor* g,
                            const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm);
 

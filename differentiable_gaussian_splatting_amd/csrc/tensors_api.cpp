@@ -145,8 +145,7 @@ gs_status gs_clip_grads(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, 
     }
     if (st != GS_OK) return st;
     return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
-        const gs_status r = launch_grad_norm(ctx, grads, n_tensors, max_norm, norm, tmp);
-        return r != GS_OK ? r : launch_scale_list(ctx, grads, to, n_tensors, norm);
+        return launch_clip(ctx, grads, n_tensors, max_norm, to, norm, tmp);
     });
 }
 
