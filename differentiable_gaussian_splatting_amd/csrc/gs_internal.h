@@ -376,6 +376,7 @@ gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n, doubl
 gs_status launch_clip(gs_ctx* ctx, const gs_tensor* in, int32_t n, double max_norm, const gs_tensor* out, float* norm,
                       std::vector<GsAlloc>* tmp);
 gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, const gs_tensor* v, const gs_tensor* g,
-                           const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm);
+                           const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm,
+                           std::vector<GsAlloc>* tmp);
 
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

@@ -32,13 +32,14 @@ struct Apart {
     uint32_t cols;
     uint32_t pad;
 };
-constexpr int kApart = 16;
+constexpr int kApart = 16;   // in a launch's kernel arguments
 
 // the fields of a launch's tensor that every kernel needs
 struct Common {
     int64_t n;
     uint32_t bend;      // blocks of the tensors up to and including this one
-    int8_t type, type2, apart, pad;
+    int8_t type, type2;
+    int16_t apart;
 };
 
 struct NormTensor {
@@ -57,9 +58,14 @@ struct AdamTensor {
     void* copy;
 };
 
-// kernel arguments, within 4 KB
+// The descriptors of a launch: in its kernel arguments (within 4 KB), or, for
+// large lists that would take more than three such launches, in a table on
+// the device that small launches fill from theirs (Adam over 220 tensors of
+// 11.3M values: 85 us against 99; over 250 tensors of 0.4M values the table
+// costs 4 us).
 template <typename T, int CAP>
 struct Job {
+    typedef T Tensor;
     static constexpr int kCap = CAP;
     T t[CAP];
     Apart apart[kApart];
@@ -69,6 +75,13 @@ struct Job {
 typedef Job<NormTensor, 144> NormJob;
 typedef Job<ScaleTensor, 108> ScaleJob;
 typedef Job<AdamTensor, 62> AdamJob;
+template <typename T>
+struct Table {
+    const T* t;
+    const Apart* apart;
+    int64_t piece;
+    int32_t count;
+};
 static_assert(sizeof(NormJob) <= 3968 && sizeof(ScaleJob) <= 3968 && sizeof(AdamJob) <= 3968, "kernel arguments");
 
 struct AdamConst {
@@ -78,19 +91,19 @@ struct AdamConst {
     float eps, keep;        // keep = 1 - lr weight_decay
 };
 
-// the tensor of this block and its piece [k0, k1)
+// the tensor of block b, and that block among the tensor's `blocks`
 template <typename J>
-__device__ __forceinline__ int piece_of_block(const J& job, int64_t& k0, int64_t& k1)
+__device__ __forceinline__ int tensor_of_block(const J& job, uint32_t b, uint32_t& among, uint32_t& blocks)
 {
-    const uint32_t b = blockIdx.x;
     int lo = 0, hi = job.count - 1;
     while (lo < hi) {
         const int mid = (lo + hi) >> 1;
         if (b < job.t[mid].c.bend) hi = mid;
         else lo = mid + 1;
     }
-    k0 = (int64_t)(b - (lo ? job.t[lo - 1].c.bend : 0u)) * job.piece;
-    k1 = min(job.t[lo].c.n, k0 + job.piece);
+    const uint32_t before = lo ? job.t[lo - 1].c.bend : 0u;
+    among = b - before;
+    blocks = job.t[lo].c.bend - before;
     return lo;
 }
 
@@ -106,6 +119,15 @@ __device__ __forceinline__ void each_apart(const Apart& a, int64_t k0, int64_t k
         const uint32_t r = (rem + j) / a.cols, c = (rem + j) - r * a.cols;
         f(k0 + j, (row0 + r) * a.stride + c, (row0 + r) * a.ostride + c);
     }
+}
+
+// a job's descriptors into a table
+template <typename J>
+__global__ __launch_bounds__(kThreads) void k_fill_table(J job, typename J::Tensor* __restrict__ t,
+                                                         Apart* __restrict__ apart)
+{
+    for (int k = threadIdx.x; k < job.count; k += kThreads) t[k] = job.t[k];
+    for (int k = threadIdx.x; k < job.aparts; k += kThreads) apart[k] = job.apart[k];
 }
 
 __device__ __forceinline__ double block_sum(double v)
@@ -135,13 +157,14 @@ __device__ __forceinline__ float factor_of(double norm, double max_norm)
     return (float)(c > 1.0 ? 1.0 : c);   // NaN stays
 }
 
-// Sum of squares of a piece: four packs of 16 bytes per thread in flight.
+// Sum of squares of the block's share of a tensor: every `blocks`-th run of
+// four packs per thread, so that all blocks together walk through memory from
+// front to back.
 template <typename T>
-__device__ __forceinline__ double squares(const T* __restrict__ p, int64_t n)
+__device__ __forceinline__ double squares(const T* __restrict__ p, int64_t n, uint32_t among, uint32_t blocks)
 {
-    constexpr int V = 16 / sizeof(T), U = 4;
+    constexpr int V = 16 / sizeof(T), U = 4, kRun = kThreads * V * U;
     double s = 0.0;
-    int64_t k = (int64_t)threadIdx.x * V;
     auto add = [&](const gst::Pack<T, V>& x) {
 #pragma unroll
         for (int e = 0; e < V; ++e) {
@@ -149,36 +172,42 @@ __device__ __forceinline__ double squares(const T* __restrict__ p, int64_t n)
             s = __builtin_fma(d, d, s);
         }
     };
-    for (; k + (U - 1) * kThreads * V + V <= n; k += U * kThreads * V) {
+    int64_t k = (int64_t)among * kRun;
+    for (; k + kRun <= n; k += (int64_t)blocks * kRun) {
         gst::Pack<T, V> x[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = gst::load<T, V>(p + k + u * kThreads * V);
+        for (int u = 0; u < U; ++u) x[u] = gst::load<T, V>(p + k + (u * kThreads + threadIdx.x) * V);
 #pragma unroll
         for (int u = 0; u < U; ++u) add(x[u]);
     }
-    for (; k + V <= n; k += kThreads * V) add(gst::load<T, V>(p + k));
-    const int64_t t = n / V * V + threadIdx.x;
-    if (t < n) {
-        const double d = (double)(float)p[t];
-        s = __builtin_fma(d, d, s);
+    if (k < n) {   // the tensor's last run, in one block
+        const int64_t whole = n / V * V;
+        for (int64_t q = k + (int64_t)threadIdx.x * V; q < whole; q += kThreads * V) add(gst::load<T, V>(p + q));
+        if (whole + threadIdx.x < n) {
+            const double d = (double)(float)p[whole + threadIdx.x];
+            s = __builtin_fma(d, d, s);
+        }
     }
     return s;
 }
 
-__global__ __launch_bounds__(kThreads) void k_squares(NormJob job, double* __restrict__ part)
+template <typename J>
+__global__ __launch_bounds__(kThreads) void k_squares(J job, double* __restrict__ part)
 {
-    int64_t k0, k1;
-    const NormTensor& t = job.t[piece_of_block(job, k0, k1)];
+    uint32_t among, blocks;
+    const NormTensor& t = job.t[tensor_of_block(job, blockIdx.x, among, blocks)];
     double s = 0.0;
     auto typed = [&](auto x) {
         using T = decltype(x);
         const T* p = (const T*)t.p;
-        if (t.c.apart < 0) s = squares<T>(p + k0, k1 - k0);
-        else
-            each_apart(job.apart[t.c.apart], k0, k1, [&](int64_t, int64_t at, int64_t) {
+        if (t.c.apart < 0) s = squares<T>(p, t.c.n, among, blocks);
+        else {
+            const int64_t k0 = among * job.piece;
+            each_apart(job.apart[t.c.apart], k0, min(t.c.n, k0 + job.piece), [&](int64_t, int64_t at, int64_t) {
                 const double d = (double)(float)p[at];
                 s = __builtin_fma(d, d, s);
             });
+        }
     };
     if (t.c.type == GS_F32) typed(float{});
     else if (t.c.type == GS_F16) typed(gst::f16{});
@@ -200,40 +229,40 @@ __global__ __launch_bounds__(kThreads) void k_norm(const double* __restrict__ pa
 template <typename T>
 __device__ __forceinline__ void scale(const T* p, T* o, int64_t n, float c)
 {
-    constexpr int V = 16 / sizeof(T), U = 4;
+    constexpr int V = 16 / sizeof(T);
     int64_t k = (int64_t)threadIdx.x * V;
-    auto put = [&](int64_t at, const gst::Pack<T, V>& x) {
+    for (; k + V <= n; k += kThreads * V) {
+        const auto x = gst::load<T, V>(p + k);
         gst::Pack<T, V> y;
 #pragma unroll
         for (int e = 0; e < V; ++e) y.v[e] = gst::narrow<T>(c * (float)x.v[e]);
-        gst::store<T, V>(o + at, y);
-    };
-    for (; k + (U - 1) * kThreads * V + V <= n; k += U * kThreads * V) {
-        gst::Pack<T, V> x[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) x[u] = gst::load<T, V>(p + k + u * kThreads * V);
-#pragma unroll
-        for (int u = 0; u < U; ++u) put(k + u * kThreads * V, x[u]);
+        gst::store_once<T, V>(o + k, y);
     }
-    for (; k + V <= n; k += kThreads * V) put(k, gst::load<T, V>(p + k));
     const int64_t t = n / V * V + threadIdx.x;
     if (t < n) o[t] = gst::narrow<T>(c * (float)p[t]);
 }
 
-// Every block adds the norm's partials itself, in one order (a launch less
-// than a norm of its own); the first one writes the norm.
-__global__ __launch_bounds__(kThreads) void k_scale(ScaleJob job, const double* __restrict__ part, int64_t parts,
-                                                    double max_norm, float* __restrict__ norm)
+// part: the norm's partials, which every block adds itself, in one order (one
+// launch less, for small lists); null: the factor is in norm already.
+template <typename J>
+__global__ __launch_bounds__(kThreads) void k_scale(J job, const double* __restrict__ part, int64_t parts,
+                                                    double max_norm, float* __restrict__ norm, int write)
 {
-    const double total = sqrt(total_of(part, parts));
-    const float c = factor_of(total, max_norm);
-    if (norm && blockIdx.x == 0 && threadIdx.x == 0) {
-        norm[0] = (float)total;
-        norm[1] = c;
+    float c;
+    if (part) {
+        const double total = sqrt(total_of(part, parts));
+        c = factor_of(total, max_norm);
+        if (write && blockIdx.x == 0 && threadIdx.x == 0) {
+            norm[0] = (float)total;
+            norm[1] = c;
+        }
+    } else {
+        c = norm[1];
     }
-    int64_t k0, k1;
-    const ScaleTensor& t = job.t[piece_of_block(job, k0, k1)];
+    uint32_t among, blocks;
+    const ScaleTensor& t = job.t[tensor_of_block(job, blockIdx.x, among, blocks)];
     if (c == 1.0f && t.o == t.p) return;
+    const int64_t k0 = among * job.piece, k1 = min(t.c.n, k0 + job.piece);
     auto typed = [&](auto x) {
         using T = decltype(x);
         const T* p = (const T*)t.p;
@@ -263,51 +292,35 @@ __device__ __forceinline__ void put_copy(const AdamTensor& t, int64_t k, float p
     else ((gst::bf16*)t.copy)[k] = gst::narrow<gst::bf16>(p);
 }
 
-// A piece: packs of four values, two in flight per thread (p, m, v of 16 bytes
-// each and the gradient's).
+// A piece, in packs of four values (p, m, v of 16 bytes each and the
+// gradient's).
 template <typename T>
 __device__ __forceinline__ void adam(const AdamTensor& t, int64_t k0, int64_t n, float c, const AdamConst& a)
 {
-    constexpr int V = 4, U = 2;
+    constexpr int V = 4;
     float *pp = t.p + k0, *mp = t.m + k0, *vp = t.v + k0;
     const T* gp = (const T*)t.g + k0;
-    auto go = [&](int64_t k, auto count) {
-        constexpr int N = decltype(count)::value;
-        gst::Pack<float, V> p[N], m[N], v[N];
-        gst::Pack<T, V> g[N];
+    for (int64_t k = (int64_t)threadIdx.x * V; k + V <= n; k += kThreads * V) {
+        auto p = gst::load<float, V>(pp + k), m = gst::load<float, V>(mp + k), v = gst::load<float, V>(vp + k);
+        const auto g = gst::load<T, V>(gp + k);
 #pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int64_t at = k + u * kThreads * V;
-            p[u] = gst::load<float, V>(pp + at);
-            m[u] = gst::load<float, V>(mp + at);
-            v[u] = gst::load<float, V>(vp + at);
-            g[u] = gst::load<T, V>(gp + at);
+        for (int e = 0; e < V; ++e) adam_value(c * (float)g.v[e], p.v[e], m.v[e], v.v[e], a);
+        gst::store<float, V>(pp + k, p);
+        gst::store<float, V>(mp + k, m);
+        gst::store<float, V>(vp + k, v);
+        if (t.copy) {
+            auto low = [&](auto x) {
+                using O = decltype(x);
+                gst::Pack<O, V> y;
+#pragma unroll
+                for (int e = 0; e < V; ++e) y.v[e] = gst::narrow<O>(p.v[e]);
+                gst::store<O, V>((O*)t.copy + k0 + k, y);
+            };
+            if (t.c.type2 == GS_F32) low(float{});
+            else if (t.c.type2 == GS_F16) low(gst::f16{});
+            else low(gst::bf16{});
         }
-#pragma unroll
-        for (int u = 0; u < N; ++u) {
-            const int64_t at = k + u * kThreads * V;
-#pragma unroll
-            for (int e = 0; e < V; ++e) adam_value(c * (float)g[u].v[e], p[u].v[e], m[u].v[e], v[u].v[e], a);
-            gst::store<float, V>(pp + at, p[u]);
-            gst::store<float, V>(mp + at, m[u]);
-            gst::store<float, V>(vp + at, v[u]);
-            if (t.copy) {
-                auto low = [&](auto x) {
-                    using O = decltype(x);
-                    gst::Pack<O, V> y;
-#pragma unroll
-                    for (int e = 0; e < V; ++e) y.v[e] = gst::narrow<O>(p[u].v[e]);
-                    gst::store<O, V>((O*)t.copy + k0 + at, y);
-                };
-                if (t.c.type2 == GS_F32) low(float{});
-                else if (t.c.type2 == GS_F16) low(gst::f16{});
-                else low(gst::bf16{});
-            }
-        }
-    };
-    int64_t k = (int64_t)threadIdx.x * V;
-    for (; k + (U - 1) * kThreads * V + V <= n; k += U * kThreads * V) go(k, std::integral_constant<int, U>{});
-    for (; k + V <= n; k += kThreads * V) go(k, std::integral_constant<int, 1>{});
+    }
     const int64_t r = n / V * V + threadIdx.x;
     if (r < n) {
         float p = pp[r], m = mp[r], v = vp[r];
@@ -319,15 +332,17 @@ __device__ __forceinline__ void adam(const AdamTensor& t, int64_t k0, int64_t n,
     }
 }
 
-__global__ __launch_bounds__(kThreads) void k_adam_list(AdamJob job, AdamConst a, const float* __restrict__ norm)
+template <typename J>
+__global__ __launch_bounds__(kThreads) void k_adam_list(J job, AdamConst a, const float* __restrict__ norm)
 {
     float c = 1.0f;
     if (norm) {
         if (!(fabsf(norm[0]) < __builtin_inff())) return;   // not finite
         c = norm[1];
     }
-    int64_t k0, k1;
-    const AdamTensor& t = job.t[piece_of_block(job, k0, k1)];
+    uint32_t among, blocks;
+    const AdamTensor& t = job.t[tensor_of_block(job, blockIdx.x, among, blocks)];
+    const int64_t k0 = among * job.piece, k1 = min(t.c.n, k0 + job.piece);
     auto typed = [&](auto x) {
         using T = decltype(x);
         if (t.c.apart < 0) adam<T>(t, k0, k1 - k0, c, a);
@@ -345,6 +360,11 @@ __global__ __launch_bounds__(kThreads) void k_adam_list(AdamJob job, AdamConst a
     else if (t.c.type == GS_F16) typed(gst::f16{});
     else typed(gst::bf16{});
 }
+
+// Lists of more values are scaled in pieces of kLargePiece, after a launch that
+// forms the factor; Adam takes kAdamPiece always: one or two packs per thread
+// and many blocks keep the blocks that run together close together in memory.
+constexpr int64_t kLarge = 4000000, kLargePiece = 2048, kAdamPiece = 1024;
 
 // rows x cols values that lie one after the other
 bool dense(const gs_tensor& t) { return t.rows <= 1 || t.stride == t.cols; }
@@ -371,42 +391,69 @@ int64_t pieces(const gs_tensor* t, int32_t n, int64_t piece)
     return s;
 }
 
-// Splits the tensors with values over launches of at most a job's
-// descriptors (and kApart of rows apart): put(descriptor, tensor index) fills
-// in the pointers, go(job, blocks) launches.  in, out: the tensors whose rows
-// may be apart (out may be null).
+// Hands a list to a kernel: put(descriptor, tensor index) fills in the
+// pointers, go(job or table, blocks) launches, once or twice.  in, out: the
+// tensors whose rows may be apart (out may be null).
 template <typename J, typename P, typename G>
-void each_launch(const gs_tensor* in, const gs_tensor* out, int32_t n, int64_t piece, P&& put, G&& go)
+gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, int64_t piece,
+                      std::vector<GsAlloc>* tmp, P&& put, G&& go)
 {
+    typedef typename J::Tensor T;
+    auto is_apart = [&](int32_t k) { return !dense(in[k]) || (out && !dense(out[k])); };
+    int64_t count = 0, aparts = 0, total = 0;
+    for (int32_t k = 0; k < n; ++k)
+        if (in[k].rows * in[k].cols > 0) {
+            total += in[k].rows * in[k].cols;
+            ++count;
+            aparts += is_apart(k);
+        }
+    T* table = nullptr;
+    Apart* table_apart = nullptr;
+    if (total > kLarge && aparts <= 0x7FFF && (count > 3 * J::kCap || aparts > 3 * kApart)) {
+        table = (T*)gs_malloc(ctx, sizeof(T) * count, GS_MEM_SCRATCH, tmp);
+        table_apart = (Apart*)gs_malloc(ctx, sizeof(Apart) * std::max<int64_t>(aparts, 1), GS_MEM_SCRATCH, tmp);
+        if (!table || !table_apart) return GS_ERR_OOM;
+    }
     J job;
     job.piece = piece;
     job.count = job.aparts = 0;
-    uint32_t blocks = 0;
+    int64_t blocks = 0;
+    int32_t at = 0, at_apart = 0;   // table entries filled
     auto flush = [&]() {
-        if (job.count) go(job, blocks);
+        if (job.count == 0) return;
+        if (table) {
+            hipLaunchKernelGGL((k_fill_table<J>), dim3(1), dim3(kThreads), 0, ctx->stream, job, table + at,
+                               table_apart + at_apart);
+            at += job.count;
+            at_apart += job.aparts;
+        } else {
+            go(job, (uint32_t)blocks);
+            blocks = 0;
+        }
         job.count = job.aparts = 0;
-        blocks = 0;
     };
     for (int32_t k = 0; k < n; ++k) {
-        const gs_tensor& t = in[k];
-        const int64_t values = t.rows * t.cols;
+        const int64_t values = in[k].rows * in[k].cols;
         if (values == 0) continue;
-        const bool apart = !dense(t) || (out && !dense(out[k]));
+        const bool apart = is_apart(k);
         if (job.count == J::kCap || (apart && job.aparts == kApart)) flush();
-        blocks += (uint32_t)ceil_div(values, piece);
-        auto& d = job.t[job.count++];
+        blocks += ceil_div(values, piece);
+        T& d = job.t[job.count++];
         d.c.n = values;
-        d.c.bend = blocks;
-        d.c.type = (int8_t)t.type;
+        d.c.bend = (uint32_t)blocks;
+        d.c.type = (int8_t)in[k].type;
         d.c.type2 = 0;
         d.c.apart = -1;
         if (apart) {
-            d.c.apart = (int8_t)job.aparts;
-            job.apart[job.aparts++] = Apart{t.stride, out ? out[k].stride : 0, (uint32_t)t.cols, 0};
+            d.c.apart = (int16_t)(at_apart + job.aparts);
+            job.apart[job.aparts++] = Apart{in[k].stride, out ? out[k].stride : 0, (uint32_t)in[k].cols, 0};
         }
         put(d, k);
     }
     flush();
+    if (table && count > 0) go(Table<T>{table, table_apart, piece, (int32_t)count}, (uint32_t)blocks);
+    GS_HIP(ctx, hipGetLastError());
+    return GS_OK;
 }
 
 // the partials of a list's squares, one per block
@@ -419,13 +466,13 @@ gs_status squares_of(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector
     if (!*part) return GS_ERR_OOM;
     GsTimerScope ts(ctx, "grad_norm");
     int64_t base = 0;
-    each_launch<NormJob>(grads, nullptr, n, piece, [&](NormTensor& d, int32_t k) { d.p = grads[k].data; },
-                         [&](const NormJob& job, uint32_t nb) {
-                             hipLaunchKernelGGL(k_squares, dim3(nb), dim3(kThreads), 0, ctx->stream, job, *part + base);
-                             base += nb;
-                         });
-    GS_HIP(ctx, hipGetLastError());
-    return GS_OK;
+    return launch_list<NormJob>(ctx, grads, nullptr, n, piece, tmp,
+                                [&](NormTensor& d, int32_t k) { d.p = grads[k].data; },
+                                [&](const auto& job, uint32_t nb) {
+                                    hipLaunchKernelGGL((k_squares<std::decay_t<decltype(job)>>), dim3(nb),
+                                                       dim3(kThreads), 0, ctx->stream, job, *part + base);
+                                    base += nb;
+                                });
 }
 
 }  // namespace
@@ -453,23 +500,26 @@ gs_status launch_clip(gs_ctx* ctx, const gs_tensor* in, int32_t n, double max_no
     const gs_status st = squares_of(ctx, in, n, tmp, &part, &parts);
     if (st != GS_OK) return st;
     GsTimerScope ts(ctx, "clip");
-    float* write = norm;   // by the first launch
-    each_launch<ScaleJob>(in, out, n, piece_of(ctx, total),
-                          [&](ScaleTensor& d, int32_t k) {
-                              d.p = in[k].data;
-                              d.o = out[k].data;
-                          },
-                          [&](const ScaleJob& job, uint32_t nb) {
-                              hipLaunchKernelGGL(k_scale, dim3(nb), dim3(kThreads), 0, ctx->stream, job, part, parts,
-                                                 max_norm, write);
-                              write = nullptr;
-                          });
-    GS_HIP(ctx, hipGetLastError());
-    return GS_OK;
+    const bool large = total > kLarge;
+    if (large)
+        hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, part, parts, max_norm, norm);
+    int write = 1;   // the first launch writes the norm
+    return launch_list<ScaleJob>(ctx, in, out, n, large ? kLargePiece : piece_of(ctx, total), tmp,
+                                 [&](ScaleTensor& d, int32_t k) {
+                                     d.p = in[k].data;
+                                     d.o = out[k].data;
+                                 },
+                                 [&](const auto& job, uint32_t nb) {
+                                     hipLaunchKernelGGL((k_scale<std::decay_t<decltype(job)>>), dim3(nb),
+                                                        dim3(kThreads), 0, ctx->stream, job, large ? nullptr : part,
+                                                        parts, max_norm, norm, write);
+                                     write = 0;
+                                 });
 }
 
 gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, const gs_tensor* v, const gs_tensor* g,
-                           const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm)
+                           const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm,
+                           std::vector<GsAlloc>* tmp)
 {
     AdamConst a;
     a.b1 = (float)o->beta1;
@@ -481,18 +531,17 @@ gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
     a.eps = (float)o->eps;
     a.keep = (float)(1.0 - o->lr * o->weight_decay);
     GsTimerScope ts(ctx, "adam_list");
-    each_launch<AdamJob>(g, nullptr, n, piece_of(ctx, values(g, n)),
-                         [&](AdamTensor& d, int32_t k) {
-                             d.p = (float*)p[k].data;
-                             d.m = (float*)m[k].data;
-                             d.v = (float*)v[k].data;
-                             d.g = g[k].data;
-                             d.copy = copies ? copies[k].data : nullptr;
-                             d.c.type2 = (int8_t)(copies ? copies[k].type : 0);
-                         },
-                         [&](const AdamJob& job, uint32_t nb) {
-                             hipLaunchKernelGGL(k_adam_list, dim3(nb), dim3(kThreads), 0, ctx->stream, job, a, norm);
-                         });
-    GS_HIP(ctx, hipGetLastError());
-    return GS_OK;
+    return launch_list<AdamJob>(ctx, g, nullptr, n, kAdamPiece, tmp,
+                                [&](AdamTensor& d, int32_t k) {
+                                    d.p = (float*)p[k].data;
+                                    d.m = (float*)m[k].data;
+                                    d.v = (float*)v[k].data;
+                                    d.g = g[k].data;
+                                    d.copy = copies ? copies[k].data : nullptr;
+                                    d.c.type2 = (int8_t)(copies ? copies[k].type : 0);
+                                },
+                                [&](const auto& job, uint32_t nb) {
+                                    hipLaunchKernelGGL((k_adam_list<std::decay_t<decltype(job)>>), dim3(nb),
+                                                       dim3(kThreads), 0, ctx->stream, job, a, norm);
+                                });
 }

@@ -182,8 +182,8 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
         total += params[k].rows * params[k].cols;
         if (total > (1ll << 42)) return gs_fail(ctx, GS_ERR_OVERFLOW, "more than 2^42 values");
     }
-    return guarded(ctx, [&](std::vector<GsAlloc>*) {
-        return launch_adam_list(ctx, params, m, v, grads, copies, n_tensors, opts, norm);
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_adam_list(ctx, params, m, v, grads, copies, n_tensors, opts, norm, tmp);
     });
 }
 
