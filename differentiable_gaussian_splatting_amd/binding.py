@@ -11,6 +11,7 @@ it is missing, ``load()`` raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes as C
 import os
 import re
@@ -90,7 +91,8 @@ class gs_view_opts(C.Structure):
                 ("adam_v", C.c_void_p), ("adam_chunk", C.c_int64), ("leaves_in", C.c_void_p),
                 ("n_leaves_in", C.c_int32), ("leaves_in_partial", C.c_int32), ("gate", C.c_void_p),
                 ("gate_view", C.c_int32), ("serial_leaves", C.c_int32), ("target_host", C.c_int32),
-                ("leaf_bytes_out", C.c_void_p), ("loss_out", C.c_void_p)]
+                ("leaf_bytes_out", C.c_void_p), ("loss_out", C.c_void_p), ("clip_norm", C.c_float),
+                ("pad", C.c_int32), ("norm_out", C.c_void_p)]
 
 
 class gs_gate_decision(C.Structure):
@@ -493,10 +495,10 @@ def _type_code(dtype):
     return _type_codes.get(dtype, -1)
 
 
-def tensor_struct(t, device=None) -> gs_tensor:
-    """gs_tensor of a device tensor: a 2-D tensor with unit column stride (rows may be apart, or one row
-    broadcast), or a contiguous tensor of any other shape, taken as one row."""
-    if not t.is_cuda or (device is not None and t.device != device):
+def _tensor_fields(t, device=None):
+    """data, rows, cols, stride and type of a device tensor's gs_tensor: a 2-D tensor with unit column stride
+    (rows may be apart, or one row broadcast), or a contiguous tensor of any other shape, taken as one row."""
+    if not t.is_cuda or (device is not None and t.get_device() != device.index):
         raise ValueError(f"a tensor on {t.device}: expected {device or 'a GPU'}")
     code = _type_code(t.dtype)
     if code < 0 or code > GS_BF16:
@@ -506,11 +508,15 @@ def tensor_struct(t, device=None) -> gs_tensor:
         stride, inner = t.stride()
         if inner != 1 and cols > 1:
             raise ValueError("the columns of a 2-D tensor must be contiguous")
-        return gs_tensor(t.data_ptr(), rows, cols, stride, code, 0)
+        return t.data_ptr(), rows, cols, stride, code
     if not t.is_contiguous():
         raise ValueError("a tensor that is not 2-D must be contiguous")
     n = t.numel()
-    return gs_tensor(t.data_ptr(), 1, n, n, code, 0)
+    return t.data_ptr(), 1, n, n, code
+
+
+def tensor_struct(t, device=None) -> gs_tensor:
+    return gs_tensor(*_tensor_fields(t, device), 0)
 
 
 class TensorList:
@@ -520,12 +526,13 @@ class TensorList:
     def __init__(self, tensors):
         self.tensors = list(tensors)
         self.n = len(self.tensors)
-        self.array = (gs_tensor * max(self.n, 1))()
         self.device = next((t.device for t in self.tensors if t is not None), None)
-        for k, t in enumerate(self.tensors):
-            if t is not None:
-                self.array[k] = tensor_struct(t, self.device)
-        self.ptr = C.cast(self.array, C.c_void_p)
+        # gs_tensor as five 64-bit words (type and pad share the last; both little-endian)
+        words = array.array("q")
+        for t in self.tensors:
+            words.extend((0, 0, 0, 0, 0) if t is None else _tensor_fields(t, self.device))
+        self._words = words
+        self.ptr = C.c_void_p(words.buffer_info()[0] if self.n else None)
 
     def __len__(self):
         return self.n
@@ -682,7 +689,8 @@ def gs_train_cost_model():
 
 def gs_train_view(ctx: Context, cam, params: DeviceScene, target, budget_bytes=0, loss="l1", lam=0.2,
                   adam=None, image_out=None, grad3d_out=None, strict=False, cost=None, max_leaves=0,
-                  leaves_in=None, partial=False, gate=None, gate_view=0, serial_leaves=False, loss_out=None):
+                  leaves_in=None, partial=False, gate=None, gate_view=0, serial_leaves=False, loss_out=None,
+                  clip_norm=0.0, norm_out=None):
     """One whole view in the library (see gs_train_view in include/gs.h).
     adam: None or dict(step, params=DeviceScene (updated), m, v, lr, beta1, beta2, eps, chunk).
     leaves_in: a cached layout (list of leaf dicts) to re-check instead of planning afresh.
@@ -691,8 +699,13 @@ def gs_train_view(ctx: Context, cam, params: DeviceScene, target, budget_bytes=0
     target: a device tensor, or a CPU tensor (pinned for the copies to overlap), which the
     library copies leaf by leaf.
     loss_out: a device float64 tensor (one element used): the loss is written there and not read
-    back (the call does not wait for the view's end); the returned "loss" is then None."""
+    back (the call does not wait for the view's end); the returned "loss" is then None.
+    clip_norm > 0: the view's gradient is clipped to that global norm before the update; norm_out: a
+    device float32 tensor of two values for the norm and the factor."""
     o = gs_view_opts()
+    o.clip_norm = float(clip_norm)
+    if norm_out is not None:
+        o.norm_out = _norm_ptr(norm_out, ctx)
     o.serial_leaves = int(bool(serial_leaves))
     o.target_host = int(not target.is_cuda)
     if not target.is_cuda and not target.is_contiguous():

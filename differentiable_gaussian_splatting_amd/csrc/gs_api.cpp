@@ -1763,6 +1763,9 @@ gs_status gs_train_view(gs_ctx* ctx, const gs_camera* cam, const gs_params* para
         return gs_fail(ctx, GS_ERR_INVALID_ARG, "Adam needs params_rw, adam_m, adam_v");
     if (opts->gate && opts->loss_out)
         return gs_fail(ctx, GS_ERR_INVALID_ARG, "a gated view needs its loss on the host (loss_out must be NULL)");
+    if (!(opts->clip_norm >= 0.0f) || (uintptr_t)opts->norm_out % 4)
+        return gs_fail(ctx, GS_ERR_INVALID_ARG, "clip_norm must be >= 0, norm_out aligned");
+    const bool clip = opts->clip_norm > 0.0f || opts->norm_out;
     std::memset(result, 0, sizeof(*result));
     gs_status st;
     gs_proj* proj = nullptr;
@@ -1885,10 +1888,19 @@ gs_status gs_train_view(gs_ctx* ctx, const gs_camera* cam, const gs_params* para
     if ((st = render_leaves(ctx, cam, proj, target, opts, leaves, true, grad2d, l1_view, image, loss_dev + 1,
                             &isect_total, walk, &walk_used)) != GS_OK)
         goto done;
-    if (opts->grad3d_out || opts->adam_step <= 0) {
+    if (opts->grad3d_out || opts->adam_step <= 0 || clip) {
         float* grad3d = (float*)gs_malloc(ctx, sizeof(float) * (int64_t)F * nc, GS_MEM_GRAD, &view);
-        if (!grad3d) { st = GS_ERR_OOM; goto done; }
+        float* norm = !clip ? nullptr
+                      : opts->norm_out ? opts->norm_out
+                                       : (float*)gs_malloc(ctx, 2 * sizeof(float), GS_MEM_GRAD, &view);
+        if (!grad3d || (clip && !norm)) { st = GS_ERR_OOM; goto done; }
         if ((st = gs_project_bwd(ctx, cam, params, proj, grad2d, grad3d)) != GS_OK) goto done;
+        if (clip) {
+            const gs_tensor g{grad3d, n_cand, F, F, GS_F32, 0};
+            const double limit = opts->clip_norm > 0.0f ? (double)opts->clip_norm
+                                                        : std::numeric_limits<double>::infinity();
+            if ((st = launch_clip(ctx, &g, 1, limit, &g, norm, &view)) != GS_OK) goto done;
+        }
         if (opts->grad3d_out && (st = launch_scatter_grad3d(ctx, proj, F, grad3d, opts->grad3d_out)) != GS_OK)
             goto done;
         if (opts->adam_step > 0 &&

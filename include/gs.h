@@ -454,7 +454,8 @@ gs_status gs_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, d
 
 /* gs_grad_norm, then out[k] = norm[1] grads[k] for every tensor, in f32 and
  * rounded once.  out: n_tensors descriptors of the same sizes and types, or
- * NULL to scale grads in place (no value is written when the factor is 1). */
+ * NULL to scale grads in place (no value is written when the factor is 1).  An
+ * out tensor is its own gradient or does not overlap any gradient. */
 gs_status gs_clip_grads(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, double max_norm, const gs_tensor* out,
                         float* norm);
 
@@ -546,6 +547,14 @@ typedef struct {
                                  /* Same bits as the read-back value.  Not     */
                                  /* with a gate, whose decision needs the loss */
                                  /* on the host: GS_ERR_INVALID_ARG            */
+    float clip_norm;             /* > 0: the view's whole gradient is scaled   */
+    int32_t pad;                 /* by min(1, clip_norm / (norm + 1e-6)) as by */
+    float* norm_out;             /* gs_clip_grads before grad3d_out and the    */
+                                 /* update; 0: it is not.  norm_out: device,   */
+                                 /* nullable: norm and factor (two floats) are */
+                                 /* written there.  With either, the compact   */
+                                 /* gradient (n_cand x F) is held whole and    */
+                                 /* adam_chunk is not used                     */
 } gs_view_opts;
 
 typedef struct {
