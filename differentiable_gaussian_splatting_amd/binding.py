@@ -177,8 +177,8 @@ def load(path: str = LIB_PATH):
         "gs_export_size": (st, [vp, vp, i32, P(C.c_size_t)]),
         "gs_util_exp": (st, [vp, vp, vp, i64]),
         "gs_util_exp_falloff": (st, [vp, vp, vp, i64]),
-        "gs_embed_fwd": (st, [vp, P(gs_tensor), vp, i32, i64, C.c_float, P(gs_tensor)]),
-        "gs_embed_bwd": (st, [vp, vp, i32, i64, P(gs_tensor), C.c_float, i64, i32, P(gs_tensor)]),
+        "gs_embed_fwd": (st, [vp, vp, vp, i32, i64, C.c_float, vp]),
+        "gs_embed_bwd": (st, [vp, vp, i32, i64, vp, C.c_float, i64, i32, vp]),
         "gs_grad_norm": (st, [vp, vp, i32, C.c_double, vp]),
         "gs_clip_grads": (st, [vp, vp, i32, C.c_double, vp, vp]),
         "gs_adam_tensors": (st, [vp, vp, vp, vp, vp, vp, i32, P(gs_adam_opts), vp]),
@@ -218,6 +218,8 @@ class Context:
     libgsmi_torchalloc.so is built, else (or with torch_allocator="python")
     by Python callbacks; torch_allocator=False: the library's own
     hipMallocAsync."""
+
+    words = None   # descriptors of a call's tensors (_two_tensors)
 
     def __init__(self, device=None, stream=None, torch_allocator=True):
         import torch
@@ -540,20 +542,31 @@ class TensorList:
 
 def _as_list(tensors, ctx):
     lst = tensors if isinstance(tensors, TensorList) else TensorList(tensors)
-    if lst.device is not None and lst.device != ctx.device:
+    if lst.device is not None and lst.device.index != ctx.device.index:
         raise ValueError(f"tensors on {lst.device}, the context is on {ctx.device}")
     return lst
 
 
 def _index(idx, ctx):
     code = _type_code(idx.dtype)
-    if code < GS_I32 or idx.device != ctx.device or not idx.is_contiguous():
+    if code < GS_I32 or not idx.is_cuda or idx.get_device() != ctx.device.index or not idx.is_contiguous():
         raise ValueError("indices must be a contiguous int32 or int64 tensor on the context's device")
     return code
 
 
+def _two_tensors(ctx, a, b):
+    """Addresses of two gs_tensors, in words that the context keeps for its calls (five each, as in TensorList)."""
+    w = ctx.words
+    if w is None:
+        w = ctx.words = array.array("q", [0] * 10)
+    w[0], w[1], w[2], w[3], w[4] = _tensor_fields(a, ctx.device)
+    w[5], w[6], w[7], w[8], w[9] = _tensor_fields(b, ctx.device)
+    at = w.buffer_info()[0]
+    return at, at + 40
+
+
 def _norm_ptr(norm, ctx):
-    if norm.device != ctx.device or _type_code(norm.dtype) != GS_F32 or norm.numel() < 2 or not norm.is_contiguous():
+    if not norm.is_cuda or norm.get_device() != ctx.device.index or _type_code(norm.dtype) != GS_F32 or norm.numel() < 2 or not norm.is_contiguous():
         raise ValueError("norm must be a float32 tensor of two values on the context's device")
     return norm.data_ptr()
 
@@ -566,16 +579,16 @@ def gs_embed_fwd(ctx: Context, table, idx, out=None, scale=1.0):
     if out is None:
         with ctx.torch.cuda.stream(ctx.stream):
             out = table.new_empty((n, table.shape[1]))
-    ctx.check(ctx.lib.gs_embed_fwd(ctx.handle, tensor_struct(table, ctx.device), idx.data_ptr(), code, n, scale,
-                                   tensor_struct(out, ctx.device)))
+    t, o = _two_tensors(ctx, table, out)
+    ctx.check(ctx.lib.gs_embed_fwd(ctx.handle, t, idx.data_ptr(), code, n, scale, o))
     return out
 
 
 def gs_embed_bwd(ctx: Context, idx, dout, dtable, scale=1.0, padding=-1, accumulate=False):
     """dtable[v] = scale * sum of dout[i] over idx[i] == v (added to dtable when accumulate)."""
     code = _index(idx, ctx)
-    ctx.check(ctx.lib.gs_embed_bwd(ctx.handle, idx.data_ptr(), code, idx.numel(), tensor_struct(dout, ctx.device),
-                                   scale, padding, accumulate, tensor_struct(dtable, ctx.device)))
+    g, t = _two_tensors(ctx, dout, dtable)
+    ctx.check(ctx.lib.gs_embed_bwd(ctx.handle, idx.data_ptr(), code, idx.numel(), g, scale, padding, accumulate, t))
     return dtable
 
 
