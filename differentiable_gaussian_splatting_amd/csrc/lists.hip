@@ -107,18 +107,34 @@ __device__ __forceinline__ int tensor_of_block(const J& job, uint32_t b, uint32_
     return lo;
 }
 
-// f(k, place) for every value k of [k0, k1) of a tensor whose rows are apart;
-// place: its offset with row stride `stride`, place2 with `ostride`.  The
+// For the values k of [k0, k1) of a tensor whose rows are apart:
+// use(k, place2, get(k, place)), place its offset with row stride `stride`,
+// place2 with `ostride`; a thread gets four values before it uses them.  The
 // first row is divided for once, the rest in 32 bits (a piece is < 2^31).
-template <typename F>
-__device__ __forceinline__ void each_apart(const Apart& a, int64_t k0, int64_t k1, F&& f)
+template <typename G, typename F>
+__device__ __forceinline__ void each_apart(const Apart& a, int64_t k0, int64_t k1, G&& get, F&& use)
 {
+    constexpr int U = 4;
     const int64_t row0 = k0 / a.cols;
-    const uint32_t rem = (uint32_t)(k0 - row0 * a.cols);
-    for (uint32_t j = threadIdx.x; j < (uint32_t)(k1 - k0); j += kThreads) {
-        const uint32_t r = (rem + j) / a.cols, c = (rem + j) - r * a.cols;
-        f(k0 + j, (row0 + r) * a.stride + c, (row0 + r) * a.ostride + c);
-    }
+    const uint32_t rem = (uint32_t)(k0 - row0 * a.cols), n = (uint32_t)(k1 - k0);
+    auto run = [&](uint32_t j, auto count) {
+        constexpr int N = decltype(count)::value;
+        int64_t row[N];
+        uint32_t c[N];
+        decltype(get(int64_t{}, int64_t{})) x[N];
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const uint32_t i = rem + j + u * kThreads, r = i / a.cols;
+            row[u] = row0 + r;
+            c[u] = i - r * a.cols;
+            x[u] = get(k0 + j + u * kThreads, row[u] * a.stride + c[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < N; ++u) use(k0 + j + u * kThreads, row[u] * a.ostride + c[u], x[u]);
+    };
+    uint32_t j = threadIdx.x;
+    for (; j + (U - 1) * kThreads < n; j += U * kThreads) run(j, std::integral_constant<int, U>{});
+    for (; j < n; j += kThreads) run(j, std::integral_constant<int, 1>{});
 }
 
 // a job's descriptors into a table
@@ -203,10 +219,12 @@ __global__ __launch_bounds__(kThreads) void k_squares(J job, double* __restrict_
         if (t.c.apart < 0) s = squares<T>(p, t.c.n, among, blocks);
         else {
             const int64_t k0 = among * job.piece;
-            each_apart(job.apart[t.c.apart], k0, min(t.c.n, k0 + job.piece), [&](int64_t, int64_t at, int64_t) {
-                const double d = (double)(float)p[at];
-                s = __builtin_fma(d, d, s);
-            });
+            each_apart(job.apart[t.c.apart], k0, min(t.c.n, k0 + job.piece),
+                       [&](int64_t, int64_t at) { return p[at]; },
+                       [&](int64_t, int64_t, T v) {
+                           const double d = (double)(float)v;
+                           s = __builtin_fma(d, d, s);
+                       });
         }
     };
     if (t.c.type == GS_F32) typed(float{});
@@ -269,9 +287,8 @@ __global__ __launch_bounds__(kThreads) void k_scale(J job, const double* __restr
         T* o = (T*)t.o;
         if (t.c.apart < 0) scale<T>(p + k0, o + k0, k1 - k0, c);
         else
-            each_apart(job.apart[t.c.apart], k0, k1, [&](int64_t, int64_t at, int64_t to) {
-                o[to] = gst::narrow<T>(c * (float)p[at]);
-            });
+            each_apart(job.apart[t.c.apart], k0, k1, [&](int64_t, int64_t at) { return p[at]; },
+                       [&](int64_t, int64_t to, T v) { o[to] = gst::narrow<T>(c * (float)v); });
     };
     if (t.c.type == GS_F32) typed(float{});
     else if (t.c.type == GS_F16) typed(gst::f16{});
@@ -347,14 +364,22 @@ __global__ __launch_bounds__(kThreads) void k_adam_list(J job, AdamConst a, cons
         using T = decltype(x);
         if (t.c.apart < 0) adam<T>(t, k0, k1 - k0, c, a);
         else
-            each_apart(job.apart[t.c.apart], k0, k1, [&](int64_t k, int64_t at, int64_t) {
-                float p = t.p[k], m = t.m[k], v = t.v[k];
-                adam_value(c * (float)((const T*)t.g)[at], p, m, v, a);
-                t.p[k] = p;
-                t.m[k] = m;
-                t.v[k] = v;
-                if (t.copy) put_copy(t, k, p);
-            });
+        {
+            struct Values {
+                float p, m, v, g;
+            };
+            each_apart(job.apart[t.c.apart], k0, k1,
+                       [&](int64_t k, int64_t at) {
+                           return Values{t.p[k], t.m[k], t.v[k], (float)((const T*)t.g)[at]};
+                       },
+                       [&](int64_t k, int64_t, Values x) {
+                           adam_value(c * x.g, x.p, x.m, x.v, a);
+                           t.p[k] = x.p;
+                           t.m[k] = x.m;
+                           t.v[k] = x.v;
+                           if (t.copy) put_copy(t, k, x.p);
+                       });
+        }
     };
     if (t.c.type == GS_F32) typed(float{});
     else if (t.c.type == GS_F16) typed(gst::f16{});
@@ -456,6 +481,30 @@ gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, in
     return GS_OK;
 }
 
+// Tensors that are neighbouring columns of the same rows (the groups of a
+// view's gradient rows) as one tensor of all those columns, so that the rows'
+// cache lines are read once: neither the norm nor the scaling needs them
+// apart.  in2: a second list (the outputs) that has to adjoin as well, or null.
+void join_columns(const gs_tensor* in, const gs_tensor* in2, int32_t n, std::vector<gs_tensor>* out,
+                  std::vector<gs_tensor>* out2)
+{
+    auto adjoins = [](const gs_tensor& a, const gs_tensor& b) {
+        const int64_t size = a.type == GS_F32 ? 4 : 2;
+        return a.type == b.type && a.rows == b.rows && a.rows > 1 && a.stride == b.stride &&
+               (char*)b.data == (char*)a.data + a.cols * size && a.cols + b.cols <= a.stride;
+    };
+    for (int32_t k = 0; k < n; ++k) {
+        if (in[k].rows * in[k].cols == 0) continue;
+        if (!out->empty() && adjoins(out->back(), in[k]) && (!in2 || adjoins(out2->back(), in2[k]))) {
+            out->back().cols += in[k].cols;
+            if (in2) out2->back().cols += in2[k].cols;
+        } else {
+            out->push_back(in[k]);
+            if (in2) out2->push_back(in2[k]);
+        }
+    }
+}
+
 // the partials of a list's squares, one per block
 gs_status squares_of(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector<GsAlloc>* tmp, double** part,
                      int64_t* parts)
@@ -477,9 +526,13 @@ gs_status squares_of(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector
 
 }  // namespace
 
-gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n, double max_norm, float* norm,
+gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* list, int32_t count, double max_norm, float* norm,
                            std::vector<GsAlloc>* tmp)
 {
+    std::vector<gs_tensor> joined;
+    join_columns(list, nullptr, count, &joined, nullptr);
+    const gs_tensor* grads = joined.data();
+    const int32_t n = (int32_t)joined.size();
     double* part;
     int64_t parts;
     const gs_status st = squares_of(ctx, grads, n, tmp, &part, &parts);
@@ -490,9 +543,13 @@ gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n, doubl
     return GS_OK;
 }
 
-gs_status launch_clip(gs_ctx* ctx, const gs_tensor* in, int32_t n, double max_norm, const gs_tensor* out, float* norm,
-                      std::vector<GsAlloc>* tmp)
+gs_status launch_clip(gs_ctx* ctx, const gs_tensor* list, int32_t count, double max_norm, const gs_tensor* to,
+                      float* norm, std::vector<GsAlloc>* tmp)
 {
+    std::vector<gs_tensor> joined, joined_out;
+    join_columns(list, to, count, &joined, &joined_out);
+    const gs_tensor *in = joined.data(), *out = joined_out.data();
+    const int32_t n = (int32_t)joined.size();
     const int64_t total = values(in, n);
     if (total == 0) return launch_grad_norm(ctx, in, n, max_norm, norm, tmp);
     double* part;
