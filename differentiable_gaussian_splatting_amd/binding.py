@@ -530,10 +530,20 @@ class TensorList:
         self.n = len(self.tensors)
         self.device = next((t.device for t in self.tensors if t is not None), None)
         # gs_tensor as five 64-bit words (type and pad share the last; both little-endian)
-        words = array.array("q")
+        words = []
+        index = self.device.index if self.device is not None else -1
+        dtype, code = None, -1
         for t in self.tensors:
-            words.extend((0, 0, 0, 0, 0) if t is None else _tensor_fields(t, self.device))
-        self._words = words
+            if t is None:
+                words += (0, 0, 0, 0, 0)
+            elif t.dim() == 2 or t.get_device() != index or not t.is_contiguous():
+                words += _tensor_fields(t, self.device)
+            else:   # the usual case, without the calls: lists may hold hundreds of tensors
+                if t.dtype is not dtype:
+                    dtype, code = t.dtype, _tensor_fields(t, self.device)[4]
+                n = t.numel()
+                words += (t.data_ptr(), 1, n, n, code)
+        self._words = words = array.array("q", words)
         self.ptr = C.c_void_p(words.buffer_info()[0] if self.n else None)
 
     def __len__(self):

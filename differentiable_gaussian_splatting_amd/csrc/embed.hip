@@ -3,9 +3,20 @@
 //   forward   out[i, c] = scale table[idx[i], c]
 //   backward  dtable[v, c] = scale sum over {i : idx[i] = v} of dout[i, c]
 //
+// Both move memory and compute next to nothing.  Forward, 6M x 48 f32 from
+// 65536 rows: 254 us, 4.7 TB/s of indices, table and output; with a table that
+// stays in one XCD's L2 (500 rows) 169 us, 6.9 TB/s, the rate of plain stores;
+// the 12.6 MB table does not (4 MB a piece), and its reads from the last cache
+// bound the call.  16384 x 4096 bf16: 29 us.
+//
 // The backward groups the positions i by index with a stable sort, so that
-// each row's sum runs over its positions in ascending order and needs no
-// atomics: the result does not depend on timing.
+// each row's sum runs over its positions in a fixed order and needs no
+// atomics: the result does not depend on timing.  6M x 48 f32 (rows 59 apart,
+// a quarter of them on one table row): 472 us, of which the sums take 361: a
+// row of 192 bytes that starts anywhere touches 2.5 lines of 128 bytes, 2.0 GB
+// in all at 5.6 TB/s; the grouping takes 95 and the join 17.  16384 x 4096
+// bf16 into 32768 rows of f32: 150 us, of which the sums with the cleared rows
+// take 130 (671 MB, 5.2 TB/s).
 #include "gs_device.h"
 #include "gs_internal.h"
 #include "gs_tensor.h"
@@ -30,7 +41,10 @@ __device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i,
 // The rows of out are cut into packs of VEC values (16 bytes of the wider
 // type); the last pack of a row whose width is no multiple of VEC starts
 // earlier and repeats some of the values before it.  A thread looks up one
-// pack, so that a wavefront writes 1 KB of neighbouring packs.  Pack k of a
+// pack, so that a wavefront writes 1 KB of neighbouring packs (two, four and
+// eight packs in flight per thread took 261, 266 and 267 us where one takes
+// 254, 6M x 48 f32), with stores that do not stay in the L2 (336 us with plain
+// ones, which push the table out of it).  Pack k of a
 // block is in row (rem + k) / per_row from the block's first row: a product
 // with `magic` (floor(2^32 / per_row) + 1, exact for k per_row < 2^32) where
 // 1 < per_row < 1024, else a compare (a block then meets at most two rows).
@@ -179,13 +193,20 @@ __device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, 
     }
 }
 
-// (2) Each team walks its chunk in batches of positions, eight rows in flight,
+// (2) Bound by the rows' random reads.  A team's lanes hold 16 bytes of a row
+// each, so that a row is read in one piece, and chunks of positions instead of
+// table rows are shared out, so that a row that many positions name costs no
+// more than others (a thread per table row took 645 ms with a quarter of 6M
+// positions on one).  Each team walks its chunk in batches, eight rows in
+// flight (the loads must not be behind branches: waiting for each in turn took
+// 470 us where this takes 361),
 // and adds rows while the table row stays the same.  A run inside the chunk is
 // written at once.  A chunk's first run, if it began before, is its head, and
 // its last, if it goes on, its tail.  After the block's teams are done, the
 // heads that belong to one run are added over the teams by doubling steps, and
 // the team in which the run begins adds its tail and writes the row, or the
-// block's piece of it (head / tail) if the run leaves the block.  Blocks after those of the positions clear the unused rows, in
+// block's piece of it (head / tail) if the run leaves the block.  Blocks after
+// those of the positions clear the unused rows, in
 // the same launch so that their stores run beside the loads.
 constexpr int kBatch = 8;
 template <typename T, int VEC>
@@ -318,7 +339,7 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
     }
 }
 
-// (3) One block per border between blocks of (2): if a run begins in the block
+// (3) One block per border between blocks of (2), most of which end at once: if a run begins in the block
 // before it and crosses the border, its tail and the heads of the blocks after
 // it are added, the teams taking every teams-th piece, their sums in order.
 template <int VEC>

@@ -2,9 +2,13 @@
 // a stable sort of (row, position), the positions ascending within a row.
 //
 // Up to kRankMax positions: tiles sorted by counting, then merged (one or two
-// launches, where the passes below take three each).  More: two or three passes of up to 9 bits of the row, lowest first, each a histogram per tile
+// launches, where the passes below take three each; a whole table gradient of
+// 16384 x 8 f32 takes 22 us so and 48 us with passes, at 65536 x 8 both take
+// about 50, at 131072 x 8 90 and 54).  More: two or three passes of up to 9 bits of the row, lowest first, each a histogram per tile
 // of 4096 positions, a scan of every digit's counts over the tiles, and a
-// stable scatter; the first pass reads the indices themselves.  Positions
+// stable scatter; the first pass reads the indices themselves.  6M positions
+// by 16 bits: 95 us, two passes of 10 us (histogram), 5 (scan) and 33 (scatter,
+// 96 MB moved; tiles of 8192 took 38).  Positions
 // that name no row (masked, padding) have a digit of their own after all
 // others in every pass, so that they end up last without a bit of the key.
 #include "gs_device.h"
@@ -319,7 +323,7 @@ __global__ __launch_bounds__(kThreads) void k_group_scatter(const I* __restrict_
 
 }  // namespace
 
-// positions up to which tiles are counted and merged
+// positions up to which tiles are counted and merged (the times above)
 constexpr int64_t kRankMax = 65536;
 
 gs_status launch_group(gs_ctx* ctx, const void* idx, int idx_type, int64_t n, int64_t rows, int64_t skip,

@@ -95,3 +95,31 @@ def test_a_view_without_candidates_has_norm_zero(ctx):
     ds = B.DeviceScene(w.scene)
     B.gs_train_view(ctx, w.camera, ds, torch.from_numpy(w.target).cuda(), clip_norm=1.0, norm_out=norm)
     assert norm.tolist() == [0.0, 1.0]
+
+
+def test_a_clipped_view_that_cannot_allocate_changes_nothing():
+    import torch
+    from tests.test_gpu_errors import FailingContext
+    f = FailingContext()
+    w = scenes.make_workload("c1_small", n=300, width=64, height=48, seed=3, sh_degree=1)
+    target = torch.from_numpy(w.target).cuda()
+    ds = B.DeviceScene(w.scene)
+    m, v = B.like_scene(ds), B.like_scene(ds)
+    old = [t.clone() for t in ds.tensors()]
+    live, k = f.mem_stats()["live"], 1
+    while True:
+        f.arm(k)
+        try:
+            B.gs_train_view(f, w.camera, ds, target, adam=dict(step=1, params=ds, m=m, v=v), clip_norm=1e-3)
+            break
+        except B.GsError as e:
+            assert e.status == B.GS_ERR_OOM
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(old, ds.tensors()))
+            assert all(float(t.abs().max()) == 0.0 for t in m.tensors() + v.tensors())
+            assert f.mem_stats()["live"] == live
+        k += 1
+    f.arm(0)
+    torch.cuda.synchronize()
+    assert k > 3 and f.mem_stats()["live"] == live and not torch.equal(old[0], ds.means)
+    f.close()

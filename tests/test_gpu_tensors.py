@@ -643,3 +643,53 @@ def test_refusals_at_the_c_entries(ctx):
     assert L.gs_adam_tensors(h, q, q, q, q, None, 1, None, None) == bad
     assert L.gs_adam_tensors(h, None, q, q, q, None, 1, C.byref(B.gs_adam_opts(1, 0, 1e-3, 0.9, 0.999, 1e-8, 0.0)),
                              None) == bad
+
+
+@pytest.mark.parametrize("n", [65_536, 65_537, 70_001])
+@pytest.mark.parametrize("v,kind", [(1, "uniform"), (2, "masked"), (511, "zipf"), (512, "sorted"), (513, "uniform"),
+                                    (300_000, "masked"), ((1 << 20) + 3, "uniform"), (40, "none"), (1, "masked")])
+def test_gradient_around_the_sorts_limits(ctx, n, v, kind):
+    """Both ways of grouping, one to three passes, and rows at the bits' edges."""
+    check_gradient(ctx, n, v, 2, kind, index="i64" if v % 2 else "i32")
+
+
+@pytest.mark.parametrize("w", [1, 2, 3, 4, 5, 7, 8, 255, 256, 257, 258, 511, 512, 513, 1025])
+def test_gradient_widths(ctx, w):
+    """Widths around the packs and column ranges, each accumulated too (columns that two lanes hold are added once)."""
+    for tn in ("f32", "bf16"):
+        check_gradient(ctx, 300, 11, w, "zipf", tn, "f32")
+        check_gradient(ctx, 300, 11, w, "hot", tn, "f32", accumulate=True)
+
+
+@pytest.mark.parametrize("count", [61, 62, 63, 107, 108, 109, 143, 144, 145, 200])
+def test_lists_around_a_launchs_tensors(ctx, count):
+    """Lists around the tensors of one launch, small and (with one large tensor) described in a table."""
+    torch = _t()
+    for big in (0, 4_100_000):
+        sizes = [k % 7 for k in range(count)] + ([big] if big else [])
+        ts, outs = make_list(sizes, "f32", seed=count), make_list(sizes, "f32", seed=1, lead=1)
+        norm = reference_norm(ts)
+        r = B.gs_clip_grads(ctx, ts, 0.5 * norm, out=outs)
+        close(r[0], norm, 2 * u * norm)
+        c = 0.5 * norm / (norm + 1e-6)
+        for t, o in zip(ts, outs):
+            close(o, f64(t) * c, 5 * u * np.abs(f64(t) * c) + 2.0 ** -149)
+        run_adam(ctx, outs, ts, OPTS, limit=0.1, copies=make_list(sizes, "f16", lead=3))
+
+
+def test_lists_of_many_column_views(ctx):
+    """More tensors with rows apart than a launch holds, in a small list and in one large enough for a table."""
+    torch = _t()
+    gen = torch.Generator().manual_seed(8)
+    for rows in (9, 60_000):
+        wide = torch.randn((rows, 150), generator=gen).cuda()
+        grads = [wide[:, 2 * k:2 * k + 1] for k in range(70)]
+        norm = reference_norm(grads)
+        close(B.gs_grad_norm(ctx, grads, 1.0)[0], norm, 2 * u * norm)
+        params = [torch.randn((rows, 1), generator=gen).cuda() for _ in grads]
+        run_adam(ctx, params, grads, OPTS, limit=1.0)
+        out = wide.clone()
+        B.gs_clip_grads(ctx, grads, 0.5 * norm, out=[out[:, 2 * k:2 * k + 1] for k in range(70)])
+        c = 0.5 * norm / (norm + 1e-6)
+        close(out[:, 0:140:2], f64(wide[:, 0:140:2]) * c, 5 * u * np.abs(f64(wide[:, 0:140:2]) * c))
+        assert torch.equal(out[:, 1:140:2], wide[:, 1:140:2])
