@@ -548,10 +548,15 @@ def test_allocation_failure_leaves_outputs(ctx):
     d = torch.full((70, 5), 2.0, device="cuda")
     g = [torch.randn(5000, device="cuda")]
     norm = torch.full((2,), 9.0, device="cuda")
+    large = [torch.randn(500_000, device="cuda")]
+    norm2 = norm.clone()
     live = f.mem_stats()["live"]
-    for call, same in ((lambda: B.gs_embed_bwd(f, idx, x, d), lambda: d.eq(2.0).all()),
-                       (lambda: B.gs_clip_grads(f, g, 1e-3, norm), lambda: norm.eq(9.0).all())):
-        keep = g[0].clone()
+    # a list as small as g is clipped without an allocation
+    for call, same, allocates in ((lambda: B.gs_embed_bwd(f, idx, x, d), lambda: d.eq(2.0).all(), True),
+                                  (lambda: B.gs_clip_grads(f, g, 1e-3, norm), lambda: norm.eq(9.0).all(), False),
+                                  (lambda: B.gs_clip_grads(f, large, 1e-3, norm2),
+                                   lambda: norm2.eq(9.0).all() and torch.equal(large[0], kept), True)):
+        keep, kept = g[0].clone(), large[0].clone()
         k = 1
         while True:
             f.arm(k)
@@ -564,7 +569,7 @@ def test_allocation_failure_leaves_outputs(ctx):
                 assert same() and torch.equal(g[0], keep) and f.mem_stats()["live"] == live
             k += 1
         f.arm(0)
-        assert k > 1 and f.mem_stats()["live"] == live
+        assert (k > 1) == allocates and f.mem_stats()["live"] == live
     f.close()
 
 
