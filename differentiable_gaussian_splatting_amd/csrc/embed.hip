@@ -158,9 +158,9 @@ __device__ __forceinline__ void put_part(float* row, uint32_t c0, uint32_t cb, c
     }
 }
 
-// Rows [v0, v0 + zero_rows) of dtable, cleared by one wavefront where no
-// position names them: each lane looks one of the rows up in the sorted keys.
-__device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, int64_t v0)
+// Which of the rows [v0, v0 + zero_rows) have no position, a bit each: every
+// lane looks one of them up in the sorted keys.
+__device__ __forceinline__ uint64_t unused_rows(const SumShape& sh, int64_t v0)
 {
     const int lane = threadIdx.x & 63;
     const int64_t v = v0 + lane;
@@ -174,7 +174,31 @@ __device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, 
         }
         unused = lo == sh.n || sh.keys[lo] != (uint32_t)v;
     }
-    uint64_t left = gsd::ballot(unused);
+    return gsd::ballot(unused);
+}
+
+// The same from a short list of indices: the lanes read all of them.
+template <typename I>
+__device__ __forceinline__ uint64_t unnamed_rows(const SumShape& sh, const I* __restrict__ idx, int64_t skip,
+                                                 int64_t v0)
+{
+    const int lane = threadIdx.x & 63;
+    uint64_t named = 0;
+    for (int64_t j = lane; j < sh.n; j += 64) {
+        const uint32_t r = row_of(idx, j, sh.rows, skip);
+        const int64_t rel = (int64_t)r - v0;
+        if (r < sh.rows && rel >= 0 && rel < 64) named |= 1ull << rel;
+    }
+    for (int o = 1; o < 64; o <<= 1) named |= (uint64_t)__shfl_xor((unsigned long long)named, o, 64);
+    const int64_t there = min((int64_t)sh.zero_rows, (int64_t)sh.rows - v0);
+    const uint64_t rows = there <= 0 ? 0ull : there >= 64 ? ~0ull : (1ull << there) - 1ull;
+    return rows & ~named;
+}
+
+// zeros in the rows v0 + r of dtable whose bit r of `left` is set, by one wavefront
+__device__ __forceinline__ void clear_rows(const SumShape& sh, const Dest& d, int64_t v0, uint64_t left)
+{
+    const int lane = threadIdx.x & 63;
     const gst::Pack<uint16_t, 8> zero{};
     const int esize = d.type == GS_F32 ? 4 : 2;
     const int64_t bytes = (int64_t)sh.cols * esize;
@@ -208,19 +232,74 @@ __device__ __forceinline__ void clear_unused(const SumShape& sh, const Dest& d, 
 // block's piece of it (head / tail) if the run leaves the block.  Blocks after
 // those of the positions clear the unused rows, in
 // the same launch so that their stores run beside the loads.
-constexpr int kBatch = 8;
-template <typename T, int VEC>
-__global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride, SumShape sh, Dest d)
+//
+// TINY: up to kTiny positions that one block of 1024 threads holds in one
+// batch per team.  The block sorts them itself, by counting as in group.hip, so
+// that a small gradient is one launch.
+constexpr int kBatch = 8, kTiny = 512;
+template <typename I>
+__device__ __forceinline__ void sort_tiny(const I* __restrict__ idx, int n, uint32_t rows, int64_t skip,
+                                          uint32_t* keys, uint32_t* pos)
 {
-    __shared__ float heads[256 * VEC];
-    __shared__ uint8_t on_from[256];   // per team: its head's run goes on behind what is added so far
+    __shared__ uint4 raw4[kTiny / 4];
+    __shared__ uint32_t cnt[2][kTiny];
+    uint32_t* raw = reinterpret_cast<uint32_t*>(raw4);
+    const int t = threadIdx.x, i = t % kTiny, half = t / kTiny, i0 = i & ~63;   // 1024 threads: two per position
+    if (half == 0) raw[i] = i < n ? row_of(idx, i, rows, skip) : 0xFFFFFFFFu;
+    __syncthreads();
+    const uint32_t ki = raw[i];
+    const int n4 = (n + 3) / 4, q0 = half ? (n4 + 1) / 2 : 0, q1 = half ? n4 : (n4 + 1) / 2;
+    const int b0 = i0 / 4, b1 = b0 + 16;   // the wavefront's own positions
+    uint32_t c = 0;
+    auto count = [&](int qa, int qb, uint32_t thr) {
+#pragma unroll 4
+        for (int q = qa; q < qb; ++q) {
+            const uint4 k = raw4[q];
+            c += (k.x < thr ? 1u : 0u) + (k.y < thr ? 1u : 0u) + (k.z < thr ? 1u : 0u) + (k.w < thr ? 1u : 0u);
+        }
+    };
+    if (i0 < n) {
+        count(q0, min(q1, b0), ki + 1u);
+        for (int q = max(q0, b0); q < min(q1, b1); ++q) {
+            const uint4 k = raw4[q];
+            c += (k.x < ki + (4 * q < i ? 1u : 0u) ? 1u : 0u) + (k.y < ki + (4 * q + 1 < i ? 1u : 0u) ? 1u : 0u) +
+                 (k.z < ki + (4 * q + 2 < i ? 1u : 0u) ? 1u : 0u) + (k.w < ki + (4 * q + 3 < i ? 1u : 0u) ? 1u : 0u);
+        }
+        count(max(q0, b1), q1, ki);
+    }
+    cnt[half][i] = c;
+    __syncthreads();
+    if (half == 0 && i < n) {
+        const uint32_t r = cnt[0][i] + cnt[1][i];
+        keys[r] = ki;
+        pos[r] = (uint32_t)i;
+    }
+    __syncthreads();
+}
+
+template <typename T, int VEC, typename I, bool TINY>
+__global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride,
+                                                                SumShape sh, Dest d, const I* __restrict__ idx,
+                                                                int64_t skip)
+{
+    constexpr int kT = TINY ? 1024 : 256;
+    __shared__ float heads[kT * VEC];
+    __shared__ uint8_t on_from[kT];   // per team: its head's run goes on behind what is added so far
     const uint32_t sums = sh.blocks * sh.slabs;
     if (blockIdx.x >= sums) {
-        clear_unused(sh, d, ((int64_t)(blockIdx.x - sums) * 4 + (threadIdx.x >> 6)) * sh.zero_rows);
+        const int64_t v0 = ((int64_t)(blockIdx.x - sums) * (kT / 64) + (threadIdx.x >> 6)) * sh.zero_rows;
+        clear_rows(sh, d, v0, TINY ? unnamed_rows(sh, idx, skip, v0) : unused_rows(sh, v0));
         return;
     }
+    const uint32_t *keys = sh.keys, *pos = sh.pos;
+    if constexpr (TINY) {
+        __shared__ uint32_t tk[kTiny], tp[kTiny];
+        sort_tiny(idx, (int)sh.n, sh.rows, skip, tk, tp);
+        keys = tk;
+        pos = tp;
+    }
     const uint32_t blk = blockIdx.x / sh.slabs, slab = blockIdx.x - blk * sh.slabs;
-    const int lanes = 1 << sh.lg, teams = 256 >> sh.lg;
+    const int lanes = 1 << sh.lg, teams = kT >> sh.lg;
     const int team = threadIdx.x >> sh.lg, lane = threadIdx.x & (lanes - 1);
     const uint32_t c0 = (slab * lanes + lane) * VEC;
     const bool on = c0 < sh.cols;                                  // this lane has columns
@@ -234,9 +313,9 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
     for (int q = 0; q < VEC; ++q) head[q] = 0.0f;
     if (s < e) {
         // the lists are padded to whole batches
-        auto k = gst::load<uint32_t, kBatch>(sh.keys + s);
-        auto p = gst::load<uint32_t, kBatch>(sh.pos + s);
-        const uint32_t before = s > 0 ? sh.keys[s - 1] : sh.rows, after = e < sh.n ? sh.keys[e] : sh.rows;
+        auto k = gst::load<uint32_t, kBatch>(keys + s);
+        auto p = gst::load<uint32_t, kBatch>(pos + s);
+        const uint32_t before = s > 0 ? keys[s - 1] : sh.rows, after = e < sh.n ? keys[e] : sh.rows;
         cur = k.v[0];
         const bool from = before == cur;
         bool in_first = true;
@@ -256,8 +335,8 @@ __global__ __launch_bounds__(256) void k_embed_sum(const T* __restrict__ dout, i
                 x[b] = gst::load<T, VEC>(col + (int64_t)r * dstride);
             }
             const int64_t jn = min(j + kBatch, (e - 1) / kBatch * kBatch);   // the last batch again at the end
-            k = gst::load<uint32_t, kBatch>(sh.keys + jn);
-            p = gst::load<uint32_t, kBatch>(sh.pos + jn);
+            k = gst::load<uint32_t, kBatch>(keys + jn);
+            p = gst::load<uint32_t, kBatch>(pos + jn);
             if (kk[kBatch - 1] == cur) {   // keys ascend: all of the batch
 #pragma unroll
                 for (int b = 0; b < kBatch; ++b) {
@@ -445,11 +524,16 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     if (rows == 0 || cols == 0 || (n == 0 && accumulate)) return GS_OK;
     // the split: columns per lane (16 bytes of dout, or fewer in narrow
     // rows), lanes per team, positions per team
-    const int most = dout->type == GS_F32 ? 4 : 8;
-    int vec = 1;
-    while (2 * vec <= most && 2 * vec <= cols) vec *= 2;
-    int lg = 0;
-    while (lg < 6 && (int64_t)vec << lg < cols) ++lg;
+    int vec = 1, lg = 0;
+    auto split = [&](int most) {
+        for (vec = 1; 2 * vec <= most && 2 * vec <= cols;) vec *= 2;
+        for (lg = 0; lg < 6 && (int64_t)vec << lg < cols;) ++lg;
+    };
+    // few positions: one block of 1024 threads, whose registers hold packs of
+    // four values
+    split(4);
+    const bool tiny = n > 0 && n <= std::min<int64_t>(kTiny, kBatch * (1024 >> lg));
+    if (!tiny) split(dout->type == GS_F32 ? 4 : 8);
     const int64_t slabs = ceil_div(cols, (int64_t)vec << lg);
     // sixteen wavefronts for each compute unit, in chunks of 8 to 256 positions
     const int64_t want = (n * slabs << lg) / (64 * 16 * (int64_t)ctx->num_cu);
@@ -460,11 +544,15 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     sh.lg = lg;
     sh.chunk = (int)std::min<int64_t>(256, std::max<int64_t>(kBatch, want / kBatch * kBatch));
     sh.per_block = (int64_t)sh.chunk * (256 >> lg);
+    if (tiny) {
+        sh.chunk = kBatch;
+        sh.per_block = (int64_t)kBatch * (1024 >> lg);
+    }
     const int64_t blocks = ceil_div(n, sh.per_block);
     // a wavefront clears about 64 KB
     const int64_t row_bytes = cols * (dtable->type == GS_F32 ? 4 : 2);
     sh.zero_rows = (int)std::min<int64_t>(64, std::max<int64_t>(1, 65536 / row_bytes));
-    const int64_t clear = accumulate ? 0 : ceil_div(rows, 4 * (int64_t)sh.zero_rows);
+    const int64_t clear = accumulate ? 0 : ceil_div(rows, (tiny ? 16 : 4) * (int64_t)sh.zero_rows);
     if (blocks * slabs + clear > 0x7FFFFFFF || slabs > 65535)
         return gs_fail(ctx, GS_ERR_OVERFLOW, "table gradient of %lld rows of %lld values", (long long)rows,
                        (long long)cols);
@@ -472,14 +560,14 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     sh.slabs = (uint32_t)slabs;
 
     GsGroups groups;
-    gs_status st = launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, true);
+    gs_status st = tiny ? GS_OK : launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, true);
     if (st != GS_OK) return st;
     if (blocks > 1) {
         sh.head = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
         sh.tail = (float*)gs_malloc(ctx, 4 * blocks * cols, GS_MEM_SCRATCH, tmp);
         if (!sh.head || !sh.tail) return GS_ERR_OOM;
     }
-    st = launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, false);
+    if (!tiny) st = launch_group(ctx, idx, idx_type, n, rows, padding, tmp, &groups, false);
     if (st != GS_OK) return st;
     sh.keys = groups.keys;
     sh.pos = groups.pos;
@@ -488,8 +576,18 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     auto sum = [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int VEC = decltype(v)::value;
-        hipLaunchKernelGGL((k_embed_sum<T, VEC>), dim3((unsigned)(blocks * slabs + clear)), dim3(256), 0, ctx->stream,
-                           (const T*)dout->data, dout->stride, sh, d);
+        auto launch = [&](auto i, auto small) {
+            using I = decltype(i);
+            constexpr bool TINY = decltype(small)::value;
+            hipLaunchKernelGGL((k_embed_sum<T, VEC, I, TINY>), dim3((unsigned)(blocks * slabs + clear)),
+                               dim3(TINY ? 1024 : 256), 0, ctx->stream, (const T*)dout->data, dout->stride, sh, d,
+                               (const I*)idx, padding);
+        };
+        if (!tiny) launch(int32_t{}, std::false_type{});
+        else if constexpr (VEC <= 4) {
+            if (idx_type == GS_I32) launch(int32_t{}, std::true_type{});
+            else launch(int64_t{}, std::true_type{});
+        }
         if (blocks > 1)
             hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)(blocks - 1), (unsigned)slabs), dim3(256), 0,
                                ctx->stream, sh, d);

@@ -698,3 +698,12 @@ def test_lists_of_many_column_views(ctx):
         c = 0.5 * norm / (norm + 1e-6)
         close(out[:, 0:140:2], f64(wide[:, 0:140:2]) * c, 5 * u * np.abs(f64(wide[:, 0:140:2]) * c))
         assert torch.equal(out[:, 1:140:2], wide[:, 1:140:2])
+
+
+@pytest.mark.parametrize("n", [8, 9, 64, 127, 128, 129, 255, 256, 257, 511, 512, 513])
+@pytest.mark.parametrize("w", [1, 3, 48, 300])
+def test_gradient_of_few_positions(ctx, n, w):
+    """Around the sizes that one block sums, with rows to clear beside them."""
+    for kind in ("one", "zipf", "masked"):
+        check_gradient(ctx, n, 700, w, kind, "bf16" if n % 2 else "f32", "f32", "i64" if w == 3 else "i32", padding=5)
+    check_gradient(ctx, n, 70, w, "uniform", "f32", "bf16", accumulate=True)
