@@ -87,6 +87,17 @@ __global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, 
 // sums over chunks of sorted positions, and zeros in the rows without a
 // position; (3) the runs that cross blocks joined.
 
+// the index list, for the sums that sort it themselves
+struct Index {
+    const void* p;
+    int64_t skip;
+    int type;
+    __device__ __forceinline__ uint32_t row(int64_t i, uint32_t rows) const
+    {
+        return type == GS_I32 ? row_of((const int32_t*)p, i, rows, skip) : row_of((const int64_t*)p, i, rows, skip);
+    }
+};
+
 // How (2) and (3) split the sorted positions and the columns.  A team of
 // `1 << lg` lanes, each holding VEC neighbouring columns (16 bytes), adds up
 // the rows of `chunk` positions; a block's 256 >> lg teams take neighbouring
@@ -113,33 +124,29 @@ struct Dest {
     float scale;
 };
 
-// the columns [c0, c1) of row v: scale s (+ old), rounded once
-template <int VEC>
-__device__ __forceinline__ void put_row(const Dest& d, uint32_t v, uint32_t c0, uint32_t cb, uint32_t cols,
-                                        const float* s)
+// This lane's columns of row v: scale s (+ old), rounded once.  The last lane
+// of a row whose width is no multiple of VEC loads and sums some columns of the
+// lane before it (cb < c0): it stores them too, the same bits, but does not add
+// them to the old values a second time.
+template <typename O, int VEC>
+__device__ __forceinline__ void put_row(const Dest& d, uint32_t v, uint32_t c0, uint32_t cb, const float* s)
 {
-    auto put = [&](auto* base) {
-        using O = std::remove_pointer_t<decltype(base)>;
-        O* o = base + (int64_t)v * d.stride;
-        if (cb == c0) {
-            gst::Pack<O, VEC> r;
-            if (d.accumulate) r = gst::load<O, VEC>(o + c0);
+    O* o = (O*)d.p + (int64_t)v * d.stride + cb;
+    gst::Pack<O, VEC> r;
+    if (!d.accumulate) {
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                r.v[e] = narrow<O>(d.accumulate ? (float)r.v[e] + d.scale * s[e] : d.scale * s[e]);
-            gst::store<O, VEC>(o + c0, r);
-        } else {   // the last lane of a row whose width is no multiple of VEC: its own columns only
+        for (int e = 0; e < VEC; ++e) r.v[e] = narrow<O>(d.scale * s[e]);
+        gst::store<O, VEC>(o, r);
+    } else if (cb == c0) {
+        r = gst::load<O, VEC>(o);
 #pragma unroll
-            for (int e = 0; e < VEC; ++e)
-                if (cb + e >= c0) {
-                    const float x = d.scale * s[e];
-                    o[cb + e] = narrow<O>(d.accumulate ? (float)o[cb + e] + x : x);
-                }
-        }
-    };
-    if (d.type == GS_F32) put((float*)d.p);
-    else if (d.type == GS_F16) put((gst::f16*)d.p);
-    else put((gst::bf16*)d.p);
+        for (int e = 0; e < VEC; ++e) r.v[e] = narrow<O>((float)r.v[e] + d.scale * s[e]);
+        gst::store<O, VEC>(o, r);
+    } else {
+#pragma unroll
+        for (int e = 0; e < VEC; ++e)
+            if (cb + e >= c0) o[e] = narrow<O>((float)o[e] + d.scale * s[e]);
+    }
 }
 
 // the same columns of a row of f32 partials
@@ -178,14 +185,12 @@ __device__ __forceinline__ uint64_t unused_rows(const SumShape& sh, int64_t v0)
 }
 
 // The same from a short list of indices: the lanes read all of them.
-template <typename I>
-__device__ __forceinline__ uint64_t unnamed_rows(const SumShape& sh, const I* __restrict__ idx, int64_t skip,
-                                                 int64_t v0)
+__device__ __forceinline__ uint64_t unnamed_rows(const SumShape& sh, const Index& idx, int64_t v0)
 {
     const int lane = threadIdx.x & 63;
     uint64_t named = 0;
     for (int64_t j = lane; j < sh.n; j += 64) {
-        const uint32_t r = row_of(idx, j, sh.rows, skip);
+        const uint32_t r = idx.row(j, sh.rows);
         const int64_t rel = (int64_t)r - v0;
         if (r < sh.rows && rel >= 0 && rel < 64) named |= 1ull << rel;
     }
@@ -237,15 +242,13 @@ __device__ __forceinline__ void clear_rows(const SumShape& sh, const Dest& d, in
 // batch per team.  The block sorts them itself, by counting as in group.hip, so
 // that a small gradient is one launch.
 constexpr int kBatch = 8, kTiny = 512;
-template <typename I>
-__device__ __forceinline__ void sort_tiny(const I* __restrict__ idx, int n, uint32_t rows, int64_t skip,
-                                          uint32_t* keys, uint32_t* pos)
+__device__ __forceinline__ void sort_tiny(const Index& idx, int n, uint32_t rows, uint32_t* keys, uint32_t* pos)
 {
     __shared__ uint4 raw4[kTiny / 4];
     __shared__ uint32_t cnt[2][kTiny];
     uint32_t* raw = reinterpret_cast<uint32_t*>(raw4);
     const int t = threadIdx.x, i = t % kTiny, half = t / kTiny, i0 = i & ~63;   // 1024 threads: two per position
-    if (half == 0) raw[i] = i < n ? row_of(idx, i, rows, skip) : 0xFFFFFFFFu;
+    if (half == 0) raw[i] = i < n ? idx.row(i, rows) : 0xFFFFFFFFu;
     __syncthreads();
     const uint32_t ki = raw[i];
     const int n4 = (n + 3) / 4, q0 = half ? (n4 + 1) / 2 : 0, q1 = half ? n4 : (n4 + 1) / 2;
@@ -277,10 +280,9 @@ __device__ __forceinline__ void sort_tiny(const I* __restrict__ idx, int n, uint
     __syncthreads();
 }
 
-template <typename T, int VEC, typename I, bool TINY>
+template <typename T, typename O, int VEC, bool TINY>
 __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __restrict__ dout, int64_t dstride,
-                                                                SumShape sh, Dest d, const I* __restrict__ idx,
-                                                                int64_t skip)
+                                                                SumShape sh, Dest d, Index idx)
 {
     constexpr int kT = TINY ? 1024 : 256;
     __shared__ float heads[kT * VEC];
@@ -288,13 +290,13 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
     const uint32_t sums = sh.blocks * sh.slabs;
     if (blockIdx.x >= sums) {
         const int64_t v0 = ((int64_t)(blockIdx.x - sums) * (kT / 64) + (threadIdx.x >> 6)) * sh.zero_rows;
-        clear_rows(sh, d, v0, TINY ? unnamed_rows(sh, idx, skip, v0) : unused_rows(sh, v0));
+        clear_rows(sh, d, v0, TINY ? unnamed_rows(sh, idx, v0) : unused_rows(sh, v0));
         return;
     }
     const uint32_t *keys = sh.keys, *pos = sh.pos;
     if constexpr (TINY) {
         __shared__ uint32_t tk[kTiny], tp[kTiny];
-        sort_tiny(idx, (int)sh.n, sh.rows, skip, tk, tp);
+        sort_tiny(idx, (int)sh.n, sh.rows, tk, tp);
         keys = tk;
         pos = tp;
     }
@@ -345,28 +347,24 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
                 }
                 continue;
             }
-            // one run of the batch after the other
-            for (;;) {
-                uint32_t next = sh.rows;
 #pragma unroll
-                for (int b = 0; b < kBatch; ++b) {
-                    const bool take = kk[b] == cur;
+            for (int b = 0; b < kBatch; ++b) {
+                if (kk[b] >= sh.rows) continue;
+                if (kk[b] != cur) {   // the run of `cur` ends here
+                    if (in_first && from) {
+                        has_head = true;
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) acc[q] += take ? (float)x[b].v[q] : 0.0f;
-                    next = min(next, kk[b] > cur ? kk[b] : sh.rows);
+                        for (int q = 0; q < VEC; ++q) head[q] = acc[q];
+                    } else if (on) {
+                        put_row<O, VEC>(d, cur, c0, cb, acc);
+                    }
+                    in_first = false;
+                    cur = kk[b];
+#pragma unroll
+                    for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
                 }
-                if (next == sh.rows) break;
-                if (in_first && from) {
-                    has_head = true;
 #pragma unroll
-                    for (int q = 0; q < VEC; ++q) head[q] = acc[q];
-                } else if (on) {
-                    put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
-                }
-                in_first = false;
-                cur = next;
-#pragma unroll
-                for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
+                for (int q = 0; q < VEC; ++q) acc[q] += (float)x[b].v[q];
             }
         }
         if (cur < sh.rows) {
@@ -378,7 +376,7 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
             } else if (after == cur) {
                 has_tail = true;
             } else if (on) {
-                put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+                put_row<O, VEC>(d, cur, c0, cb, acc);
             }
         }
     }
@@ -414,7 +412,7 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
             leaves = on_from[team + 1];
         }
         if (leaves) put_part<VEC>(sh.tail + (int64_t)blk * sh.cols, c0, cb, acc);
-        else put_row<VEC>(d, cur, c0, cb, sh.cols, acc);
+        else put_row<O, VEC>(d, cur, c0, cb, acc);
     }
 }
 
@@ -468,7 +466,9 @@ __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
 #pragma unroll
         for (int q = 0; q < VEC; ++q) acc[q] += part[((t << sh.lg) + lane) * VEC + q];
     }
-    put_row<VEC>(d, row, c0, cb, sh.cols, acc);
+    if (d.type == GS_F32) put_row<float, VEC>(d, row, c0, cb, acc);
+    else if (d.type == GS_F16) put_row<gst::f16, VEC>(d, row, c0, cb, acc);
+    else put_row<gst::bf16, VEC>(d, row, c0, cb, acc);
 }
 
 }  // namespace
@@ -576,18 +576,17 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     auto sum = [&](auto t, auto v) {
         using T = decltype(t);
         constexpr int VEC = decltype(v)::value;
-        auto launch = [&](auto i, auto small) {
-            using I = decltype(i);
+        auto launch = [&](auto o, auto small) {
+            using O = decltype(o);
             constexpr bool TINY = decltype(small)::value;
-            hipLaunchKernelGGL((k_embed_sum<T, VEC, I, TINY>), dim3((unsigned)(blocks * slabs + clear)),
+            hipLaunchKernelGGL((k_embed_sum<T, O, VEC, TINY>), dim3((unsigned)(blocks * slabs + clear)),
                                dim3(TINY ? 1024 : 256), 0, ctx->stream, (const T*)dout->data, dout->stride, sh, d,
-                               (const I*)idx, padding);
+                               Index{idx, padding, idx_type});
         };
-        if (!tiny) launch(int32_t{}, std::false_type{});
-        else if constexpr (VEC <= 4) {
-            if (idx_type == GS_I32) launch(int32_t{}, std::true_type{});
-            else launch(int64_t{}, std::true_type{});
-        }
+        with_type(dtable->type, [&](auto o) {
+            if (!tiny) launch(o, std::false_type{});
+            else if constexpr (VEC <= 4) launch(o, std::true_type{});
+        });
         if (blocks > 1)
             hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)(blocks - 1), (unsigned)slabs), dim3(256), 0,
                                ctx->stream, sh, d);
