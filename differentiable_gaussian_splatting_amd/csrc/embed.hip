@@ -12,11 +12,11 @@
 // The backward groups the positions i by index with a stable sort, so that
 // each row's sum runs over its positions in a fixed order and needs no
 // atomics: the result does not depend on timing.  6M x 48 f32 (rows 59 apart,
-// a quarter of them on one table row): 472 us, of which the sums take 361: a
+// a quarter of them on one table row): 472 us, of which the sums take 359: a
 // row of 192 bytes that starts anywhere touches 2.5 lines of 128 bytes, 2.0 GB
 // in all at 5.6 TB/s; the grouping takes 95 and the join 17.  16384 x 4096
-// bf16 into 32768 rows of f32: 150 us, of which the sums with the cleared rows
-// take 130 (671 MB, 5.2 TB/s).
+// bf16 into 32768 rows of f32: 146 us, of which the sums with the cleared rows
+// take 121-131 (671 MB, 5.1-5.5 TB/s).  257 x 45 f32: 9.6 us, one launch.
 #include "gs_device.h"
 #include "gs_internal.h"
 #include "gs_tensor.h"
@@ -228,7 +228,7 @@ __device__ __forceinline__ void clear_rows(const SumShape& sh, const Dest& d, in
 // more than others (a thread per table row took 645 ms with a quarter of 6M
 // positions on one).  Each team walks its chunk in batches, eight rows in
 // flight (the loads must not be behind branches: waiting for each in turn took
-// 470 us where this takes 361),
+// 470 us where this takes 359),
 // and adds rows while the table row stays the same.  A run inside the chunk is
 // written at once.  A chunk's first run, if it began before, is its head, and
 // its last, if it goes on, its tail.  After the block's teams are done, the
@@ -529,10 +529,14 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
         for (vec = 1; 2 * vec <= most && 2 * vec <= cols;) vec *= 2;
         for (lg = 0; lg < 6 && (int64_t)vec << lg < cols;) ++lg;
     };
-    // few positions: one block of 1024 threads, whose registers hold packs of
-    // four values
+    // few positions: one launch (a block of 1024 threads, whose registers hold
+    // packs of four values) instead of two, up to about 320 positions (x 4 f32:
+    // 200 positions 8.9 us against 10.4, 300 10.3 against 10.5, 384 11.3 against
+    // 10.6), or instead of three, where the other form needs a join, up to what
+    // the block holds (x 48: 200 positions 8.7 against 14.4, 512 13.4 against 14.7)
     split(4);
-    const bool tiny = n > 0 && n <= std::min<int64_t>(kTiny, kBatch * (1024 >> lg));
+    const bool joined = n > (int64_t)kBatch * (256 >> lg);
+    const bool tiny = n > 0 && n <= std::min<int64_t>(joined ? kTiny : 320, kBatch * (1024 >> lg));
     if (!tiny) split(dout->type == GS_F32 ? 4 : 8);
     const int64_t slabs = ceil_div(cols, (int64_t)vec << lg);
     // sixteen wavefronts for each compute unit, in chunks of 8 to 256 positions
