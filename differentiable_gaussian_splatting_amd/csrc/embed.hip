@@ -44,9 +44,9 @@ __device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i,
 // pack, so that a wavefront writes 1 KB of neighbouring packs (two, four and
 // eight packs in flight per thread took 261, 266 and 267 us where one takes
 // 254, 6M x 48 f32), with stores that do not stay in the L2 (336 us with plain
-// ones, which push the table out of it).  Pack k of a
-// block is in row (rem + k) / per_row from the block's first row: a product
-// with `magic` (floor(2^32 / per_row) + 1, exact for k per_row < 2^32) where
+// ones, which push the table out of it).  Pack k of a block is in row
+// (rem + k) / per_row from the block's first row: a product with `magic`
+// (floor(2^32 / per_row) + 1, exact for k per_row < 2^32) where
 // 1 < per_row < 1024, else a compare (a block then meets at most two rows).
 struct FwdShape {
     int64_t n;             // rows of out
@@ -60,7 +60,7 @@ template <typename T, typename O, typename I, int VEC>
 __global__ __launch_bounds__(256) void k_embed_fwd(const T* __restrict__ table, const I* __restrict__ idx,
                                                    O* __restrict__ out, FwdShape sh)
 {
-    const int64_t base = (int64_t)blockIdx.x * 256;
+    const int64_t base = ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * 256;
     const int64_t row0 = base / sh.per_row;
     const uint32_t k = (uint32_t)(base - row0 * sh.per_row) + threadIdx.x;
     const uint32_t r = sh.per_row == 1     ? k
@@ -228,15 +228,14 @@ __device__ __forceinline__ void clear_rows(const SumShape& sh, const Dest& d, in
 // more than others (a thread per table row took 645 ms with a quarter of 6M
 // positions on one).  Each team walks its chunk in batches, eight rows in
 // flight (the loads must not be behind branches: waiting for each in turn took
-// 470 us where this takes 359),
-// and adds rows while the table row stays the same.  A run inside the chunk is
-// written at once.  A chunk's first run, if it began before, is its head, and
-// its last, if it goes on, its tail.  After the block's teams are done, the
-// heads that belong to one run are added over the teams by doubling steps, and
-// the team in which the run begins adds its tail and writes the row, or the
-// block's piece of it (head / tail) if the run leaves the block.  Blocks after
-// those of the positions clear the unused rows, in
-// the same launch so that their stores run beside the loads.
+// 470 us where this takes 359), and adds rows while the table row stays the
+// same.  A run inside the chunk is written at once.  A chunk's first run, if
+// it began before, is its head, and its last, if it goes on, its tail.  After
+// the block's teams are done, the heads that belong to one run are added over
+// the teams by doubling steps, and the team in which the run begins adds its
+// tail and writes the row, or the block's piece of it (head / tail) if the run
+// leaves the block.  Blocks after those of the positions clear the unused
+// rows, in the same launch so that their stores run beside the loads.
 //
 // TINY: up to kTiny positions that one block of 1024 threads holds in one
 // batch per team.  The block sorts them itself, by counting as in group.hip, so
@@ -416,9 +415,10 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
     }
 }
 
-// (3) One block per border between blocks of (2), most of which end at once: if a run begins in the block
-// before it and crosses the border, its tail and the heads of the blocks after
-// it are added, the teams taking every teams-th piece, their sums in order.
+// (3) One block per border between blocks of (2), most of which end at once:
+// if a run begins in the block before it and crosses the border, its tail and
+// the heads of the blocks after it are added, the teams taking every teams-th
+// piece, their sums in order.
 template <int VEC>
 __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
 {
@@ -491,14 +491,16 @@ gs_status launch_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx,
     sh.tstride = table->stride;
     sh.ostride = out->stride;
     sh.scale = scale;
-    if (blocks > 0x7FFFFFFF) return gs_fail(ctx, GS_ERR_OVERFLOW, "lookup of %lld x %lld values", (long long)n,
-                                            (long long)cols);
+    // a launch takes fewer than 2^32 threads in x
+    const int64_t gx = std::min<int64_t>(blocks, 1 << 22), gy = ceil_div(blocks, gx);
+    if (gy > 65535)
+        return gs_fail(ctx, GS_ERR_OVERFLOW, "lookup of %lld x %lld values", (long long)n, (long long)cols);
     GsTimerScope ts(ctx, "embed_fwd");
     auto go = [&](auto t, auto o, auto i, auto v) {
         using T = decltype(t);
         using O = decltype(o);
         using I = decltype(i);
-        hipLaunchKernelGGL((k_embed_fwd<T, O, I, decltype(v)::value>), dim3((unsigned)blocks),
+        hipLaunchKernelGGL((k_embed_fwd<T, O, I, decltype(v)::value>), dim3((unsigned)gx, (unsigned)gy),
                            dim3(256), 0, ctx->stream, (const T*)table->data, (const I*)idx, (O*)out->data, sh);
     };
     with_type(table->type, [&](auto t) {
@@ -557,7 +559,7 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     const int64_t row_bytes = cols * (dtable->type == GS_F32 ? 4 : 2);
     sh.zero_rows = (int)std::min<int64_t>(64, std::max<int64_t>(1, 65536 / row_bytes));
     const int64_t clear = accumulate ? 0 : ceil_div(rows, (tiny ? 16 : 4) * (int64_t)sh.zero_rows);
-    if (blocks * slabs + clear > 0x7FFFFFFF || slabs > 65535)
+    if (blocks * slabs + clear > 0xFFFFFF || slabs > 65535)   // 2^32 threads
         return gs_fail(ctx, GS_ERR_OVERFLOW, "table gradient of %lld rows of %lld values", (long long)rows,
                        (long long)cols);
     sh.blocks = (uint32_t)blocks;

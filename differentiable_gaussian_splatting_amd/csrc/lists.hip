@@ -487,6 +487,9 @@ constexpr int64_t kLarge = 4000000, kLargePiece = 2048, kAdamPiece = 1024;
 // rows x cols values that lie one after the other
 bool dense(const gs_tensor& t) { return t.rows <= 1 || t.stride == t.cols; }
 
+// at least `piece` values per block, and fewer than 2^32 threads
+int64_t bounded(int64_t piece, int64_t total) { return std::max(piece, ceil_div(ceil_div(total, 1 << 23), 1024) * 1024); }
+
 // values per block for `total` values: about eight blocks of 256 threads per
 // compute unit, at least 1024 values
 int64_t piece_of(const gs_ctx* ctx, int64_t total)
@@ -585,7 +588,7 @@ void join_columns(const gs_tensor* in, const gs_tensor* in2, int32_t n, std::vec
     auto adjoins = [](const gs_tensor& a, const gs_tensor& b) {
         const int64_t size = a.type == GS_F32 ? 4 : 2;
         return a.type == b.type && a.rows == b.rows && a.rows > 1 && a.stride == b.stride &&
-               (char*)b.data == (char*)a.data + a.cols * size && a.cols + b.cols <= a.stride;
+               (char*)b.data == (char*)a.data + a.cols * size && a.cols + b.cols <= a.stride && a.cols + b.cols <= 0x7FFFFFFF;
     };
     for (int32_t k = 0; k < n; ++k) {
         if (in[k].rows * in[k].cols == 0) continue;
@@ -683,7 +686,7 @@ gs_status launch_clip(gs_ctx* ctx, const gs_tensor* list, int32_t count, double 
     if (large)
         hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, part, parts, max_norm, norm);
     int write = 1;   // the first launch writes the norm
-    return launch_list<ScaleJob>(ctx, in, out, n, large ? kLargePiece : piece_of(ctx, total), tmp,
+    return launch_list<ScaleJob>(ctx, in, out, n, large ? bounded(kLargePiece, total) : piece_of(ctx, total), tmp,
                                  [&](ScaleTensor& d, int32_t k) {
                                      d.p = in[k].data;
                                      d.o = out[k].data;
@@ -710,7 +713,7 @@ gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
     a.eps = (float)o->eps;
     a.keep = (float)(1.0 - o->lr * o->weight_decay);
     GsTimerScope ts(ctx, "adam_list");
-    return launch_list<AdamJob>(ctx, g, nullptr, n, kAdamPiece, tmp,
+    return launch_list<AdamJob>(ctx, g, nullptr, n, bounded(kAdamPiece, values(g, n)), tmp,
                                 [&](AdamTensor& d, int32_t k) {
                                     d.p = (float*)p[k].data;
                                     d.m = (float*)m[k].data;

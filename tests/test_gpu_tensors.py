@@ -151,6 +151,25 @@ def test_offsets_past_32_bits(ctx):
     assert d[0].eq(2.0).all() and d[1].eq(5.0).all()
 
 
+def test_output_of_more_than_one_launch_row(ctx):
+    """36e9 values of bf16: more packs than a launch has threads in x."""
+    torch = _t()
+    n, w = 1_100_000, 32_768
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 72 GB of free device memory")
+    table = torch.zeros((3, w), dtype=torch.bfloat16, device="cuda")
+    table[1], table[2] = 1.0, 2.0
+    idx = (torch.arange(n, device="cuda") % 3).int()
+    out = torch.empty((n, w), dtype=torch.bfloat16, device="cuda")
+    B.gs_embed_fwd(ctx, table, idx, out)
+    for a in range(0, n, 100_000):
+        part = out[a:a + 100_000]
+        want = idx[a:a + 100_000].float()
+        assert torch.equal(part.amax(1).float(), want) and torch.equal(part.amin(1).float(), want)
+    del out
+    torch.cuda.empty_cache()
+
+
 # ---------------------------------------------------------------------------- its gradient
 
 def table_gradient(i, x, v, padding):
