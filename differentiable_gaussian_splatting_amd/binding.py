@@ -500,9 +500,10 @@ def _type_code(dtype):
 def _tensor_fields(t, device=None):
     """data, rows, cols, stride and type of a device tensor's gs_tensor: a 2-D tensor with unit column stride
     (rows may be apart, or one row broadcast), or a contiguous tensor of any other shape, taken as one row."""
-    if not t.is_cuda or (device is not None and t.get_device() != device.index):
+    at = t.get_device()   # -1: not a GPU
+    if at < 0 or (device is not None and at != device.index):
         raise ValueError(f"a tensor on {t.device}: expected {device or 'a GPU'}")
-    code = _type_code(t.dtype)
+    code = _type_codes.get(t.dtype, -1) if _type_codes else _type_code(t.dtype)
     if code < 0 or code > GS_BF16:
         raise ValueError(f"element type {t.dtype}: expected float32, float16 or bfloat16")
     if t.dim() == 2:
@@ -559,7 +560,7 @@ def _as_list(tensors, ctx):
 
 def _index(idx, ctx):
     code = _type_code(idx.dtype)
-    if code < GS_I32 or not idx.is_cuda or idx.get_device() != ctx.device.index or not idx.is_contiguous():
+    if code < GS_I32 or idx.get_device() != ctx.device.index or not idx.is_contiguous():
         raise ValueError("indices must be a contiguous int32 or int64 tensor on the context's device")
     return code
 
@@ -576,7 +577,7 @@ def _two_tensors(ctx, a, b):
 
 
 def _norm_ptr(norm, ctx):
-    if not norm.is_cuda or norm.get_device() != ctx.device.index or _type_code(norm.dtype) != GS_F32 or norm.numel() < 2 or not norm.is_contiguous():
+    if norm.get_device() != ctx.device.index or _type_code(norm.dtype) != GS_F32 or norm.numel() < 2 or not norm.is_contiguous():
         raise ValueError("norm must be a float32 tensor of two values on the context's device")
     return norm.data_ptr()
 

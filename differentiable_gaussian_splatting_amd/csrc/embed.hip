@@ -12,10 +12,10 @@
 // The backward groups the positions i by index with a stable sort, so that
 // each row's sum runs over its positions in a fixed order and needs no
 // atomics: the result does not depend on timing.  6M x 48 f32 (rows 59 apart,
-// a quarter of them on one table row): 472 us, of which the sums take 359: a
+// a quarter of them on one table row): 465 us, of which the sums take 359: a
 // row of 192 bytes that starts anywhere touches 2.5 lines of 128 bytes, 2.0 GB
-// in all at 5.6 TB/s; the grouping takes 95 and the join 17.  16384 x 4096
-// bf16 into 32768 rows of f32: 146 us, of which the sums with the cleared rows
+// in all at 5.6 TB/s; the grouping takes 95 and the join 12.  16384 x 4096
+// bf16 into 32768 rows of f32: 145 us, of which the sums with the cleared rows
 // take 121-131 (671 MB, 5.1-5.5 TB/s).  257 x 45 f32: 9.6 us, one launch.
 #include "gs_device.h"
 #include "gs_internal.h"
@@ -450,10 +450,26 @@ __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
 #pragma unroll
     for (int q = 0; q < VEC; ++q) acc[q] = 0.0f;
     if (on) {
-#pragma unroll 4
-        for (int64_t t = team; t <= m; t += teams) {   // piece 0: the tail
-            const float* src = t == 0 ? sh.tail + b * sh.cols : sh.head + (b + t) * sh.cols;
-            const auto x = gst::load<float, VEC>(src + cb);
+        // piece 0 is the tail, piece t the head of block b + t; eight in flight
+        const float* heads = sh.head + b * sh.cols + cb;
+        if (team == 0) {
+            const auto x = gst::load<float, VEC>(sh.tail + b * sh.cols + cb);
+#pragma unroll
+            for (int q = 0; q < VEC; ++q) acc[q] = x.v[q];
+        }
+        int64_t t = team == 0 ? teams : team;
+        for (; t + 7 * teams <= m; t += 8 * teams) {
+            gst::Pack<float, VEC> x[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) x[u] = gst::load<float, VEC>(heads + (t + u * teams) * sh.cols);
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+#pragma unroll
+                for (int q = 0; q < VEC; ++q) acc[q] += x[u].v[q];
+            }
+        }
+        for (; t <= m; t += teams) {
+            const auto x = gst::load<float, VEC>(heads + t * sh.cols);
 #pragma unroll
             for (int q = 0; q < VEC; ++q) acc[q] += x.v[q];
         }

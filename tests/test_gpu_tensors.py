@@ -720,7 +720,7 @@ def test_lists_of_many_column_views(ctx):
 
 
 @pytest.mark.parametrize("n", [8, 9, 64, 127, 128, 129, 255, 256, 257, 511, 512, 513])
-@pytest.mark.parametrize("w", [1, 3, 48, 300])
+@pytest.mark.parametrize("w", [1, 3, 48, 257, 300])
 def test_gradient_of_few_positions(ctx, n, w):
     """Around the sizes that one block sums, with rows to clear beside them."""
     for kind in ("one", "zipf", "masked"):
