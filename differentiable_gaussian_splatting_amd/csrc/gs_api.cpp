@@ -1896,10 +1896,13 @@ gs_status gs_train_view(gs_ctx* ctx, const gs_camera* cam, const gs_params* para
         if (!grad3d || (clip && !norm)) { st = GS_ERR_OOM; goto done; }
         if ((st = gs_project_bwd(ctx, cam, params, proj, grad2d, grad3d)) != GS_OK) goto done;
         if (clip) {
+            // without clip_norm the norm alone: a gradient that is not finite
+            // somewhere has the factor 0 or NaN, which must scale nothing
             const gs_tensor g{grad3d, n_cand, F, F, GS_F32, 0};
-            const double limit = opts->clip_norm > 0.0f ? (double)opts->clip_norm
-                                                        : std::numeric_limits<double>::infinity();
-            if ((st = launch_clip(ctx, &g, 1, limit, &g, norm, &view)) != GS_OK) goto done;
+            st = opts->clip_norm > 0.0f
+                     ? launch_clip(ctx, &g, 1, (double)opts->clip_norm, &g, norm, &view)
+                     : launch_grad_norm(ctx, &g, 1, std::numeric_limits<double>::infinity(), norm, &view);
+            if (st != GS_OK) goto done;
         }
         if (opts->grad3d_out && (st = launch_scatter_grad3d(ctx, proj, F, grad3d, opts->grad3d_out)) != GS_OK)
             goto done;

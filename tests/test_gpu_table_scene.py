@@ -123,3 +123,35 @@ def test_a_clipped_view_that_cannot_allocate_changes_nothing():
     torch.cuda.synchronize()
     assert k > 3 and f.mem_stats()["live"] == live and not torch.equal(old[0], ds.means)
     f.close()
+
+
+def _broken_view(ctx, **kw):
+    """A first update of a view whose gradient is not finite for some of its Gaussians (a pixel of the target is
+    NaN); returns the scene's tensors before and after, the moments, and the dense gradient."""
+    import torch
+    w = scenes.make_workload("c2_hd", n=4000, width=200, height=120, posed=True, seed=12)
+    target = torch.from_numpy(w.target).cuda()
+    target[:, 40, 60] = float("nan")
+    ds = B.DeviceScene(w.scene)
+    m, v = B.like_scene(ds), B.like_scene(ds)
+    old = [t.clone() for t in ds.tensors()]
+    g3 = torch.zeros((4000, 59), device="cuda")
+    B.gs_train_view(ctx, w.camera, ds, target, loss="l1_ssim", grad3d_out=g3,
+                    adam=dict(step=1, params=ds, m=m, v=v, lr=1e-3), **kw)
+    return old, ds.tensors(), m.tensors() + v.tensors(), g3
+
+
+def test_asking_for_the_norm_leaves_a_view_as_it_is(ctx):
+    """norm_out without clip_norm scales nothing, also where a Gaussian's gradient is not finite: its neighbours
+    are updated as without norm_out."""
+    import torch
+    _, new0, _, g0 = _broken_view(ctx)
+    bad = ~g0.isfinite()
+    assert 0 < int(bad.sum()) < bad.numel() // 2
+    norm = torch.zeros(2, device="cuda")
+    _, new1, _, g1 = _broken_view(ctx, norm_out=norm)
+    assert torch.equal(~g1.isfinite(), bad)
+    assert rel_l2(g1[~bad].cpu().numpy(), g0[~bad].cpu().numpy()) <= 1e-4
+    for a, b in zip(new0, new1):
+        assert torch.equal(a.isfinite(), b.isfinite())
+    assert not norm.isfinite().any()
