@@ -84,8 +84,10 @@ __device__ __forceinline__ void adam_group(const AdamGroup& gr, int blk, int nbl
 template <int DEG>
 __global__ __launch_bounds__(256) void k_adam(uint32_t n, int64_t n_cand, const uint32_t* __restrict__ ids,
                                               int64_t s0, int64_t s1, const int32_t* __restrict__ slot_of,
-                                              const float* __restrict__ grad3d, AdamJob job, AdamArgs a)
+                                              const float* __restrict__ grad3d, AdamJob job, AdamArgs a,
+                                              const float* __restrict__ norm)
 {
+    if (norm && !(fabsf(norm[0]) < __builtin_inff())) return;   // a clipped gradient without a finite norm
     constexpr int F = 11 + 3 * (DEG + 1) * (DEG + 1);
     const uint32_t g0 = s0 == 0 ? 0u : ids[s0];
     const uint32_t g1 = s1 >= n_cand ? n : ids[s1];
@@ -118,7 +120,7 @@ __global__ __launch_bounds__(256) void k_scatter(int64_t n, int F, const int32_t
 
 gs_status launch_adam(gs_ctx* ctx, const gs_proj* proj, int64_t n, int sh_degree, const gs_param_ptrs* p,
                       const gs_param_ptrs* m, const gs_param_ptrs* v, const float* grad3d, int64_t s0, int64_t s1,
-                      int32_t step, float lr, float b1, float b2, float eps)
+                      int32_t step, float lr, float b1, float b2, float eps, const float* norm)
 {
     const int K = (sh_degree + 1) * (sh_degree + 1);
     const AdamArgs a = gsd::adam_args(step, lr, b1, b2, eps);
@@ -143,7 +145,7 @@ gs_status launch_adam(gs_ctx* ctx, const gs_proj* proj, int64_t n, int sh_degree
         job.bend[q] = total;
     }
 #define GS_ADAM(D) hipLaunchKernelGGL(k_adam<D>, dim3((unsigned)total), dim3(256), 0, ctx->stream, (uint32_t)n, \
-                                      proj->n_cand, proj->ids, s0, s1, proj->slot_of, grad3d, job, a)
+                                      proj->n_cand, proj->ids, s0, s1, proj->slot_of, grad3d, job, a, norm)
     switch (sh_degree) {
     case 0: GS_ADAM(0); break;
     case 1: GS_ADAM(1); break;

@@ -1906,9 +1906,13 @@ gs_status gs_train_view(gs_ctx* ctx, const gs_camera* cam, const gs_params* para
         }
         if (opts->grad3d_out && (st = launch_scatter_grad3d(ctx, proj, F, grad3d, opts->grad3d_out)) != GS_OK)
             goto done;
+        // a clipped view whose norm is not finite leaves its update out, as
+        // gs_adam_tensors does: scaled by 0 or NaN it would put NaN into
+        // every parameter
         if (opts->adam_step > 0 &&
-            (st = gs_adam_step(ctx, proj, params->n, params->sh_degree, opts->params_rw, opts->adam_m, opts->adam_v,
-                               grad3d, opts->adam_step, opts->lr, opts->beta1, opts->beta2, opts->eps)) != GS_OK)
+            (st = launch_adam(ctx, proj, params->n, params->sh_degree, opts->params_rw, opts->adam_m, opts->adam_v,
+                              grad3d, 0, proj->n_cand, opts->adam_step, opts->lr, opts->beta1, opts->beta2, opts->eps,
+                              opts->clip_norm > 0.0f ? norm : nullptr)) != GS_OK)
             goto done;
     } else if (opts->adam_chunk <= 0) {
         // projection backward fused with the update over all Gaussians

@@ -341,10 +341,11 @@ gs_status ssim_static_buffers(gs_ctx* ctx, int W, int H, SsimStatic* out);
 
 // adam.hip
 // Adam over the Gaussians whose candidates are the slots [s0, s1), with their
-// gradient rows in grad3d (row s - s0); [0, n_cand) covers every Gaussian
+// gradient rows in grad3d (row s - s0); [0, n_cand) covers every Gaussian.
+// norm (device, or null): nothing is changed when norm[0] is not finite
 gs_status launch_adam(gs_ctx* ctx, const gs_proj* proj, int64_t n, int sh_degree, const gs_param_ptrs* p,
                       const gs_param_ptrs* m, const gs_param_ptrs* v, const float* grad3d, int64_t s0, int64_t s1,
-                      int32_t step, float lr, float b1, float b2, float eps);
+                      int32_t step, float lr, float b1, float b2, float eps, const float* norm = nullptr);
 gs_status launch_scatter_grad3d(gs_ctx* ctx, const gs_proj* proj, int F, const float* grad3d, float* dense);
 // projection backward of the candidates fused with one Adam step over all N
 // Gaussians (no gradient array); p: the parameters the backward reads, pr /

@@ -550,11 +550,14 @@ typedef struct {
     float clip_norm;             /* > 0: the view's whole gradient is scaled   */
     int32_t pad;                 /* by min(1, clip_norm / (norm + 1e-6)) as by */
     float* norm_out;             /* gs_clip_grads before grad3d_out and the    */
-                                 /* update; 0: it is not.  norm_out: device,   */
-                                 /* nullable: norm and factor (two floats) are */
-                                 /* written there.  With either, the compact   */
-                                 /* gradient (n_cand x F) is held whole and    */
-                                 /* adam_chunk is not used                     */
+                                 /* update, which is left out when the norm is */
+                                 /* not finite; 0: it is not.  norm_out:       */
+                                 /* device, nullable: norm and factor (two     */
+                                 /* floats) are written there, the factor 1    */
+                                 /* without clip_norm unless the norm is not   */
+                                 /* finite.  With either, the compact gradient */
+                                 /* (n_cand x F) is held whole and adam_chunk  */
+                                 /* is not used                                */
 } gs_view_opts;
 
 typedef struct {

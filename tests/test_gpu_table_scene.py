@@ -155,3 +155,14 @@ def test_asking_for_the_norm_leaves_a_view_as_it_is(ctx):
     for a, b in zip(new0, new1):
         assert torch.equal(a.isfinite(), b.isfinite())
     assert not norm.isfinite().any()
+
+
+def test_clipped_view_leaves_an_update_out_whose_norm_is_not_finite(ctx):
+    import torch
+    for norm in (torch.zeros(2, device="cuda"), None):
+        old, new, moments, _ = _broken_view(ctx, clip_norm=1.0, norm_out=norm)
+        for a, b in zip(old, new):
+            assert torch.equal(a, b)
+        for t in moments:
+            assert t.eq(0.0).all()
+        assert norm is None or not norm[0].isfinite()
