@@ -1883,7 +1883,13 @@ gs_status gs_train_view(gs_ctx* ctx, const gs_camera* cam, const gs_params* para
         result->gate_backward = d.backward;
         result->gate_forced = d.forced;
         result->gate_score = d.score;
-        if (!d.backward) goto finish;
+        if (!d.backward) {
+            // no gradient: the norm 0, and the factor 1
+            if (opts->norm_out && ((st = launch_fill_f32(ctx, opts->norm_out, 0.0f, 1)) != GS_OK ||
+                                   (st = launch_fill_f32(ctx, opts->norm_out + 1, 1.0f, 1)) != GS_OK))
+                goto done;
+            goto finish;
+        }
     }
     if ((st = render_leaves(ctx, cam, proj, target, opts, leaves, true, grad2d, l1_view, image, loss_dev + 1,
                             &isect_total, walk, &walk_used)) != GS_OK)

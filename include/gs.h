@@ -555,9 +555,10 @@ typedef struct {
                                  /* device, nullable: norm and factor (two     */
                                  /* floats) are written there, the factor 1    */
                                  /* without clip_norm unless the norm is not   */
-                                 /* finite.  With either, the compact gradient */
-                                 /* (n_cand x F) is held whole and adam_chunk  */
-                                 /* is not used                                */
+                                 /* finite; 0 and 1 for a view whose backward  */
+                                 /* the gate skips.  With either, the compact  */
+                                 /* gradient (n_cand x F) is held whole and    */
+                                 /* adam_chunk is not used                     */
 } gs_view_opts;
 
 typedef struct {

@@ -166,3 +166,24 @@ def test_clipped_view_leaves_an_update_out_whose_norm_is_not_finite(ctx):
         for t in moments:
             assert t.eq(0.0).all()
         assert norm is None or not norm[0].isfinite()
+
+
+def test_a_view_that_the_gate_skips_has_norm_zero(ctx):
+    """A gate runs the backward of some views of a sequence and skips others: norm and factor are those of
+    this view, never of one before it."""
+    import torch
+    w = scenes.make_workload("c1_small", n=300, width=64, height=48, seed=3, sh_degree=1)
+    target = torch.from_numpy(w.target).cuda()
+    ds = B.DeviceScene(w.scene)
+    gate = B.Gate(1, warmup=1)
+    seen = set()
+    for k, f in enumerate([1.0, 1.3, 0.7, 0.6, 1.4, 0.5, 0.45, 0.4]):
+        norm = torch.full((2,), 7.0, device="cuda")
+        r = B.gs_train_view(ctx, w.camera, ds, target * f, gate=gate, gate_view=0, clip_norm=1e-3, norm_out=norm)
+        seen.add(r["backward"])
+        if r["backward"]:
+            assert norm[0] > 0.0 and norm[1] <= 1.0 and float(norm[0]) != 7.0
+        else:
+            assert norm.tolist() == [0.0, 1.0], k
+    assert seen == {True, False}
+    gate.close()
