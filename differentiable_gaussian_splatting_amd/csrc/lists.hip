@@ -512,29 +512,46 @@ int64_t pieces(const gs_tensor* t, int32_t n, int64_t piece)
     return s;
 }
 
-// Hands a list to a kernel: put(descriptor, tensor index) fills in the
-// pointers, go(job or table, blocks) launches, once or twice.  in, out: the
-// tensors whose rows may be apart (out may be null).
-template <typename J, typename P, typename G>
-gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, int64_t piece,
-                      std::vector<GsAlloc>* tmp, P&& put, G&& go)
+bool is_apart(const gs_tensor* in, const gs_tensor* out, int32_t k)
+{
+    return !dense(in[k]) || (out && !dense(out[k]));
+}
+
+// The device table of a list that gets one (see Table), else nothing.  Taken
+// apart from launch_list, so that a call has all its memory before its first
+// launch writes anything.
+template <typename J>
+struct ListMemory {
+    typename J::Tensor* t = nullptr;
+    Apart* apart = nullptr;
+};
+
+template <typename J>
+gs_status take_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, std::vector<GsAlloc>* tmp,
+                    ListMemory<J>* mem)
 {
     typedef typename J::Tensor T;
-    auto is_apart = [&](int32_t k) { return !dense(in[k]) || (out && !dense(out[k])); };
     int64_t count = 0, aparts = 0, total = 0;
     for (int32_t k = 0; k < n; ++k)
         if (in[k].rows * in[k].cols > 0) {
             total += in[k].rows * in[k].cols;
             ++count;
-            aparts += is_apart(k);
+            aparts += is_apart(in, out, k);
         }
-    T* table = nullptr;
-    Apart* table_apart = nullptr;
-    if (total > kLarge && aparts <= 0x7FFF && (count > 3 * J::kCap || aparts > 3 * kApart)) {
-        table = (T*)gs_malloc(ctx, sizeof(T) * count, GS_MEM_SCRATCH, tmp);
-        table_apart = (Apart*)gs_malloc(ctx, sizeof(Apart) * std::max<int64_t>(aparts, 1), GS_MEM_SCRATCH, tmp);
-        if (!table || !table_apart) return GS_ERR_OOM;
-    }
+    if (total <= kLarge || aparts > 0x7FFF || (count <= 3 * J::kCap && aparts <= 3 * kApart)) return GS_OK;
+    mem->t = (T*)gs_malloc(ctx, sizeof(T) * count, GS_MEM_SCRATCH, tmp);
+    mem->apart = (Apart*)gs_malloc(ctx, sizeof(Apart) * std::max<int64_t>(aparts, 1), GS_MEM_SCRATCH, tmp);
+    return mem->t && mem->apart ? GS_OK : GS_ERR_OOM;
+}
+
+// Hands a list to a kernel: put(descriptor, tensor index) fills in the
+// pointers, go(job or table, blocks) launches, once or twice.  in, out: the
+// tensors whose rows may be apart (out may be null).  Allocates nothing.
+template <typename J, typename P, typename G>
+gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, int64_t piece,
+                      const ListMemory<J>& mem, P&& put, G&& go)
+{
+    typedef typename J::Tensor T;
     J job;
     job.piece = piece;
     job.count = job.aparts = 0;
@@ -542,9 +559,9 @@ gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, in
     int32_t at = 0, at_apart = 0;   // table entries filled
     auto flush = [&]() {
         if (job.count == 0) return;
-        if (table) {
-            hipLaunchKernelGGL((k_fill_table<J>), dim3(1), dim3(kThreads), 0, ctx->stream, job, table + at,
-                               table_apart + at_apart);
+        if (mem.t) {
+            hipLaunchKernelGGL((k_fill_table<J>), dim3(1), dim3(kThreads), 0, ctx->stream, job, mem.t + at,
+                               mem.apart + at_apart);
             at += job.count;
             at_apart += job.aparts;
         } else {
@@ -556,7 +573,7 @@ gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, in
     for (int32_t k = 0; k < n; ++k) {
         const int64_t values = in[k].rows * in[k].cols;
         if (values == 0) continue;
-        const bool apart = is_apart(k);
+        const bool apart = is_apart(in, out, k);
         if (job.count == J::kCap || (apart && job.aparts == kApart)) flush();
         blocks += ceil_div(values, piece);
         T& d = job.t[job.count++];
@@ -572,7 +589,7 @@ gs_status launch_list(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, in
         put(d, k);
     }
     flush();
-    if (table && count > 0) go(Table<T>{table, table_apart, piece, (int32_t)count}, (uint32_t)blocks);
+    if (mem.t) go(Table<T>{mem.t, mem.apart, piece, at}, (uint32_t)blocks);
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;
 }
@@ -603,22 +620,31 @@ void join_columns(const gs_tensor* in, const gs_tensor* in2, int32_t n, std::vec
 }
 
 // the partials of a list's squares, one per block
-gs_status squares_of(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector<GsAlloc>* tmp, double** part,
-                     int64_t* parts)
+struct Squares {
+    double* part;
+    int64_t parts, piece;
+    ListMemory<NormJob> mem;
+};
+
+gs_status take_squares(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector<GsAlloc>* tmp, Squares* q)
 {
-    const int64_t piece = piece_of(ctx, values(grads, n));
-    *parts = pieces(grads, n, piece);
-    *part = (double*)gs_malloc(ctx, 8 * std::max<int64_t>(*parts, 1), GS_MEM_SCRATCH, tmp);
-    if (!*part) return GS_ERR_OOM;
+    q->piece = piece_of(ctx, values(grads, n));
+    q->parts = pieces(grads, n, q->piece);
+    q->part = (double*)gs_malloc(ctx, 8 * std::max<int64_t>(q->parts, 1), GS_MEM_SCRATCH, tmp);
+    return q->part ? take_list(ctx, grads, nullptr, n, tmp, &q->mem) : GS_ERR_OOM;
+}
+
+gs_status launch_squares(gs_ctx* ctx, const gs_tensor* grads, int32_t n, const Squares& q)
+{
     GsTimerScope ts(ctx, "grad_norm");
     int64_t base = 0;
-    return launch_list<NormJob>(ctx, grads, nullptr, n, piece, tmp,
-                                [&](NormTensor& d, int32_t k) { d.p = grads[k].data; },
-                                [&](const auto& job, uint32_t nb) {
-                                    hipLaunchKernelGGL((k_squares<std::decay_t<decltype(job)>>), dim3(nb),
-                                                       dim3(kThreads), 0, ctx->stream, job, *part + base);
-                                    base += nb;
-                                });
+    return launch_list(ctx, grads, nullptr, n, q.piece, q.mem,
+                       [&](NormTensor& d, int32_t k) { d.p = grads[k].data; },
+                       [&](const auto& job, uint32_t nb) {
+                           hipLaunchKernelGGL((k_squares<std::decay_t<decltype(job)>>), dim3(nb), dim3(kThreads), 0,
+                                              ctx->stream, job, q.part + base);
+                           base += nb;
+                       });
 }
 
 }  // namespace
@@ -626,24 +652,22 @@ gs_status squares_of(gs_ctx* ctx, const gs_tensor* grads, int32_t n, std::vector
 // k_small for lists of up to kSmall values that fit one launch: scaling 0: the
 // norm alone, 1: into out, 2: in place.  False: not such a list.
 static bool launch_small(gs_ctx* ctx, const gs_tensor* in, const gs_tensor* out, int32_t n, int scaling,
-                         double max_norm, float* norm, std::vector<GsAlloc>* tmp, gs_status* st)
+                         double max_norm, float* norm, gs_status* st)
 {
     const int64_t total = values(in, n);
     if (total == 0 || total > kSmall || n > kSmallTensors) return false;
-    int32_t aparts = 0;
-    for (int32_t k = 0; k < n; ++k) aparts += !dense(in[k]) || (out && !dense(out[k]));
-    if (aparts > kApart) return false;
+    static_assert(kSmallTensors <= kApart && kSmallTensors <= ScaleJob::kCap, "one launch");
     GsTimerScope ts(ctx, scaling ? "clip" : "grad_norm");
-    *st = launch_list<ScaleJob>(ctx, in, out, n, kSmallPiece, tmp,
-                                [&](ScaleTensor& d, int32_t k) {
-                                    d.p = in[k].data;
-                                    d.o = out ? out[k].data : nullptr;
-                                },
-                                [&](const auto& job, uint32_t) {
-                                    if constexpr (std::is_same_v<std::decay_t<decltype(job)>, ScaleJob>)
-                                        hipLaunchKernelGGL(k_small, dim3(1), dim3(kSmallThreads), 0, ctx->stream, job,
-                                                           max_norm, norm, scaling);
-                                });
+    *st = launch_list(ctx, in, out, n, kSmallPiece, ListMemory<ScaleJob>{},
+                      [&](ScaleTensor& d, int32_t k) {
+                          d.p = in[k].data;
+                          d.o = out ? out[k].data : nullptr;
+                      },
+                      [&](const auto& job, uint32_t) {
+                          if constexpr (std::is_same_v<std::decay_t<decltype(job)>, ScaleJob>)
+                              hipLaunchKernelGGL(k_small, dim3(1), dim3(kSmallThreads), 0, ctx->stream, job, max_norm,
+                                                 norm, scaling);
+                      });
     return true;
 }
 
@@ -655,13 +679,12 @@ gs_status launch_grad_norm(gs_ctx* ctx, const gs_tensor* list, int32_t count, do
     const gs_tensor* grads = joined.data();
     const int32_t n = (int32_t)joined.size();
     gs_status st;
-    if (launch_small(ctx, grads, nullptr, n, 0, max_norm, norm, tmp, &st)) return st;
-    double* part;
-    int64_t parts;
-    st = squares_of(ctx, grads, n, tmp, &part, &parts);
-    if (st != GS_OK) return st;
+    if (launch_small(ctx, grads, nullptr, n, 0, max_norm, norm, &st)) return st;
+    Squares q;
+    if ((st = take_squares(ctx, grads, n, tmp, &q)) != GS_OK) return st;
+    if ((st = launch_squares(ctx, grads, n, q)) != GS_OK) return st;
     GsTimerScope ts(ctx, "grad_norm");
-    hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, part, parts, max_norm, norm);
+    hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, q.part, q.parts, max_norm, norm);
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;
 }
@@ -676,27 +699,28 @@ gs_status launch_clip(gs_ctx* ctx, const gs_tensor* list, int32_t count, double 
     const int64_t total = values(in, n);
     if (total == 0) return launch_grad_norm(ctx, in, n, max_norm, norm, tmp);
     gs_status st;
-    if (launch_small(ctx, in, out, n, to == list ? 2 : 1, max_norm, norm, tmp, &st)) return st;
-    double* part;
-    int64_t parts;
-    st = squares_of(ctx, in, n, tmp, &part, &parts);
-    if (st != GS_OK) return st;
+    if (launch_small(ctx, in, out, n, to == list ? 2 : 1, max_norm, norm, &st)) return st;
+    Squares q;
+    ListMemory<ScaleJob> mem;
+    if ((st = take_squares(ctx, in, n, tmp, &q)) != GS_OK) return st;
+    if ((st = take_list(ctx, in, out, n, tmp, &mem)) != GS_OK) return st;
+    if ((st = launch_squares(ctx, in, n, q)) != GS_OK) return st;
     GsTimerScope ts(ctx, "clip");
     const bool large = total > kLarge;
     if (large)
-        hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, part, parts, max_norm, norm);
+        hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, q.part, q.parts, max_norm, norm);
     int write = 1;   // the first launch writes the norm
-    return launch_list<ScaleJob>(ctx, in, out, n, large ? bounded(kLargePiece, total) : piece_of(ctx, total), tmp,
-                                 [&](ScaleTensor& d, int32_t k) {
-                                     d.p = in[k].data;
-                                     d.o = out[k].data;
-                                 },
-                                 [&](const auto& job, uint32_t nb) {
-                                     hipLaunchKernelGGL((k_scale<std::decay_t<decltype(job)>>), dim3(nb),
-                                                        dim3(kThreads), 0, ctx->stream, job, large ? nullptr : part,
-                                                        parts, max_norm, norm, write);
-                                     write = 0;
-                                 });
+    return launch_list(ctx, in, out, n, large ? bounded(kLargePiece, total) : piece_of(ctx, total), mem,
+                       [&](ScaleTensor& d, int32_t k) {
+                           d.p = in[k].data;
+                           d.o = out[k].data;
+                       },
+                       [&](const auto& job, uint32_t nb) {
+                           hipLaunchKernelGGL((k_scale<std::decay_t<decltype(job)>>), dim3(nb), dim3(kThreads), 0,
+                                              ctx->stream, job, large ? nullptr : q.part, q.parts, max_norm, norm,
+                                              write);
+                           write = 0;
+                       });
 }
 
 gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, const gs_tensor* v, const gs_tensor* g,
@@ -712,18 +736,21 @@ gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
     a.inv2 = (float)(1.0 / (1.0 - std::pow(o->beta2, (double)o->step)));
     a.eps = (float)o->eps;
     a.keep = (float)(1.0 - o->lr * o->weight_decay);
+    ListMemory<AdamJob> mem;
+    const gs_status st = take_list(ctx, g, nullptr, n, tmp, &mem);
+    if (st != GS_OK) return st;
     GsTimerScope ts(ctx, "adam_list");
-    return launch_list<AdamJob>(ctx, g, nullptr, n, bounded(kAdamPiece, values(g, n)), tmp,
-                                [&](AdamTensor& d, int32_t k) {
-                                    d.p = (float*)p[k].data;
-                                    d.m = (float*)m[k].data;
-                                    d.v = (float*)v[k].data;
-                                    d.g = g[k].data;
-                                    d.copy = copies ? copies[k].data : nullptr;
-                                    d.c.type2 = (int8_t)(copies ? copies[k].type : 0);
-                                },
-                                [&](const auto& job, uint32_t nb) {
-                                    hipLaunchKernelGGL((k_adam_list<std::decay_t<decltype(job)>>), dim3(nb),
-                                                       dim3(kThreads), 0, ctx->stream, job, a, norm);
-                                });
+    return launch_list(ctx, g, nullptr, n, bounded(kAdamPiece, values(g, n)), mem,
+                       [&](AdamTensor& d, int32_t k) {
+                           d.p = (float*)p[k].data;
+                           d.m = (float*)m[k].data;
+                           d.v = (float*)v[k].data;
+                           d.g = g[k].data;
+                           d.copy = copies ? copies[k].data : nullptr;
+                           d.c.type2 = (int8_t)(copies ? copies[k].type : 0);
+                       },
+                       [&](const auto& job, uint32_t nb) {
+                           hipLaunchKernelGGL((k_adam_list<std::decay_t<decltype(job)>>), dim3(nb), dim3(kThreads), 0,
+                                              ctx->stream, job, a, norm);
+                       });
 }

@@ -726,3 +726,58 @@ def test_gradient_of_few_positions(ctx, n, w):
     for kind in ("one", "zipf", "masked"):
         check_gradient(ctx, n, 700, w, kind, "bf16" if n % 2 else "f32", "f32", "i64" if w == 3 else "i32", padding=5)
     check_gradient(ctx, n, 70, w, "uniform", "f32", "bf16", accumulate=True)
+
+
+# ---------------------------------------------------------------------------- lists at the limits of a launch
+
+def long_list(kind):
+    """(tensors, buffer) of lists of more than four million values whose descriptors go to a table on the device:
+    columns of wide rows, or dense tensors."""
+    torch = _t()
+    gen = torch.Generator().manual_seed(11)
+    if kind == "columns":
+        wide = torch.randn((70_001, 130), generator=gen).cuda()
+        return [wide[:, 2 * k:2 * k + 1] for k in range(65)], wide
+    ts = make_list([11] * 432 + [4_200_000], "f32", seed=12)
+    return ts, ts[0]._base
+
+
+@pytest.mark.parametrize("kind", ["columns", "dense"])
+def test_allocation_failure_leaves_the_outputs_of_a_long_list(kind):
+    """Every allocation of a call fails in turn, the descriptor tables among them: norm, outputs, parameters and
+    moments keep their values."""
+    torch = _t()
+    from tests.test_gpu_errors import FailingContext
+    f = FailingContext()
+    ts, buf = long_list(kind)
+    norm = torch.full((2,), 9.0, device="cuda")
+    outs = [torch.full_like(t, 5.0) for t in ts]
+    p, m, v = ([torch.full(t.shape, x, device="cuda") for t in ts] for x in (1.0, 2.0, 3.0))
+    lists = [B.TensorList(x) for x in (ts, outs, p, m, v)]
+    keep = buf.clone()
+    full = lambda xs, x: all(bool(t.eq(x).all()) for t in xs)
+    untouched = lambda: (bool(norm.eq(9.0).all()) and torch.equal(buf, keep) and full(outs, 5.0) and full(p, 1.0) and
+                         full(m, 2.0) and full(v, 3.0))
+    live = f.mem_stats()["live"]
+    for call in (lambda: B.gs_grad_norm(f, lists[0], 1e-3, norm), lambda: B.gs_clip_grads(f, lists[0], 1e-3, norm),
+                 lambda: B.gs_clip_grads(f, lists[0], 1e-3, norm, out=lists[1]),
+                 lambda: B.gs_adam_tensors(f, *lists[2:], lists[0], **OPTS)):
+        k = 1
+        while True:
+            f.arm(k)
+            try:
+                call()
+                break
+            except B.GsError as e:
+                assert e.status == B.GS_ERR_OOM
+                torch.cuda.synchronize()
+                assert untouched(), k
+                assert f.mem_stats()["live"] == live
+            k += 1
+        f.arm(0)
+        assert k > 2
+        buf.copy_(keep)
+        norm.fill_(9.0)
+        for t in outs:
+            t.fill_(5.0)
+    f.close()
