@@ -173,7 +173,7 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
             if (st != GS_OK) return st;
             if (q < 3 && own[q]->type != GS_F32)
                 return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be GS_F32", name[q], k);
-            if (own[q]->rows > 1 && own[q]->stride != own[q]->cols)
+            if (own[q]->rows > 1 && own[q]->cols > 0 && own[q]->stride != own[q]->cols)
                 return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be contiguous", name[q], k);
         }
         gs_status st = check_tensor(ctx, grads + k, false, "gradient", k);

@@ -781,3 +781,16 @@ def test_allocation_failure_leaves_the_outputs_of_a_long_list(kind):
         for t in outs:
             t.fill_(5.0)
     f.close()
+
+
+def test_adam_of_tensors_without_values(ctx):
+    """Rows without columns and columns without rows take part in a list and change nothing in it."""
+    torch = _t()
+    gen = torch.Generator().manual_seed(14)
+    shapes = [(5, 0), (7, 3), (0, 4), (1, 0), (0,), (6,)]
+    params, grads = ([torch.randn(s, generator=gen).cuda() for s in shapes] for _ in range(2))
+    assert params[0].stride() == (1, 1)
+    run_adam(ctx, params, grads, OPTS, copies=[torch.empty(s, dtype=torch.bfloat16, device="cuda") for s in shapes])
+    r = B.gs_grad_norm(ctx, grads, 1.0)
+    norm = reference_norm(grads)
+    close(r[0], norm, 2 * u * norm)
