@@ -415,21 +415,22 @@ __global__ __launch_bounds__(TINY ? 1024 : 256) void k_embed_sum(const T* __rest
     }
 }
 
-// (3) One block per border between blocks of (2), most of which end at once:
-// if a run begins in the block before it and crosses the border, its tail and
-// the heads of the blocks after it are added, the teams taking every teams-th
-// piece, their sums in order.
+// (3) One block per border between blocks of (2) and column range, most of
+// which end at once: if a run begins in the block before it and crosses the
+// border, its tail and the heads of the blocks after it are added, the teams
+// taking every teams-th piece, their sums in order.
 template <int VEC>
 __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
 {
     __shared__ float part[256 * VEC];
     __shared__ uint32_t more[4];
-    const int64_t b = blockIdx.x, end = (b + 1) * sh.per_block;
+    const uint32_t slab = blockIdx.x % sh.slabs;
+    const int64_t b = blockIdx.x / sh.slabs, end = (b + 1) * sh.per_block;
     const uint32_t row = sh.keys[end];   // end < n: only inner borders are launched
     if (row >= sh.rows || sh.keys[end - 1] != row) return;
     if (b > 0 && sh.keys[b * sh.per_block - 1] == row) return;   // it began earlier
     // blocks b + 1 .. b + m hold its heads: block t does if the key at its start is row
-    const int64_t blocks = gridDim.x + 1;
+    const int64_t blocks = sh.blocks;
     int64_t m = 0;
     for (;;) {
         const int64_t t = b + 1 + m + threadIdx.x;
@@ -443,7 +444,7 @@ __global__ __launch_bounds__(256) void k_embed_join(SumShape sh, Dest d)
     }
     const int lanes = 1 << sh.lg, teams = 256 >> sh.lg;
     const int team = threadIdx.x >> sh.lg, lane = threadIdx.x & (lanes - 1);
-    const uint32_t c0 = ((uint32_t)blockIdx.y * lanes + lane) * VEC;
+    const uint32_t c0 = (slab * lanes + lane) * VEC;
     const bool on = c0 < sh.cols;
     const uint32_t cb = min(c0, sh.cols - VEC);
     float acc[VEC];
@@ -554,7 +555,9 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     // the block holds (x 48: 200 positions 8.7 against 14.4, 512 13.4 against 14.7)
     split(4);
     const bool joined = n > (int64_t)kBatch * (256 >> lg);
-    const bool tiny = n > 0 && n <= std::min<int64_t>(joined ? kTiny : 320, kBatch * (1024 >> lg));
+    // a launch has fewer than 2^32 threads: with rows of 2^28 columns or more
+    // the smaller blocks take the column ranges
+    const bool tiny = n > 0 && n <= std::min<int64_t>(joined ? kTiny : 320, kBatch * (1024 >> lg)) && cols < 1 << 28;
     if (!tiny) split(dout->type == GS_F32 ? 4 : 8);
     const int64_t slabs = ceil_div(cols, (int64_t)vec << lg);
     // sixteen wavefronts for each compute unit, in chunks of 8 to 256 positions
@@ -575,7 +578,7 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
     const int64_t row_bytes = cols * (dtable->type == GS_F32 ? 4 : 2);
     sh.zero_rows = (int)std::min<int64_t>(64, std::max<int64_t>(1, 65536 / row_bytes));
     const int64_t clear = accumulate ? 0 : ceil_div(rows, (tiny ? 16 : 4) * (int64_t)sh.zero_rows);
-    if (blocks * slabs + clear > 0xFFFFFF || slabs > 65535)   // 2^32 threads
+    if (blocks * slabs + clear > 0xFFFFFF)   // 2^32 threads
         return gs_fail(ctx, GS_ERR_OVERFLOW, "table gradient of %lld rows of %lld values", (long long)rows,
                        (long long)cols);
     sh.blocks = (uint32_t)blocks;
@@ -610,8 +613,8 @@ gs_status launch_embed_bwd(gs_ctx* ctx, const void* idx, int idx_type, int64_t n
             else if constexpr (VEC <= 4) launch(o, std::true_type{});
         });
         if (blocks > 1)
-            hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)(blocks - 1), (unsigned)slabs), dim3(256), 0,
-                               ctx->stream, sh, d);
+            hipLaunchKernelGGL((k_embed_join<VEC>), dim3((unsigned)((blocks - 1) * slabs)), dim3(256), 0, ctx->stream,
+                               sh, d);
     };
     with_type(dout->type, [&](auto t) {
         if (vec == 1) sum(t, std::integral_constant<int, 1>{});

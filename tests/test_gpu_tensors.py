@@ -794,3 +794,20 @@ def test_adam_of_tensors_without_values(ctx):
     r = B.gs_grad_norm(ctx, grads, 1.0)
     norm = reference_norm(grads)
     close(r[0], norm, 2 * u * norm)
+
+
+@pytest.mark.parametrize("n", [2, 200, 1500])
+def test_gradient_of_very_wide_rows(ctx, n):
+    """More column ranges than a launch has blocks in y: 2 positions (one launch), 200 (one block of positions per
+    range), and 1500 that share one gradient row (several, joined).  Whole numbers, so that every sum is exact."""
+    torch = _t()
+    w = 256 * 65_536 + 5
+    row = (torch.arange(w, device="cuda") % 5 - 2).float()
+    dout = row.expand(n, w) if n > 2 else torch.stack([row, -3.0 * row])
+    idx = torch.full((n,), 2, dtype=torch.int32, device="cuda")
+    idx[1] = 0
+    d = torch.full((3, w), 7.0, device="cuda")
+    B.gs_embed_bwd(ctx, idx, dout, d, scale=0.5)
+    assert torch.equal(d[0], 0.5 * dout[1]) and d[1].eq(0.0).all() and torch.equal(d[2], 0.5 * (n - 1) * row)
+    B.gs_embed_bwd(ctx, idx, dout, d, scale=0.5, accumulate=True)
+    assert torch.equal(d[0], dout[1]) and d[1].eq(0.0).all() and torch.equal(d[2], (n - 1) * row)
