@@ -565,6 +565,13 @@ def _index(idx, ctx):
     return code
 
 
+def _rows(t, idx):
+    """A row per index: a contiguous tensor of the indices' shape and one dimension more, as n x width."""
+    if t.dim() != 2 and t.dim() == idx.dim() + 1 and t.shape[:-1] == idx.shape and t.is_contiguous():
+        return t.view(idx.numel(), t.shape[-1])
+    return t
+
+
 def _two_tensors(ctx, a, b):
     """Addresses of two gs_tensors, in words that the context keeps for its calls (five each, as in TensorList)."""
     w = ctx.words
@@ -584,21 +591,22 @@ def _norm_ptr(norm, ctx):
 
 def gs_embed_fwd(ctx: Context, table, idx, out=None, scale=1.0):
     """out[i] = scale * table[idx[i]] (zeros where idx[i] is outside the table); idx of any shape, out
-    idx.numel() x table.shape[1] (allocated in the table's type when None)."""
+    idx.numel() x table.shape[1] (allocated in the table's type when None) or, contiguous, idx.shape and the width."""
     code = _index(idx, ctx)
     n = idx.numel()
     if out is None:
         with ctx.torch.cuda.stream(ctx.stream):
             out = table.new_empty((n, table.shape[1]))
-    t, o = _two_tensors(ctx, table, out)
+    t, o = _two_tensors(ctx, table, _rows(out, idx))
     ctx.check(ctx.lib.gs_embed_fwd(ctx.handle, t, idx.data_ptr(), code, n, scale, o))
     return out
 
 
 def gs_embed_bwd(ctx: Context, idx, dout, dtable, scale=1.0, padding=-1, accumulate=False):
-    """dtable[v] = scale * sum of dout[i] over idx[i] == v (added to dtable when accumulate)."""
+    """dtable[v] = scale * sum of dout[i] over idx[i] == v (added to dtable when accumulate); dout as out of
+    gs_embed_fwd."""
     code = _index(idx, ctx)
-    g, t = _two_tensors(ctx, dout, dtable)
+    g, t = _two_tensors(ctx, _rows(dout, idx), dtable)
     ctx.check(ctx.lib.gs_embed_bwd(ctx.handle, idx.data_ptr(), code, idx.numel(), g, scale, padding, accumulate, t))
     return dtable
 

@@ -811,3 +811,28 @@ def test_gradient_of_very_wide_rows(ctx, n):
     assert torch.equal(d[0], 0.5 * dout[1]) and d[1].eq(0.0).all() and torch.equal(d[2], 0.5 * (n - 1) * row)
     B.gs_embed_bwd(ctx, idx, dout, d, scale=0.5, accumulate=True)
     assert torch.equal(d[0], dout[1]) and d[1].eq(0.0).all() and torch.equal(d[2], (n - 1) * row)
+
+
+def test_rows_in_the_shape_of_their_indices(ctx):
+    """Indices (B, T) and contiguous rows (B, T, W), as a model holds them."""
+    torch = _t()
+    gen = torch.Generator().manual_seed(15)
+    table, idx = torch.randn((9, 12), generator=gen).cuda(), torch.randint(-1, 9, (3, 5), generator=gen).cuda()
+    out = torch.empty((3, 5, 12), device="cuda")
+    assert B.gs_embed_fwd(ctx, table, idx, out) is out
+    assert torch.equal(out.view(15, 12), B.gs_embed_fwd(ctx, table, idx))
+    d, want = torch.empty_like(table), torch.empty_like(table)
+    B.gs_embed_bwd(ctx, idx, out, d)
+    B.gs_embed_bwd(ctx, idx, out.view(15, 12), want)
+    assert torch.equal(d, want)
+    one = torch.empty((1, 12), device="cuda")
+    assert torch.equal(B.gs_embed_fwd(ctx, table, idx[0, 1], one[0])[None], B.gs_embed_fwd(ctx, table, idx[0, 1:2]))
+    # rows that are not those of the indices
+    for bad in (torch.empty((3, 5, 11), device="cuda"), torch.empty((5, 3, 24), device="cuda"),
+                torch.empty((3, 4, 12), device="cuda")):
+        with pytest.raises((ValueError, B.GsError)):
+            B.gs_embed_bwd(ctx, idx, bad, d)
+        with pytest.raises((ValueError, B.GsError)):
+            B.gs_embed_fwd(ctx, table, idx, bad)
+    with pytest.raises(ValueError):
+        B.gs_embed_bwd(ctx, idx, out.transpose(0, 1), d)
