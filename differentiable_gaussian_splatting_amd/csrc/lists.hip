@@ -484,6 +484,12 @@ constexpr int32_t kSmallTensors = 16;
 // the factor formed in the scaling launch, 13.7 with a launch of its own.
 constexpr int64_t kLarge = 4000000, kLargePiece = 2048, kAdamPiece = 1024;
 
+// A list of more than kParts partials (one per tensor at least) is also scaled
+// after a launch that forms the factor, as every block would add them all: of
+// tensors of 40 values each, 2000 take 163 us without that launch and 166 with
+// it, 3000 241 and 242, 4000 338 and 322, 100,000 45,000 and 8,430.
+constexpr int64_t kParts = 3072;
+
 // rows x cols values that lie one after the other
 bool dense(const gs_tensor& t) { return t.rows <= 1 || t.stride == t.cols; }
 
@@ -706,8 +712,8 @@ gs_status launch_clip(gs_ctx* ctx, const gs_tensor* list, int32_t count, double 
     if ((st = take_list(ctx, in, out, n, tmp, &mem)) != GS_OK) return st;
     if ((st = launch_squares(ctx, in, n, q)) != GS_OK) return st;
     GsTimerScope ts(ctx, "clip");
-    const bool large = total > kLarge;
-    if (large)
+    const bool large = total > kLarge, first = large || q.parts > kParts;   // the factor is formed first
+    if (first)
         hipLaunchKernelGGL(k_norm, dim3(1), dim3(kThreads), 0, ctx->stream, q.part, q.parts, max_norm, norm);
     int write = 1;   // the first launch writes the norm
     return launch_list(ctx, in, out, n, large ? bounded(kLargePiece, total) : piece_of(ctx, total), mem,
@@ -717,7 +723,7 @@ gs_status launch_clip(gs_ctx* ctx, const gs_tensor* list, int32_t count, double 
                        },
                        [&](const auto& job, uint32_t nb) {
                            hipLaunchKernelGGL((k_scale<std::decay_t<decltype(job)>>), dim3(nb), dim3(kThreads), 0,
-                                              ctx->stream, job, large ? nullptr : q.part, q.parts, max_norm, norm,
+                                              ctx->stream, job, first ? nullptr : q.part, q.parts, max_norm, norm,
                                               write);
                            write = 0;
                        });
