@@ -880,3 +880,59 @@ def test_clip_of_many_small_tensors_takes_time_in_proportion(ctx):
     alone = seconds(lambda: B.gs_grad_norm(ctx, ts, 1.0, norm))
     both = seconds(lambda: B.gs_clip_grads(ctx, ts, 1.0, norm))
     assert both < 6.0 * alone, (both, alone)
+
+
+def mixed_list(live, big, seed):
+    """`live` tensors with values, every ninth of them a column of wide rows, an empty one after every fifth, and
+    the last one of `big` values where big > 0; beside them contiguous tensors of the same shapes."""
+    torch = _t()
+    g = torch.Generator().manual_seed(seed)
+    wide = torch.randn((13, 2 * (live // 9) + 2), generator=g).cuda()
+    ts, column = [], 0
+    for k in range(live):
+        if k % 9 == 4:
+            ts.append(wide[:, 2 * column:2 * column + 1])
+            column += 1
+        else:
+            ts.append(torch.randn(big if big and k == live - 1 else 1 + k % 6, generator=g).cuda())
+        if k % 5 == 2:
+            ts.append(torch.empty(0, device="cuda"))
+    return ts, [torch.randn(t.shape, generator=g).cuda() for t in ts]
+
+
+# tensors that one launch describes in its arguments: Adam 62, clip 108, norm 144; a list of more than four million
+# values has them in a table from three times as many on
+LIMITS = [61, 62, 63, 107, 108, 109, 143, 144, 145, 185, 186, 187, 323, 324, 325, 431, 432, 433, 500]
+
+
+@pytest.mark.parametrize("big", [0, 4_100_000])
+@pytest.mark.parametrize("live", LIMITS)
+def test_lists_at_the_limits_of_a_launch(ctx, live, big):
+    torch = _t()
+    ts, outs = mixed_list(live, big, live)
+    assert sum(t.numel() > 0 for t in ts) == live
+    whole = np.concatenate([f64(t).ravel() for t in ts])
+    norm = math.sqrt(float((whole ** 2).sum()))
+    c = min(1.0, 0.5 * norm / (norm + 1e-6))
+    r = B.gs_grad_norm(ctx, ts, 0.5 * norm)
+    close(r[0], norm, 2 * u * norm)
+    close(r[1], c, 2 * u * c)
+    assert torch.equal(B.gs_clip_grads(ctx, ts, 0.5 * norm, out=outs), r)
+    got = np.concatenate([f64(o).ravel() for o in outs])
+    assert (np.abs(got - whole * c) <= 5 * u * np.abs(whole * c)).all()
+    gen = torch.Generator().manual_seed(live)
+    ps, ms = ([torch.randn(t.shape, generator=gen).cuda() for t in ts] for _ in range(2))
+    vs = [torch.rand(t.shape, generator=gen).cuda() for t in ts]
+    low = [torch.empty(t.shape, dtype=torch.float16, device="cuda") if k % 4 else None for k, t in enumerate(ts)]
+    flat = lambda xs: np.concatenate([f64(x).ravel() for x in xs])
+    old = [flat(x) for x in (ps, ms, vs)]
+    o = dict(OPTS, step=3)
+    B.gs_adam_tensors(ctx, ps, ms, vs, ts, norm=r, copies=low, **o)
+    p1, m1, v1, den, upd = adam_reference(*old, whole, c, o)
+    for x, want, bound in zip((ps, ms, vs), (p1, m1, v1), _adam_bounds(*old, whole, c, o, den, upd, v1)):
+        assert (np.abs(flat(x) - want) <= bound).all()
+    for p, k in zip(ps, low):
+        assert k is None or torch.equal(k, p.half())
+    B.gs_clip_grads(ctx, ts, 0.5 * norm)
+    for t, x in zip(ts, outs):
+        assert torch.equal(t, x)
