@@ -27,16 +27,8 @@
 namespace {
 
 using gst::narrow;
+using gst::row_of;
 using gst::with_type;
-
-// idx[i] as a row of the table, or rows (a value no row has) when it is
-// outside [0, rows) or equal to skip
-template <typename I>
-__device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i, uint32_t rows, int64_t skip)
-{
-    const int64_t v = (int64_t)idx[i];
-    return v >= 0 && v < (int64_t)rows && v != skip ? (uint32_t)v : rows;
-}
 
 // The rows of out are cut into packs of VEC values (16 bytes of the wider
 // type); the last pack of a row whose width is no multiple of VEC starts

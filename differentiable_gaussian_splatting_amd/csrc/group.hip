@@ -4,8 +4,8 @@
 // Up to kRankMax positions: tiles sorted by counting, then merged (one or two
 // launches, where the passes below take three each; a whole table gradient of
 // 16384 x 8 f32 takes 22 us so and 48 us with passes, at 65536 x 8 both take
-// about 50, at 131072 x 8 90 and 54).  More: two or three passes of up to 9 bits of the row, lowest first, each a histogram per tile
-// of 4096 positions, a scan of every digit's counts over the tiles, and a
+// about 50, at 131072 x 8 90 and 54).  More: one to four passes of up to 9 bits
+// of the row, lowest first, each a histogram per tile of 4096 positions, a scan of every digit's counts over the tiles, and a
 // stable scatter; the first pass reads the indices themselves.  6M positions
 // by 16 bits: 95 us, two passes of 10 us (histogram), 5 (scan) and 33 (scatter,
 // 96 MB moved; tiles of 8192 took 38).  Positions
@@ -13,19 +13,14 @@
 // others in every pass, so that they end up last without a bit of the key.
 #include "gs_device.h"
 #include "gs_internal.h"
+#include "gs_tensor.h"
 
 #include <algorithm>
 #include <type_traits>
 
 namespace {
 
-// idx[i] as a row of the table, or `rows` when it names none
-template <typename I>
-__device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i, uint32_t rows, int64_t skip)
-{
-    const int64_t v = (int64_t)idx[i];
-    return v >= 0 && v < (int64_t)rows && v != skip ? (uint32_t)v : rows;
-}
+using gst::row_of;
 
 // Tiles of 2048 positions, each sorted by counting: position i of a tile goes
 // to the place

@@ -55,6 +55,15 @@ __device__ __forceinline__ T narrow(float x)
     return (T)x;
 }
 
+// idx[i] as a row of a table, or `rows` (a value no row has) when it is outside
+// [0, rows) or equal to skip
+template <typename I>
+__device__ __forceinline__ uint32_t row_of(const I* __restrict__ idx, int64_t i, uint32_t rows, int64_t skip)
+{
+    const int64_t v = (int64_t)idx[i];
+    return v >= 0 && v < (int64_t)rows && v != skip ? (uint32_t)v : rows;
+}
+
 // Calls f with a value of the element type (GS_F32, GS_F16, GS_BF16).
 template <typename F>
 inline void with_type(int type, F&& f)

@@ -936,3 +936,25 @@ def test_lists_at_the_limits_of_a_launch(ctx, live, big):
     B.gs_clip_grads(ctx, ts, 0.5 * norm)
     for t, x in zip(ts, outs):
         assert torch.equal(t, x)
+
+
+@pytest.mark.parametrize("v,on", [((1 << 27) + 5, "f32"), ((1 << 31) - 1, "bf16")])
+def test_gradient_of_more_rows_than_three_passes_sort(ctx, v, on):
+    """Rows of 28 and 31 bits, grouped in four passes.  Whole numbers: every sum is exact."""
+    torch = _t()
+    n = 70_001
+    rng = np.random.default_rng(31)
+    # rows that differ in every digit, the first and last among them, and positions that name none
+    names = np.unique(np.concatenate([[0, 1, v - 2, v - 1], rng.integers(0, v, 3000), 1 << np.arange(27)]))
+    i = np.where(rng.random(n) < 0.1, rng.choice([-1, v, v + 1], n), rng.choice(names, n))
+    x = rng.integers(-3, 4, n)
+    d = torch.full((v, 1), 5.0, dtype=dtype(on), device="cuda")
+    B.gs_embed_bwd(ctx, torch.from_numpy(i).cuda(), torch.from_numpy(x).float()[:, None].cuda(), d)
+    sums = np.zeros(names.size)
+    inside = (i >= 0) & (i < v)
+    np.add.at(sums, np.searchsorted(names, i[inside]), x[inside].astype(np.float64))
+    at = torch.from_numpy(names).cuda()
+    got = d[at, 0]
+    assert torch.equal(got, torch.from_numpy(sums).float().to(dtype(on)).cuda())
+    d[at] = 0.0
+    assert not any(bool(part.any()) for part in d.split(1 << 28))
