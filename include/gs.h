@@ -416,7 +416,8 @@ enum { GS_F32 = 0, GS_F16 = 1, GS_BF16 = 2, GS_I32 = 3, GS_I64 = 4 };
  * rows, cols >= 0; no value is read where either is 0.  A tensor that is only
  * read may have any stride >= 0 (0: one row, broadcast); one that is written
  * needs stride >= cols unless it has at most one row.  data is aligned to its
- * element, no more. */
+ * element, no more.  Every call refuses a tensor of more than 2^40 values, and
+ * one whose rows are apart and hold 2^31 values or more, with OVERFLOW. */
 typedef struct {
     void* data;
     int64_t rows, cols, stride;
@@ -428,8 +429,8 @@ typedef struct {
  * once to out's type (to nearest, ties to even); a row of zeros where idx[i]
  * is outside [0, table->rows) (a masked token).  idx: device, n contiguous
  * GS_I32 or GS_I64 values.  out: n x table->cols.  Table and out may have
- * different types.  Errors: INVALID_ARG, OVERFLOW (n or table->rows >= 2^31,
- * cols >= 2^31), DEVICE. */
+ * different types.  Errors: INVALID_ARG, OVERFLOW (n, table->rows or cols
+ * >= 2^31), DEVICE. */
 gs_status gs_embed_fwd(gs_ctx* ctx, const gs_tensor* table, const void* idx, int32_t idx_type, int64_t n, float scale,
                        const gs_tensor* out);
 
@@ -449,13 +450,15 @@ gs_status gs_embed_bwd(gs_ctx* ctx, const void* idx, int32_t idx_type, int64_t n
  * the clip factor norm[1] = min(1, max_norm / (norm + 1e-6)).  norm: device, two
  * floats.  max_norm >= 0, +inf for the norm alone (factor 1).  A value that is
  * not finite makes norm[0] inf or NaN and norm[1] 0 or NaN.  grads: host array
- * of n_tensors >= 0 descriptors.  Errors: INVALID_ARG, OOM, DEVICE. */
+ * of n_tensors >= 0 descriptors.  Errors: INVALID_ARG, OVERFLOW (also more than
+ * 2^42 values in all), OOM, DEVICE. */
 gs_status gs_grad_norm(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, double max_norm, float* norm);
 
 /* gs_grad_norm, then out[k] = norm[1] grads[k] for every tensor, in f32 and
  * rounded once.  out: n_tensors descriptors of the same sizes and types, or
  * NULL to scale grads in place (no value is written when the factor is 1).  An
- * out tensor is its own gradient or does not overlap any gradient. */
+ * out tensor is its own gradient or does not overlap any gradient.  Errors: as
+ * gs_grad_norm. */
 gs_status gs_clip_grads(gs_ctx* ctx, const gs_tensor* grads, int32_t n_tensors, double max_norm, const gs_tensor* out,
                         float* norm);
 
@@ -476,7 +479,7 @@ typedef struct {
  * parameters rounded to the copy's type.  All of a tensor's descriptors have
  * its rows and cols; params, m, v and copies are contiguous (stride = cols, or
  * at most one row), grads may be strided.  Each parameter is updated from its
- * own values alone.  Errors: INVALID_ARG, DEVICE. */
+ * own values alone.  Errors: as gs_grad_norm. */
 gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor* m, const gs_tensor* v,
                           const gs_tensor* grads, const gs_tensor* copies, int32_t n_tensors,
                           const gs_adam_opts* opts, const float* norm);

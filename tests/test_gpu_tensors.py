@@ -958,3 +958,28 @@ def test_gradient_of_more_rows_than_three_passes_sort(ctx, v, on):
     assert torch.equal(got, torch.from_numpy(sums).float().to(dtype(on)).cuda())
     d[at] = 0.0
     assert not any(bool(part.any()) for part in d.split(1 << 28))
+
+
+def test_sizes_beyond_the_limits_are_refused(ctx):
+    """OVERFLOW from each entry, by descriptors of broadcast rows (nothing is launched)."""
+    torch = _t()
+    L, h, over = ctx.lib, ctx.handle, B.GS_ERR_OVERFLOW
+    x, norm = torch.zeros(64, device="cuda"), torch.empty(2, device="cuda")
+    idx = torch.zeros(4, dtype=torch.int32, device="cuda")
+    T = lambda rows, cols, stride: B.gs_tensor(x.data_ptr(), rows, cols, stride, 0, 0)
+    ref = C.byref
+    huge, apart = T(1 << 31, 1 << 10, 0), T(2, 1 << 31, 0)
+    for t in (huge, apart):
+        assert L.gs_embed_fwd(h, ref(t), idx.data_ptr(), B.GS_I32, 4, 1.0, ref(T(4, t.cols, t.cols))) == over
+        assert L.gs_embed_bwd(h, idx.data_ptr(), B.GS_I32, t.rows, ref(t), 1.0, -1, 0, ref(T(1, t.cols, t.cols))) == over
+        a = C.cast((B.gs_tensor * 1)(t), C.c_void_p)
+        o = B.gs_adam_opts(1, 0, 1e-3, 0.9, 0.999, 1e-8, 0.0)
+        p = C.cast((B.gs_tensor * 1)(T(1, 8, 8)), C.c_void_p)
+        assert L.gs_grad_norm(h, a, 1, 1.0, norm.data_ptr()) == over
+        assert L.gs_clip_grads(h, a, 1, 1.0, a, norm.data_ptr()) == over
+        assert L.gs_adam_tensors(h, p, p, p, a, None, 1, o, None) == over
+    for n, rows, cols in ((1 << 31, 4, 8), (4, 1 << 31, 8), (4, 4, 1 << 31)):
+        assert L.gs_embed_fwd(h, ref(T(rows, cols, 0 if cols < 99 else cols)), idx.data_ptr(), B.GS_I32, n, 1.0,
+                              ref(T(4, 8, 8))) == over
+    many = (B.gs_tensor * 5)(*[T(1 << 30, 1 << 10, 0) for _ in range(5)])   # 5 x 2^40 values
+    assert L.gs_grad_norm(h, C.cast(many, C.c_void_p), 5, 1.0, norm.data_ptr()) == over
