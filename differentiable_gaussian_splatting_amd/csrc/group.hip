@@ -2,13 +2,14 @@
 // a stable sort of (row, position), the positions ascending within a row.
 //
 // Up to kRankMax positions: tiles sorted by counting, then merged (one or two
-// launches, where the passes below take three each; a whole table gradient of
-// 16384 x 8 f32 takes 22 us so and 48 us with passes, at 65536 x 8 both take
-// about 50, at 131072 x 8 90 and 54).  More: one to four passes of up to 9 bits
-// of the row, lowest first, each a histogram per tile of 4096 positions, a scan of every digit's counts over the tiles, and a
-// stable scatter; the first pass reads the indices themselves.  6M positions
-// by 16 bits: 95 us, two passes of 10 us (histogram), 5 (scan) and 33 (scatter,
-// 96 MB moved; tiles of 8192 took 38).  Positions
+// launches, where the passes below take three each; whole table gradients of
+// rows of 8 f32 into 32768 take, so and with passes, 15.2 and 32 us for 4000
+// positions, 22.4 and 37 for 32768, 35.8 and 38 for 65536, 57.5 and 38 for
+// 98304).  More: one to four passes of up to 9 bits of the row, lowest first,
+// each a histogram per tile of 4096 positions, a scan of every digit's counts
+// over the tiles, and a stable scatter; the first pass reads the indices
+// themselves.  6M positions by 16 bits: 95 us, two passes of 10 us (histogram),
+// 5 (scan) and 33 (scatter, 96 MB moved; tiles of 8192 took 38).  Positions
 // that name no row (masked, padding) have a digit of their own after all
 // others in every pass, so that they end up last without a bit of the key.
 #include "gs_device.h"
