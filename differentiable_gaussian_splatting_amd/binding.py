@@ -121,6 +121,11 @@ class gs_adam_opts(C.Structure):
                 ("beta2", C.c_double), ("eps", C.c_double), ("weight_decay", C.c_double)]
 
 
+class gs_muon_opts(C.Structure):
+    _fields_ = [("steps", C.c_int32), ("nesterov", C.c_int32), ("lr", C.c_double), ("momentum", C.c_double),
+                ("weight_decay", C.c_double)]
+
+
 ALLOC_FN = C.CFUNCTYPE(C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p)
 FREE_FN = C.CFUNCTYPE(None, C.c_void_p, C.c_void_p, C.c_size_t, C.c_void_p)
 
@@ -182,6 +187,11 @@ def load(path: str = LIB_PATH):
         "gs_grad_norm": (st, [vp, vp, i32, C.c_double, vp]),
         "gs_clip_grads": (st, [vp, vp, i32, C.c_double, vp, vp]),
         "gs_adam_tensors": (st, [vp, vp, vp, vp, vp, vp, i32, P(gs_adam_opts), vp]),
+        "gs_linear_fwd": (st, [vp, vp, vp, vp, i32, vp, vp, vp]),
+        "gs_linear_bwd": (st, [vp, vp, vp, vp, i32, vp, i32, vp, vp, vp]),
+        "gs_gated_fwd": (st, [vp, vp, vp, i32, vp, vp]),
+        "gs_gated_bwd": (st, [vp, vp, vp, vp, i32, vp, i32, vp, vp]),
+        "gs_muon_tensors": (st, [vp, vp, vp, vp, vp, i32, P(gs_muon_opts), vp]),
         "gs_train_view": (st, [vp, P(gs_camera), P(gs_params), vp, P(gs_view_opts), P(gs_view_result)]),
     }
     for name, (res, args) in sig.items():
@@ -572,11 +582,16 @@ def _rows(t, idx):
     return t
 
 
+def _words(ctx):
+    """Memory of a call's gs_tensors, kept by the context for its calls (five words each, as in TensorList)."""
+    if ctx.words is None:
+        ctx.words = array.array("q", [0] * 40)
+    return ctx.words
+
+
 def _two_tensors(ctx, a, b):
-    """Addresses of two gs_tensors, in words that the context keeps for its calls (five each, as in TensorList)."""
-    w = ctx.words
-    if w is None:
-        w = ctx.words = array.array("q", [0] * 10)
+    """Addresses of two gs_tensors."""
+    w = _words(ctx)
     w[0], w[1], w[2], w[3], w[4] = _tensor_fields(a, ctx.device)
     w[5], w[6], w[7], w[8], w[9] = _tensor_fields(b, ctx.device)
     at = w.buffer_info()[0]
@@ -647,6 +662,88 @@ def gs_adam_tensors(ctx: Context, params, m, v, grads, step, lr=1e-3, beta1=0.9,
         raise ValueError("the lists have different lengths")
     o = gs_adam_opts(step, 0, lr, beta1, beta2, eps, weight_decay)
     ctx.check(ctx.lib.gs_adam_tensors(ctx.handle, p.ptr, m.ptr, v.ptr, g.ptr, None if k is None else k.ptr, p.n, o,
+                                      None if norm is None else _norm_ptr(norm, ctx)))
+
+
+# ---------------------------------------------------------------------------- layers
+
+GS_ACTIVATIONS = {"none": 0, "relu": 1, "silu": 2, "gelu": 3, "sigmoid": 4}
+
+
+def _activation(act):
+    code = GS_ACTIVATIONS.get(act)
+    if code is None:
+        raise ValueError(f"activation {act!r}: expected one of {', '.join(GS_ACTIVATIONS)}")
+    return code
+
+
+def _layer_tensors(ctx, *tensors):
+    """Addresses of a layer call's gs_tensors (None: absent)."""
+    w, device = _words(ctx), ctx.device
+    at, where, k = w.buffer_info()[0], [], 0
+    for t in tensors:
+        if t is None:
+            where.append(None)
+            continue
+        w[k], w[k + 1], w[k + 2], w[k + 3], w[k + 4] = _tensor_fields(t, device)
+        where.append(at + 8 * k)
+        k += 5
+    return where
+
+
+def _new(ctx, like, *shape):
+    with ctx.torch.cuda.stream(ctx.stream):
+        return like.new_empty(shape)
+
+
+def gs_linear_fwd(ctx: Context, x, w, bias=None, act="none", residual=None, pre=None, out=None):
+    """out = act(x w^T + bias) + residual: x n x in, w outs x in, bias outs values, residual and out n x outs
+    (out allocated in x's type when None; it may be residual).  pre (n x outs, x's type): the activation's argument,
+    kept for gs_linear_bwd."""
+    code = _activation(act)
+    if out is None:
+        out = _new(ctx, x, x.shape[0], w.shape[0])
+    X, W, b, r, p, o = _layer_tensors(ctx, x, w, bias, residual, pre, out)
+    ctx.check(ctx.lib.gs_linear_fwd(ctx.handle, X, W, b, code, r, p, o))
+    return out
+
+
+def gs_linear_bwd(ctx: Context, x, w, dout, pre=None, act="none", dx=None, dw=None, dbias=None, accumulate=False):
+    """Gradients of gs_linear_fwd into those of dx, dw and dbias that are given (added to dw and dbias when
+    accumulate); the residual's gradient is dout."""
+    code = _activation(act)
+    X, W, p, d, gx, gw, gb = _layer_tensors(ctx, x, w, pre, dout, dx, dw, dbias)
+    ctx.check(ctx.lib.gs_linear_bwd(ctx.handle, X, W, p, code, d, accumulate, gx, gw, gb))
+
+
+def gs_gated_fwd(ctx: Context, x, w, act="silu", pre=None, out=None):
+    """out = act(g) * u with [g u] = x w^T; w: the outs gate rows, then the outs up rows.  pre (n x 2 outs, x's
+    type): [g u], kept for gs_gated_bwd."""
+    code = _activation(act)
+    if out is None:
+        out = _new(ctx, x, x.shape[0], w.shape[0] // 2)
+    X, W, p, o = _layer_tensors(ctx, x, w, pre, out)
+    ctx.check(ctx.lib.gs_gated_fwd(ctx.handle, X, W, code, p, o))
+    return out
+
+
+def gs_gated_bwd(ctx: Context, x, w, pre, dout, act="silu", dx=None, dw=None, accumulate=False):
+    """Gradients of gs_gated_fwd into those of dx and dw that are given (added to dw when accumulate)."""
+    code = _activation(act)
+    X, W, p, d, gx, gw = _layer_tensors(ctx, x, w, pre, dout, dx, dw)
+    ctx.check(ctx.lib.gs_gated_bwd(ctx.handle, X, W, p, code, d, accumulate, gx, gw))
+
+
+def gs_muon_tensors(ctx: Context, params, m, grads, lr=0.02, momentum=0.95, nesterov=True, weight_decay=0.0, steps=5,
+                    norm=None, copies=None):
+    """One Muon step over lists of matrices (TensorLists or 2-D tensors): momentum m, orthogonalised by `steps`
+    Newton-Schulz steps; norm and copies as for gs_adam_tensors."""
+    p, m, g = (_as_list(x, ctx) for x in (params, m, grads))
+    k = None if copies is None else _as_list(copies, ctx)
+    if not p.n == m.n == g.n or (k is not None and k.n != p.n):
+        raise ValueError("the lists have different lengths")
+    o = gs_muon_opts(steps, nesterov, lr, momentum, weight_decay)
+    ctx.check(ctx.lib.gs_muon_tensors(ctx.handle, p.ptr, m.ptr, g.ptr, None if k is None else k.ptr, p.n, o,
                                       None if norm is None else _norm_ptr(norm, ctx)))
 
 

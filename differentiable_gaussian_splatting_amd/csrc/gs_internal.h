@@ -380,4 +380,16 @@ gs_status launch_adam_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
                            const gs_tensor* copies, int32_t n, const gs_adam_opts* o, const float* norm,
                            std::vector<GsAlloc>* tmp);
 
+// layers.hip: linear layers (gated: both projections and their product)
+gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int act,
+                            const gs_tensor* residual, const gs_tensor* pre, const gs_tensor* out, bool gated,
+                            std::vector<GsAlloc>* tmp);
+gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int act,
+                            const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw,
+                            const gs_tensor* dbias, bool gated, std::vector<GsAlloc>* tmp);
+// muon.hip
+gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, const gs_tensor* g,
+                           const gs_tensor* copies, int32_t n, const gs_muon_opts* o, const float* norm,
+                           std::vector<GsAlloc>* tmp);
+
 static inline int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }

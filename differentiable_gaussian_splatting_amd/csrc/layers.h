@@ -1,0 +1,90 @@
+// layers.h -- what the files of the layer operators share: activations, the
+// description of one matrix product with its epilogue, and its launch.
+#pragma once
+
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "gs_internal.h"
+#include "mm.h"
+
+namespace gsm {
+
+// z sigma(v) and its slope, sigma(v) + z sigma(v) sigma(-v) v', with v = z
+// (silu), v = 2 sqrt(2 / pi) (z + 0.044715 z^3) (gelu).  With q = exp(-|v|) and
+// r = 1 / (1 + q), sigma is r or q r and sigma(v) sigma(-v) = q r^2: no
+// difference of near numbers.  Where q vanishes the value is z or 0, the slope
+// 1 or 0, at infinities too.
+constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.044715f;
+
+struct Sigma {
+    float p, t;   // sigma(v), sigma(v) sigma(-v)
+};
+__device__ __forceinline__ Sigma sigma(float v)
+{
+    const float q = expf(-fabsf(v)), r = 1.0f / (1.0f + q);
+    return Sigma{v >= 0.0f ? r : q * r, q * r * r};
+}
+__device__ __forceinline__ float gelu_arg(float z) { return kGelu1 * (z + kGelu3 * z * z * z); }
+
+__device__ __forceinline__ float act_value(float z, int act)
+{
+    if (act == GS_ACT_NONE) return z;
+    if (act == GS_ACT_RELU) return z < 0.0f ? 0.0f : z;   // NaN stays
+    const Sigma s = sigma(act == GS_ACT_GELU ? gelu_arg(z) : z);
+    if (act == GS_ACT_SIGMOID) return s.p;
+    return s.p == 0.0f ? 0.0f : z * s.p;
+}
+
+// value and slope
+__device__ __forceinline__ float2 act_both(float z, int act)
+{
+    if (act == GS_ACT_NONE) return make_float2(z, 1.0f);
+    if (act == GS_ACT_RELU) return make_float2(z < 0.0f ? 0.0f : z, z > 0.0f ? 1.0f : 0.0f);
+    const Sigma s = sigma(act == GS_ACT_GELU ? gelu_arg(z) : z);
+    if (act == GS_ACT_SIGMOID) return make_float2(s.p, s.t);
+    const float dv = act == GS_ACT_GELU ? kGelu1 * (1.0f + 3.0f * kGelu3 * z * z) : 1.0f;
+    return make_float2(s.p == 0.0f ? 0.0f : z * s.p, s.t == 0.0f ? s.p : s.p + z * s.t * dv);
+}
+
+// What follows a product: out = act(z + bias) + residual, with z + bias kept
+// in pre (each null: not there).  Types are GS_F32 or the product's own.
+struct Epilogue {
+    const void* bias;
+    const void* res;
+    void* pre;
+    void* out;
+    int64_t ldres, ldpre, ldout;
+    int64_t n;                   // columns of out
+    int32_t act;
+    int8_t bias_type, res_type, pre_type, out_type;
+};
+
+enum { kLarge = 0, kSmall = 1 };   // tiles
+
+struct LayerMm {
+    Operand a, b;                // rows of out, columns of out
+    int64_t m, k;
+    Epilogue e;
+    int64_t tm, tn;              // tiles
+    int64_t kper;                // values of k of a split, a multiple of the tile's step
+    float* ws;                   // sums of the splits (splits > 1), wn floats per row
+    int64_t wn;
+    int32_t splits, tile;
+    bool a_col, b_col, gated;    // a_col only with b_col
+};
+
+// one type each (layer_mm_*.hip)
+gs_status launch_layer_mm_f32(gs_ctx* ctx, const LayerMm& g);
+gs_status launch_layer_mm_f16(gs_ctx* ctx, const LayerMm& g);
+gs_status launch_layer_mm_bf16(gs_ctx* ctx, const LayerMm& g);
+
+// rows, columns and k step of each tile
+struct TileSize {
+    int m, n, k;
+};
+constexpr TileSize kTiles16[] = {{128, 128, 64}, {64, 64, 64}};
+constexpr TileSize kTiles32[] = {{128, 128, 32}, {64, 64, 32}};
+
+}  // namespace gsm

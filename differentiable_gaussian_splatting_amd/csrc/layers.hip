@@ -1,0 +1,243 @@
+// layers.hip -- linear and gated layers: how their matrix products are cut
+// into tiles and splits, and the gradient of the activation with the bias
+// gradient's column sums.
+//
+//   linear: out = act(x w^T + bias) + residual
+//           dz = dout act'(pre), dx = dz w, dw = dz^T x, dbias = sum over rows of dz
+//   gated:  [g u] = x w^T, out = act(g) u
+//           dg = dout u act'(g), du = dout act(g), then as above
+#include <algorithm>
+
+#include "layer_mm.h"
+
+namespace {
+
+using namespace gsm;
+
+constexpr int kDzThreads = 256;
+
+// dz, four columns of a row per thread: tx threads side by side, 256 / tx rows
+// at once, a block walks `rows` rows.  dz is rounded to the layer's type, as
+// the matrix instructions take it (a gradient that passes between layers of
+// that type would be rounded the same way); the column sums are of the f32
+// values, one partial row per block row, so they do not depend on timing.
+struct DzJob {
+    const void *pre, *dout;
+    void* dz;            // null: the sums alone
+    float* sums;         // [row blocks][n], null: none
+    int64_t m, n;        // n: columns of dout
+    int64_t ldpre, lddout, rows;
+    int32_t act, dout_type, tx, col_blocks;
+};
+
+template <typename S, bool GATED>
+__global__ __launch_bounds__(kDzThreads) void k_dz(const DzJob g)
+{
+    const int x = threadIdx.x % g.tx, y = threadIdx.x / g.tx, ny = kDzThreads / g.tx;
+    const int type = sizeof(S) == 4 ? GS_F32 : -1;
+    const int64_t cb = blockIdx.x % g.col_blocks, rb = blockIdx.x / g.col_blocks;
+    const int64_t n = (cb * g.tx + x) * 4, end = min(g.m, (rb + 1) * g.rows);
+    const int valid = (int)min((int64_t)4, g.n - n);
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (valid > 0) {
+        for (int64_t m = rb * g.rows + y; m < end; m += ny) {
+            const f32x4 d = load4<S>(g.dout, m * g.lddout + n, g.dout_type, valid);
+            f32x4 dz = d;
+            if constexpr (GATED) {
+                const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
+                const f32x4 u = load4<S>(g.pre, m * g.ldpre + g.n + n, type, valid);
+                f32x4 du;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 v = act_both(z[j], g.act);
+                    dz[j] = d[j] * u[j] * v.y;
+                    du[j] = d[j] * v.x;
+                }
+                store4<S>(g.dz, m * 2 * g.n + g.n + n, type, valid, du);
+                store4<S>(g.dz, m * 2 * g.n + n, type, valid, dz);
+            } else {
+                if (g.act != GS_ACT_NONE) {
+                    const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) dz[j] = d[j] * act_both(z[j], g.act).y;
+                }
+                if (g.dz) store4<S>(g.dz, m * g.n + n, type, valid, dz);
+                sum += dz;
+            }
+        }
+    }
+    if constexpr (!GATED) {
+        if (!g.sums) return;
+        __shared__ f32x4 part[kDzThreads];
+        part[threadIdx.x] = sum;
+        __syncthreads();
+        if (y == 0 && valid > 0) {
+            for (int q = 1; q < ny; ++q) sum += part[q * g.tx + x];
+            store4<float>(g.sums, rb * g.n + n, GS_F32, valid, sum);
+        }
+    }
+}
+
+// out[n] = (old out[n]) + sum over `blocks` rows of sums[..][n]: 64 columns a
+// block, four quarters of the rows
+template <typename S>
+__global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ sums, int64_t blocks, int64_t n, void* out,
+                                                  int out_type, int accumulate)
+{
+    __shared__ float part[4][64];
+    const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
+    const int64_t c = (int64_t)blockIdx.x * 64 + x;
+    float s = 0.0f;
+    if (c < n)
+        for (int64_t b = q; b < blocks; b += 4) s += sums[b * n + c];
+    part[q][x] = s;
+    __syncthreads();
+    if (q || c >= n) return;
+    s = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
+    if (out_type == GS_F32) {
+        float* o = (float*)out + c;
+        *o = accumulate ? *o + s : s;
+    } else {
+        S* o = (S*)out + c;
+        *o = gst::narrow<S>(accumulate ? (float)*o + s : s);
+    }
+}
+
+// Tiles and splits of a product of m x n (n of the tiles: both halves of a
+// gated layer) over k, and the floats of its workspace.
+int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
+{
+    const int64_t n = g->e.n * (g->gated ? 2 : 1);
+    g->tile = g->m > 64 && n > 64 ? kLarge : kSmall;
+    const TileSize t = f32 ? kTiles32[g->tile] : kTiles16[g->tile];
+    g->tm = ceil_div(g->m, t.m);
+    g->tn = ceil_div(n, t.n);
+    const int64_t steps = ceil_div(g->k, t.k), tiles = g->tm * g->tn;
+    int64_t splits = std::max<int64_t>(1, std::min(2 * ctx->num_cu / tiles, steps / 4));
+    const int64_t each = std::max<int64_t>(1, ceil_div(steps, splits));
+    splits = std::max<int64_t>(1, ceil_div(steps, each));
+    g->kper = each * t.k;
+    g->splits = (int32_t)splits;
+    g->ws = nullptr;
+    g->wn = (g->e.n + 3) / 4 * 4 * (g->gated ? 2 : 1);
+    return splits > 1 ? splits * g->m * g->wn : 0;
+}
+
+gs_status launch_mm(gs_ctx* ctx, int type, const LayerMm& g)
+{
+    if (g.m == 0 || g.e.n == 0) return GS_OK;
+    return type == GS_F32 ? launch_layer_mm_f32(ctx, g) :
+           type == GS_F16 ? launch_layer_mm_f16(ctx, g) : launch_layer_mm_bf16(ctx, g);
+}
+
+Operand operand(const void* p, int64_t ld, int64_t rows, int64_t gate = 0)
+{
+    return Operand{p, ld, rows, 1.0f, (int32_t)gate};
+}
+
+}  // namespace
+
+gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int act,
+                            const gs_tensor* residual, const gs_tensor* pre, const gs_tensor* out, bool gated,
+                            std::vector<GsAlloc>* tmp)
+{
+    LayerMm g{};
+    g.m = out->rows;
+    g.k = x->cols;
+    g.gated = gated;
+    g.a = operand(x->data, x->stride, x->rows);
+    g.b = operand(w->data, w->stride, w->rows, gated ? out->cols : 0);
+    g.e.n = out->cols;
+    g.e.act = act;
+    if (bias) g.e.bias = bias->data, g.e.bias_type = (int8_t)bias->type;
+    if (residual) g.e.res = residual->data, g.e.ldres = residual->stride, g.e.res_type = (int8_t)residual->type;
+    if (pre) g.e.pre = pre->data, g.e.ldpre = pre->stride, g.e.pre_type = (int8_t)pre->type;
+    g.e.out = out->data, g.e.ldout = out->stride, g.e.out_type = (int8_t)out->type;
+    if (g.m == 0 || g.e.n == 0) return GS_OK;
+    const int64_t ws = plan(ctx, x->type == GS_F32, &g);
+    if (ws && !(g.ws = (float*)gs_malloc(ctx, 4 * ws, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+    return launch_mm(ctx, x->type, g);
+}
+
+gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int act,
+                            const gs_tensor* dout, int accumulate, const gs_tensor* dx, const gs_tensor* dw,
+                            const gs_tensor* dbias, bool gated, std::vector<GsAlloc>* tmp)
+{
+    const int type = x->type;
+    const int64_t size = type == GS_F32 ? 4 : 2, m = x->rows, k = x->cols, n = w->rows;
+    // dz, the layer's dout itself where nothing changes it
+    const bool own = m * n > 0 && (gated || act != GS_ACT_NONE || dout->type != type) && (dx || dw);
+    DzJob z{};
+    int64_t row_blocks = 0;
+    if (own || (dbias && m > 0)) {
+        z.pre = pre ? pre->data : nullptr;
+        z.ldpre = pre ? pre->stride : 0;
+        z.dout = dout->data;
+        z.lddout = dout->stride;
+        z.dout_type = dout->type;
+        z.act = act;
+        z.m = m;
+        z.n = dout->cols;
+        const int64_t groups = ceil_div(z.n, 4);
+        z.tx = 64;
+        while (z.tx > 1 && z.tx / 2 >= groups) z.tx /= 2;
+        z.col_blocks = (int32_t)ceil_div(groups, z.tx);
+        const int ny = kDzThreads / z.tx;
+        z.rows = ceil_div(std::max<int64_t>(ceil_div(m * z.col_blocks, 2048), 4 * ny), ny) * ny;
+        row_blocks = ceil_div(m, z.rows);
+        if (own && !(z.dz = gs_malloc(ctx, m * n * size, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+        if (dbias && !(z.sums = (float*)gs_malloc(ctx, 4 * row_blocks * n, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+    }
+    const void* dz = own ? z.dz : dout->data;
+    const int64_t lddz = own ? n : dout->stride;
+    LayerMm gx{}, gw{};
+    int64_t ws = 0;
+    if (dx && m * k > 0) {
+        gx.m = m;
+        gx.k = n;
+        gx.b_col = true;
+        gx.a = operand(dz, lddz, m);
+        gx.b = operand(w->data, w->stride, k);
+        gx.e.n = k;
+        gx.e.out = dx->data, gx.e.ldout = dx->stride, gx.e.out_type = (int8_t)dx->type;
+        ws = std::max(ws, plan(ctx, type == GS_F32, &gx));
+    }
+    if (dw && n * k > 0) {
+        gw.m = n;
+        gw.k = m;
+        gw.a_col = gw.b_col = true;
+        gw.a = operand(dz, lddz, n);
+        gw.b = operand(x->data, x->stride, k);
+        gw.e.n = k;
+        gw.e.out = dw->data, gw.e.ldout = dw->stride, gw.e.out_type = (int8_t)dw->type;
+        if (accumulate) gw.e.res = dw->data, gw.e.ldres = dw->stride, gw.e.res_type = (int8_t)dw->type;
+        ws = std::max(ws, plan(ctx, type == GS_F32, &gw));
+    }
+    float* sums = nullptr;   // of both products, one after the other
+    if (ws && !(sums = (float*)gs_malloc(ctx, 4 * ws, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+    gx.ws = gw.ws = sums;
+
+    if (z.m > 0 && z.n > 0) {
+        GsTimerScope ts(ctx, "layer_dz");
+        const dim3 grid((uint32_t)(row_blocks * z.col_blocks)), block(kDzThreads);
+        auto go = [&](auto s) {
+            typedef decltype(s) S;
+            if (gated) hipLaunchKernelGGL((k_dz<S, true>), grid, block, 0, ctx->stream, z);
+            else hipLaunchKernelGGL((k_dz<S, false>), grid, block, 0, ctx->stream, z);
+        };
+        gst::with_type(type, go);
+        GS_HIP(ctx, hipGetLastError());
+    }
+    if (dbias && n > 0) {
+        GsTimerScope ts(ctx, "layer_dz");
+        gst::with_type(type, [&](auto s) {
+            hipLaunchKernelGGL((k_sum_rows<decltype(s)>), dim3((uint32_t)ceil_div(n, 64)), dim3(256), 0, ctx->stream,
+                               z.sums, row_blocks, n, dbias->data, dbias->type, accumulate);
+        });
+        GS_HIP(ctx, hipGetLastError());
+    }
+    gs_status st = GS_OK;
+    if (gw.m > 0) st = launch_mm(ctx, type, gw);
+    if (st == GS_OK && gx.m > 0) st = launch_mm(ctx, type, gx);
+    return st;
+}

@@ -1,5 +1,5 @@
-// tensors_api.cpp -- the C ABI of the table and tensor-list calls (declared in
-// include/gs.h): argument checks, workspaces and launches.
+// tensors_api.cpp -- the C ABI of the table, tensor-list and layer calls
+// (declared in include/gs.h): argument checks, workspaces and launches.
 #include <cmath>
 
 #include "gs_internal.h"
@@ -56,6 +56,19 @@ gs_status check_sizes(gs_ctx* ctx, const gs_tensor* a, const gs_tensor* b, const
     return GS_OK;
 }
 
+// a tensor that an update writes: of the parameter's sizes, contiguous, f32 unless it is a copy
+gs_status check_contiguous(gs_ctx* ctx, const gs_tensor* t, const gs_tensor* param, bool f32, const char* what,
+                           int32_t k)
+{
+    gs_status st = check_tensor(ctx, t, true, what, k);
+    if (st == GS_OK) st = check_sizes(ctx, param, t, what, k);
+    if (st != GS_OK) return st;
+    if (f32 && t->type != GS_F32) return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be GS_F32", what, k);
+    if (t->rows > 1 && t->cols > 0 && t->stride != t->cols)
+        return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be contiguous", what, k);
+    return GS_OK;
+}
+
 // Runs a launcher with a list of workspaces of its own, released in stream
 // order afterwards; no exception leaves.
 template <typename F>
@@ -85,6 +98,55 @@ gs_status check_norm_args(gs_ctx* ctx, const gs_tensor* grads, int32_t n, double
         if (total > (1ll << 42)) return gs_fail(ctx, GS_ERR_OVERFLOW, "more than 2^42 values");
     }
     return GS_OK;
+}
+
+// A tensor of a layer whose values have the type `type`, or GS_F32 where
+// `wide` allows it: rows x cols of a call.  NULL: not there.
+gs_status check_part(gs_ctx* ctx, const gs_tensor* t, bool written, int type, bool wide, int64_t rows, int64_t cols,
+                     const char* what)
+{
+    if (!t) return GS_OK;
+    const gs_status st = check_tensor(ctx, t, written, what);
+    if (st != GS_OK) return st;
+    if (t->type != type && !(wide && t->type == GS_F32))
+        return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s: element type %d with a layer of type %d", what, t->type, type);
+    if (t->rows != rows || t->cols != cols)
+        return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s is %lld x %lld, expected %lld x %lld", what, (long long)t->rows,
+                       (long long)t->cols, (long long)rows, (long long)cols);
+    return GS_OK;
+}
+
+// What every layer call checks: x (n x in), w (outs x in, or 2 outs x in when
+// gated), the activation and the n x outs tensor y (out or dout).
+gs_status check_layer(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, int32_t act, const gs_tensor* y,
+                      bool written, bool gated, const char* what)
+{
+    gs_status st = check_tensor(ctx, x, false, "x");
+    if (st == GS_OK) st = check_tensor(ctx, w, false, "w");
+    if (st == GS_OK) st = check_tensor(ctx, y, written, what);
+    if (st != GS_OK) return st;
+    if (act < GS_ACT_NONE || act > GS_ACT_SIGMOID) return gs_fail(ctx, GS_ERR_INVALID_ARG, "activation %d", act);
+    if (x->rows > kMaxIndex || x->cols > kMaxIndex || w->rows > kMaxIndex)
+        return gs_fail(ctx, GS_ERR_OVERFLOW, "a layer of %lld rows from %lld to %lld columns", (long long)x->rows,
+                       (long long)x->cols, (long long)w->rows);
+    if (gated && w->rows % 2) return gs_fail(ctx, GS_ERR_INVALID_ARG, "a gated layer's w has gate and up rows");
+    st = check_part(ctx, w, false, x->type, false, w->rows, x->cols, "w");
+    if (st == GS_OK) st = check_part(ctx, y, written, x->type, true, x->rows, w->rows / (gated ? 2 : 1), what);
+    return st;
+}
+
+gs_status check_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
+                           const gs_tensor* dout, const gs_tensor* dx, const gs_tensor* dw, const gs_tensor* dbias,
+                           bool gated)
+{
+    gs_status st = check_layer(ctx, x, w, act, dout, false, gated, "dout");
+    if (st != GS_OK) return st;
+    if (!pre && (gated || act != GS_ACT_NONE)) return gs_fail(ctx, GS_ERR_INVALID_ARG, "pre is NULL");
+    if (gated || act != GS_ACT_NONE) st = check_part(ctx, pre, false, x->type, false, x->rows, w->rows, "pre");
+    if (st == GS_OK) st = check_part(ctx, dx, true, x->type, false, x->rows, x->cols, "dx");
+    if (st == GS_OK) st = check_part(ctx, dw, true, x->type, true, w->rows, x->cols, "dw");
+    if (st == GS_OK) st = check_part(ctx, dbias, true, x->type, true, 1, w->rows, "dbias");
+    return st;
 }
 
 }  // namespace
@@ -168,13 +230,8 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
         const char* name[4] = {"parameter", "first moment", "second moment", "copy"};
         for (int q = 0; q < 4; ++q) {
             if (!own[q]) continue;
-            gs_status st = check_tensor(ctx, own[q], true, name[q], k);
-            if (st == GS_OK) st = check_sizes(ctx, params + k, own[q], name[q], k);
+            const gs_status st = check_contiguous(ctx, own[q], params + k, q < 3, name[q], k);
             if (st != GS_OK) return st;
-            if (q < 3 && own[q]->type != GS_F32)
-                return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be GS_F32", name[q], k);
-            if (own[q]->rows > 1 && own[q]->cols > 0 && own[q]->stride != own[q]->cols)
-                return gs_fail(ctx, GS_ERR_INVALID_ARG, "%s %d must be contiguous", name[q], k);
         }
         gs_status st = check_tensor(ctx, grads + k, false, "gradient", k);
         if (st == GS_OK) st = check_sizes(ctx, params + k, grads + k, "gradient", k);
@@ -184,6 +241,90 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
     }
     return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
         return launch_adam_list(ctx, params, m, v, grads, copies, n_tensors, opts, norm, tmp);
+    });
+}
+
+gs_status gs_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int32_t act,
+                        const gs_tensor* residual, const gs_tensor* pre, const gs_tensor* out)
+{
+    if (!ctx) return GS_ERR_INVALID_ARG;
+    gs_status st = check_layer(ctx, x, w, act, out, true, false, "out");
+    if (st == GS_OK) st = check_part(ctx, bias, false, x->type, true, 1, w->rows, "bias");
+    if (st == GS_OK) st = check_part(ctx, residual, false, x->type, true, x->rows, w->rows, "residual");
+    if (st == GS_OK) st = check_part(ctx, pre, true, x->type, false, x->rows, w->rows, "pre");
+    if (st != GS_OK) return st;
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_linear_fwd(ctx, x, w, bias, act, residual, pre, out, false, tmp);
+    });
+}
+
+gs_status gs_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
+                        const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw,
+                        const gs_tensor* dbias)
+{
+    if (!ctx) return GS_ERR_INVALID_ARG;
+    const gs_status st = check_linear_bwd(ctx, x, w, pre, act, dout, dx, dw, dbias, false);
+    if (st != GS_OK) return st;
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_linear_bwd(ctx, x, w, act == GS_ACT_NONE ? nullptr : pre, act, dout, accumulate != 0, dx, dw, dbias,
+                                 false, tmp);
+    });
+}
+
+gs_status gs_gated_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, int32_t act, const gs_tensor* pre,
+                       const gs_tensor* out)
+{
+    if (!ctx) return GS_ERR_INVALID_ARG;
+    gs_status st = check_layer(ctx, x, w, act, out, true, true, "out");
+    if (st == GS_OK) st = check_part(ctx, pre, true, x->type, false, x->rows, w->rows, "pre");
+    if (st != GS_OK) return st;
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_linear_fwd(ctx, x, w, nullptr, act, nullptr, pre, out, true, tmp);
+    });
+}
+
+gs_status gs_gated_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
+                       const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw)
+{
+    if (!ctx) return GS_ERR_INVALID_ARG;
+    const gs_status st = check_linear_bwd(ctx, x, w, pre, act, dout, dx, dw, nullptr, true);
+    if (st != GS_OK) return st;
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_linear_bwd(ctx, x, w, pre, act, dout, accumulate != 0, dx, dw, nullptr, true, tmp);
+    });
+}
+
+gs_status gs_muon_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor* m, const gs_tensor* grads,
+                          const gs_tensor* copies, int32_t n_tensors, const gs_muon_opts* opts, const float* norm)
+{
+    if (!ctx) return GS_ERR_INVALID_ARG;
+    if (n_tensors < 0 || (n_tensors > 0 && (!params || !m || !grads)) || !opts)
+        return gs_fail(ctx, GS_ERR_INVALID_ARG, "gs_muon_tensors arguments");
+    if (opts->steps < 0 || opts->steps > 20 || !(opts->momentum >= 0.0 && opts->momentum < 1.0) ||
+        !std::isfinite(opts->lr) || !std::isfinite(opts->weight_decay))
+        return gs_fail(ctx, GS_ERR_INVALID_ARG,
+                       "Muon options: 0 <= steps <= 20, 0 <= momentum < 1, lr and weight decay finite");
+    if (norm && (uintptr_t)norm % 4) return gs_fail(ctx, GS_ERR_INVALID_ARG, "norm pointer not aligned");
+    int64_t total = 0;
+    for (int32_t k = 0; k < n_tensors; ++k) {
+        const gs_tensor* own[3] = {params + k, m + k, copies && copies[k].data ? copies + k : nullptr};
+        const char* name[3] = {"parameter", "momentum", "copy"};
+        for (int q = 0; q < 3; ++q) {
+            if (!own[q]) continue;
+            gs_status st = check_contiguous(ctx, own[q], params + k, q < 2, name[q], k);
+            if (st != GS_OK) return st;
+        }
+        gs_status st = check_tensor(ctx, grads + k, false, "gradient", k);
+        if (st == GS_OK) st = check_sizes(ctx, params + k, grads + k, "gradient", k);
+        if (st != GS_OK) return st;
+        if (params[k].rows > (1 << 20) || params[k].cols > (1 << 20))
+            return gs_fail(ctx, GS_ERR_OVERFLOW, "matrix %d: %lld x %lld", k, (long long)params[k].rows,
+                           (long long)params[k].cols);
+        total += params[k].rows * params[k].cols;
+        if (total > (1ll << 42)) return gs_fail(ctx, GS_ERR_OVERFLOW, "more than 2^42 values");
+    }
+    return guarded(ctx, [&](std::vector<GsAlloc>* tmp) {
+        return launch_muon_list(ctx, params, m, grads, copies, n_tensors, opts, norm, tmp);
     });
 }
 

@@ -484,6 +484,88 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
                           const gs_tensor* grads, const gs_tensor* copies, int32_t n_tensors,
                           const gs_adam_opts* opts, const float* norm);
 
+/* ---- layers, and the update of their matrices ------------------------------ */
+
+/* A scene may also form its attributes with a small network: feature rows
+ * (looked up in a table, say) pass through linear and gated layers and become
+ * SH rows or opacity logits, whose gradient rows come back from the view.  The
+ * layers' matrices are updated by gs_muon_tensors, everything else by
+ * gs_adam_tensors.  The calls take any widths, and rows from one to millions.
+ *
+ * What is said above of the table and list calls holds for these too:
+ * asynchronous, workspaces allocated before the first launch, no copies
+ * between host and device, the same bits for the same inputs on the same
+ * device, streams.  Rows of different calls do not mix: an output row depends
+ * on its own input row and the weights alone.
+ *
+ * Types: x, w, pre and dx have one type T of GS_F32, GS_F16 and GS_BF16;
+ * out, residual, bias, dout, dw and dbias are T or GS_F32 each.  Sums are f32;
+ * every output is rounded once.  f32 values are multiplied as three bf16 parts
+ * each (six products; what is left out of x y is below 2^-22 |x y|); an f32
+ * value of x or w (or dz) that is not finite makes its results NaN. */
+enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3, GS_ACT_SIGMOID = 4 };
+
+/* out = act(z) + residual, z = x w^T + bias, with
+ *   relu max(z, 0), silu z s(z), sigmoid s(z), s(z) = 1 / (1 + exp(-z)),
+ *   gelu z s(2 sqrt(2 / pi) (z + 0.044715 z^3)) (the tanh form).
+ * x: n x in; w: outs x in (any stride, as every tensor that is only read);
+ * bias: 1 x outs or NULL; residual: n x outs or NULL; pre: n x outs or NULL:
+ * z rounded to T, for the backward pass; out: n x outs.  residual may be out
+ * itself (same data and stride); out and pre overlap nothing else.  Errors:
+ * INVALID_ARG, OVERFLOW (n, in or outs >= 2^31), OOM, DEVICE. */
+gs_status gs_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int32_t act,
+                        const gs_tensor* residual, const gs_tensor* pre, const gs_tensor* out);
+
+/* Gradients of gs_linear_fwd: dz = dout act'(pre) (relu'(0) = 0),
+ *   dx = dz w,  dw = dz^T x,  dbias = sum of dz over the rows,
+ * dw and dbias plus their old values when accumulate != 0.  The residual's
+ * gradient is dout.  pre: as written by gs_linear_fwd; not read (may be NULL)
+ * for GS_ACT_NONE.  dz is rounded to T for dx and dw, not for dbias.  dx, dw,
+ * dbias: each may be NULL: not wanted.  Without rows, dw and dbias are zero (or
+ * stay).  An output overlaps no input and no other output.  Errors: as
+ * gs_linear_fwd. */
+gs_status gs_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
+                        const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw,
+                        const gs_tensor* dbias);
+
+/* A gated pair of projections: [g u] = x w^T, out = act(g) u.  w: 2 outs x in,
+ * the outs rows of g, then those of u; pre: n x 2 outs or NULL: [g u] rounded
+ * to T; out: n x outs.  Sizes 2 outs < 2^31; else as gs_linear_fwd. */
+gs_status gs_gated_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, int32_t act, const gs_tensor* pre,
+                       const gs_tensor* out);
+
+/* Gradients of gs_gated_fwd: dg = dout u act'(g), du = dout act(g),
+ *   dx = [dg du] w,  dw = [dg du]^T x (plus the old dw when accumulate != 0).
+ * dg and du are rounded to T.  pre is required.  Else as gs_linear_bwd. */
+gs_status gs_gated_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
+                       const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw);
+
+typedef struct {
+    int32_t steps;             /* Newton-Schulz steps, 0..20 (5 usual)        */
+    int32_t nesterov;          /* 1: u = g' + momentum m, 0: u = m            */
+    double lr, momentum, weight_decay;
+} gs_muon_opts;
+
+/* One Muon step over a list of n_tensors matrices: momentum, whose matrix is
+ * orthogonalised by Newton-Schulz products, with decoupled weight decay:
+ *   g' = f g,  m = momentum m + g',  u = g' + momentum m  (or m),
+ *   X = u / (|u| + 1e-7)  (|u|: Frobenius norm),
+ *   steps times:  G = X X^T,  X = a X + (b G + c G G) X
+ *                 with a, b, c = 3.4445, -4.7750, 2.0315
+ *                 (singular values of X go towards [0.68, 1.21]; for a matrix
+ *                 of more rows than columns the same with X^T),
+ *   p = p (1 - lr weight_decay) - lr sqrt(max(1, rows / cols)) X,
+ * f = norm[1] where norm is given (as by gs_grad_norm), else 1; when norm[0] is
+ * not finite nothing is changed.  params, m: GS_F32, contiguous; grads: any type,
+ * may be strided; copies: as in gs_adam_tensors.  Each tensor is one matrix of
+ * its own rows and cols; matrices of the same or different sizes share
+ * launches.  The products are formed to f32's accuracy (values in two f16
+ * parts, sums in f32).  A matrix whose u holds a value that is not finite
+ * gets parameters that are not.  Errors: INVALID_ARG, OVERFLOW (as
+ * gs_grad_norm, and rows or cols above 2^20), OOM, DEVICE. */
+gs_status gs_muon_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor* m, const gs_tensor* grads,
+                          const gs_tensor* copies, int32_t n_tensors, const gs_muon_opts* opts, const float* norm);
+
 /* ---- one whole view ---------------------------------------------------- */
 
 typedef struct {
