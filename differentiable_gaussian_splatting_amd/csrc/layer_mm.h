@@ -103,12 +103,23 @@ __device__ __forceinline__ void epilogue_gated(const Epilogue& e, int64_t m, int
     store4<S>(e.out, m * e.ldout + f, e.out_type, valid, y);
 }
 
+// A wave's LDS writes are there for its own reads.
+__device__ __forceinline__ void wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Tiles of the product, each over one of `splits` ranges of k; with more than
 // one, the sums go to ws [split][m][wn] and k_join adds them up.
 template <typename S, int P, bool ACOL, bool BCOL, bool GATED, typename T>
-__global__ __launch_bounds__(T::NT) void k_layer_mm(const LayerMm g)
+__global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
 {
-    __shared__ Lds<S, P, T> lds;
+    constexpr int kCols = T::NI * (GATED ? 8 : 16), kRow = T::NI * 16 + 4;   // of a wave's results; padded row in LDS
+    __shared__ union {
+        Lds<S, P, T> tile;
+        float out[T::NT / 64 * 32 * kRow];
+    } lds;
     const int64_t tiles = g.tm * g.tn, total = tiles * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
@@ -122,28 +133,40 @@ __global__ __launch_bounds__(T::NT) void k_layer_mm(const LayerMm g)
 #pragma unroll
             for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (b != (int64_t)blockIdx.x) __syncthreads();   // the previous tile's reads of lds
-        mm_tile<S, P, ACOL, BCOL, T>(g.a, g.b, m0, n0, k0, min(g.k, k0 + g.kper), lds, acc);
-        const int64_t mw = m0 + (wave % T::WM) * T::MI * 16 + (lane & 15);
-        const int64_t nw = n0 / (GATED ? 2 : 1) + (wave / T::WM) * T::NI * (GATED ? 8 : 16) + (lane >> 4) * 4;
+        mm_tile<S, P, ACOL, BCOL, T>(g.a, g.b, m0, n0, k0, min(g.k, k0 + g.kper), lds.tile, acc);
+        // The results go through LDS, 32 rows of each wave at a time, so that a
+        // lane takes four columns next to its neighbours' (whole lines are
+        // read and written) and the epilogue's code is a loop.
+        __syncthreads();
+        float* mine = reinterpret_cast<float*>(&lds) + wave * 32 * kRow;
+        const int64_t mw = m0 + (wave % T::WM) * T::MI * 16;
+        const int64_t nw = n0 / (GATED ? 2 : 1) + (wave / T::WM) * kCols;
 #pragma unroll
-        for (int r = 0; r < T::MI; ++r) {
-            const int64_t m = mw + r * 16;
-            if (m >= g.m) continue;
+        for (int r = 0; r < T::MI; r += 2) {
+            if (mw + r * 16 >= g.m) break;
 #pragma unroll
-            for (int q = 0; q < T::NI; q += GATED ? 2 : 1) {
-                const int64_t n = nw + q * (GATED ? 8 : 16);
-                if (n >= g.e.n) continue;
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < T::NI; ++q)
+                    *reinterpret_cast<f32x4*>(mine + (h * 16 + (lane & 15)) * kRow + q * 16 + (lane >> 4) * 4) = acc[q][r + h];
+            wave_fence();
+            for (int t = lane; t < 32 * kCols / 4; t += 64) {
+                const int row = t / (kCols / 4), c = t % (kCols / 4) * 4;
+                const int64_t m = mw + r * 16 + row, n = nw + c;
+                if (m >= g.m || n >= g.e.n) continue;
+                const float* v = mine + row * kRow + (GATED ? (c >> 4) * 32 + (c & 15) : c);
+                const f32x4 x = *reinterpret_cast<const f32x4*>(v);
                 if (g.splits > 1) {
                     float* w = g.ws + (s * g.m + m) * g.wn + n;
-                    gst::store<float, 4>(w, __builtin_bit_cast(Four, acc[q][r]));
-                    if constexpr (GATED)
-                        gst::store<float, 4>(w + g.wn / 2, __builtin_bit_cast(Four, acc[q + 1][r]));
+                    gst::store<float, 4>(w, __builtin_bit_cast(Four, x));
+                    if constexpr (GATED) gst::store<float, 4>(w + g.wn / 2, *reinterpret_cast<const Four*>(v + 16));
                 } else if constexpr (GATED) {
-                    epilogue_gated<S>(g.e, m, n, acc[q][r], acc[q + 1][r]);
+                    epilogue_gated<S>(g.e, m, n, x, *reinterpret_cast<const f32x4*>(v + 16));
                 } else {
-                    epilogue<S>(g.e, m, n, acc[q][r]);
+                    epilogue<S>(g.e, m, n, x);
                 }
             }
+            wave_fence();
         }
     }
 }
@@ -178,12 +201,14 @@ void launch_mode(gs_ctx* ctx, const LayerMm& g)
     else hipLaunchKernelGGL((k_layer_mm<S, P, false, false, false, T>), grid, block, 0, ctx->stream, g);
 }
 
-template <typename S, int P, typename Large, typename Small>
+template <typename S, int P, typename Large, typename Medium, typename Small, typename Tiny>
 gs_status launch_layer_mm(gs_ctx* ctx, const LayerMm& g)
 {
     GsTimerScope ts(ctx, "layer_mm");
     if (g.tile == kLarge) launch_mode<S, P, Large>(ctx, g);
-    else launch_mode<S, P, Small>(ctx, g);
+    else if (g.tile == kMedium) launch_mode<S, P, Medium>(ctx, g);
+    else if (g.tile == kSmall) launch_mode<S, P, Small>(ctx, g);
+    else launch_mode<S, P, Tiny>(ctx, g);
     if (g.splits > 1) {
         const dim3 grid((uint32_t)std::min(ceil_div(g.m * ((g.e.n + 3) / 4), 256), kMaxGrid)), block(256);
         if (g.gated) hipLaunchKernelGGL((k_join<S, true>), grid, block, 0, ctx->stream, g);

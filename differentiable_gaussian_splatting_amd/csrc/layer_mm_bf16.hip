@@ -5,7 +5,7 @@ namespace gsm {
 
 gs_status launch_layer_mm_bf16(gs_ctx* ctx, const LayerMm& g)
 {
-    return launch_layer_mm<bf16, 1, Tile<128, 128, 64, 2, 2, 2>, Tile<64, 64, 64, 2, 2, 2>>(ctx, g);
+    return launch_layer_mm<bf16, 1, Large16, Medium16, Small16, Tiny16>(ctx, g);
 }
 
 }  // namespace gsm

@@ -61,7 +61,9 @@ struct Epilogue {
     int8_t bias_type, res_type, pre_type, out_type;
 };
 
-enum { kLarge = 0, kSmall = 1 };   // tiles
+// The tiles of a product.  kTiny is for operands with fewer than 8 values side
+// by side (Stage in mm.h).
+enum { kLarge = 0, kMedium = 1, kSmall = 2, kTiny = 3 };
 
 struct LayerMm {
     Operand a, b;                // rows of out, columns of out
@@ -80,11 +82,13 @@ gs_status launch_layer_mm_f32(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_f16(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_bf16(gs_ctx* ctx, const LayerMm& g);
 
-// rows, columns and k step of each tile
-struct TileSize {
-    int m, n, k;
-};
-constexpr TileSize kTiles16[] = {{128, 128, 64}, {64, 64, 64}};
-constexpr TileSize kTiles32[] = {{128, 128, 32}, {64, 64, 32}};
+typedef Tile<256, 256, 64, 2, 4, 2> Large16;
+typedef Tile<128, 128, 64, 2, 2, 1> Medium16;
+typedef Tile<64, 64, 64, 2, 2, 2> Small16;
+typedef Tile<64, 64, 64, 2, 2, 2, true> Tiny16;
+typedef Tile<256, 128, 32, 4, 2, 2> Large32;
+typedef Tile<128, 128, 32, 2, 2, 1> Medium32;
+typedef Tile<64, 64, 32, 2, 2, 2> Small32;
+typedef Tile<64, 64, 32, 2, 2, 2, true> Tiny32;
 
 }  // namespace gsm

@@ -103,24 +103,58 @@ __global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ sums
     }
 }
 
+// What a block of each tile takes for one step of k when `slots` of them run at
+// once (measured on large products: 256 x 256 x 64 at 900 TFLOP/s, 128 x 128 x
+// 64 at 740; f32: 256 x 128 x 32 at 205, 128 x 128 x 32 at 195).
+struct TileCost {
+    int32_t m, n, k, per_cu;
+    double step_us;
+};
+template <typename T>
+constexpr TileCost cost(int per_cu, double step_us)
+{
+    return TileCost{T::BM, T::BN, T::BK, per_cu, step_us};
+}
+constexpr TileCost kCost16[] = {cost<Large16>(1, 2.4), cost<Medium16>(2, 1.45), cost<Small16>(3, 0.9),
+                                cost<Tiny16>(3, 0.9)};
+constexpr TileCost kCost32[] = {cost<Large32>(1, 2.6), cost<Medium32>(2, 2.7), cost<Small32>(3, 1.3),
+                                cost<Tiny32>(3, 1.3)};
+constexpr double kJoinUs = 4.0;          // a further launch
+constexpr double kJoinRate = 4e6;        // bytes per us of sums written and read
+
 // Tiles and splits of a product of m x n (n of the tiles: both halves of a
-// gated layer) over k, and the floats of its workspace.
+// gated layer) over k, those that the costs above make fastest, and the floats
+// of its workspace.
 int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
 {
-    const int64_t n = g->e.n * (g->gated ? 2 : 1);
-    g->tile = g->m > 64 && n > 64 ? kLarge : kSmall;
-    const TileSize t = f32 ? kTiles32[g->tile] : kTiles16[g->tile];
-    g->tm = ceil_div(g->m, t.m);
-    g->tn = ceil_div(n, t.n);
-    const int64_t steps = ceil_div(g->k, t.k), tiles = g->tm * g->tn;
-    int64_t splits = std::max<int64_t>(1, std::min(2 * ctx->num_cu / tiles, steps / 4));
-    const int64_t each = std::max<int64_t>(1, ceil_div(steps, splits));
-    splits = std::max<int64_t>(1, ceil_div(steps, each));
-    g->kper = each * t.k;
-    g->splits = (int32_t)splits;
+    const int64_t n = g->e.n * (g->gated ? 2 : 1), wn = (g->e.n + 3) / 4 * 4 * (g->gated ? 2 : 1);
+    const bool tiny = (!g->a_col && g->k < 8) || (g->a_col && g->m < 8) || (!g->b_col && g->k < 8) ||
+                      (g->b_col && g->e.n < 8);
+    double best = 0.0;
+    int64_t best_each = 1;
+    for (int t = tiny ? kTiny : kLarge; t <= (tiny ? kTiny : kSmall); ++t) {
+        const TileCost& c = f32 ? kCost32[t] : kCost16[t];
+        const int64_t tiles = ceil_div(g->m, c.m) * ceil_div(n, c.n), steps = std::max<int64_t>(1, ceil_div(g->k, c.k));
+        const int64_t slots = (int64_t)c.per_cu * ctx->num_cu;
+        for (int64_t s = 1; s <= steps; s += std::max<int64_t>(1, s / 4)) {
+            if (s > 1 && (tiles * s > 2 * slots || s * g->m * wn > (1ll << 28))) break;
+            const int64_t each = ceil_div(steps, s);
+            const double us = (double)ceil_div(tiles * s, slots) * (each + 1) * c.step_us +
+                              (s > 1 ? kJoinUs + 8.0 * s * g->m * wn / kJoinRate : 0.0);
+            if (best > 0.0 && us >= best) continue;
+            best = us;
+            best_each = each;
+            g->tile = t;
+        }
+    }
+    const TileCost& c = f32 ? kCost32[g->tile] : kCost16[g->tile];
+    g->tm = ceil_div(g->m, c.m);
+    g->tn = ceil_div(n, c.n);
+    g->kper = best_each * c.k;
+    g->splits = (int32_t)std::max<int64_t>(1, ceil_div(g->k, g->kper));
     g->ws = nullptr;
-    g->wn = (g->e.n + 3) / 4 * 4 * (g->gated ? 2 : 1);
-    return splits > 1 ? splits * g->m * g->wn : 0;
+    g->wn = wn;
+    return g->splits > 1 ? g->splits * g->m * wn : 0;
 }
 
 gs_status launch_mm(gs_ctx* ctx, int type, const LayerMm& g)

@@ -4,10 +4,11 @@
 // Operands.  Each is a matrix in memory whose k either runs along the rows
 // ("row": value (r, k) at p[r ld + k]) or down the columns ("col": at
 // p[k ld + r]), so that x w^T, dz w and dz^T x all read their operands where
-// they are: nothing is transposed in memory.  A thread loads 8 values of k
-// (row), or 8 x 4 values (col) that it turns round in registers, and writes
-// them to LDS as 16-byte chunks of consecutive k, the form that a lane of the
-// matrix instruction takes.
+// they are: nothing is transposed in memory.  A thread loads 8 neighbouring
+// values and writes them to LDS as one 16-byte chunk.  A lane of the matrix
+// instruction takes 8 consecutive k of one r: a chunk of a row tile, or two
+// transposing LDS reads of a col tile, in which each group of 16 lanes fetches
+// 4 k x 16 r and every lane receives its r's 4 values.
 //
 // Types.  16-bit values are multiplied as they are (products are exact in f32,
 // sums are f32).  f32 values are split into parts whose products run at the
@@ -22,12 +23,13 @@
 //          2^-25 below that).  Three products (h h, h l, l h).  For the
 //          Newton-Schulz products, whose values are bounded.
 //
-// LDS holds each tile as rows of BK values; chunk c of row r stands at place
-// c ^ f(r), f from the low four bits of r, so that the 16 lanes that read one
-// chunk of 16 rows, and the lanes that write chunks of every fourth row, meet
-// different banks.  A tile's successor is loaded into registers while the
-// matrix instructions run and is written to the other LDS buffer afterwards
-// (one barrier per BK).
+// LDS holds a row tile as rows of BK values, with chunk c of row r at place
+// c ^ f(r), f from the low four bits of r: the 16 lanes that read one chunk of
+// 16 rows meet different banks.  It holds a col tile as BK rows of R values,
+// with 16-value unit q of row k at place q ^ h(k), so that the 16 rows of k
+// that a transposing read touches spread over the banks.  A tile's successor
+// is loaded into registers while the matrix instructions run and is written to
+// the other LDS buffer afterwards (one barrier per BK).
 #pragma once
 
 #include "gs_tensor.h"
@@ -47,8 +49,9 @@ struct Operand {
     int32_t gate;     // > 0: row r of the tile is a gate or an up row (see row_of_tile)
 };
 
-template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_>
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, bool TINY_ = false>
 struct Tile {
+    static constexpr bool TINY = TINY_;   // operands with fewer than 8 values of k or columns (see Stage)
     static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, STAGES = STAGES_;
     static constexpr int NT = WM * WN * 64;
     static constexpr int MI = BM / WM / 16, NI = BN / WN / 16;   // 16 x 16 results of a wave
@@ -98,12 +101,18 @@ __device__ __forceinline__ void split(const S (&v)[8], float scale, gst::Pack<ty
     }
 }
 
-// place of chunk c in row r of an LDS tile
+// place of chunk c in row r of a row tile
 template <int BK>
 __device__ __forceinline__ int place(int r, int c)
 {
     if constexpr (BK == 64) return c ^ ((r & 7) ^ ((r >> 3) & 1));
     else return c ^ (((r >> 1) & 3) ^ ((r >> 3) & 1));
+}
+// what is xored into the 16-value unit of row k of a col tile of R values
+template <int R>
+__device__ __forceinline__ int unit_swap(int k)
+{
+    return ((k & 3) | ((k >> 1) & 4)) & (R / 16 - 1);
 }
 
 // The matrix row that row r of a tile starting at n0 stands for.  With
@@ -116,81 +125,122 @@ __device__ __forceinline__ int64_t row_of_tile(const Operand& o, int64_t n0, int
     return min(f, (int64_t)o.gate - 1) + ((r >> 4) & 1) * (int64_t)o.gate;
 }
 
-// One operand's way from memory to LDS: R rows of BK values per step.
-template <typename S, int P, int R, int BK, int NT, bool COL>
+// v moved down by n places (zeros follow), n >= 0
+__device__ __forceinline__ void move_down(float (&v)[8], int n)
+{
+#pragma unroll
+    for (int step = 4; step; step >>= 1)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[j] = n & step ? (j + step < 8 ? v[j + step < 8 ? j + step : 0] : 0.0f) : v[j];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[j] = n >= 8 ? 0.0f : v[j];
+}
+template <typename S>
+__device__ __forceinline__ void move_down(S (&v)[8], int n)
+{
+    uint64_t lo, hi;
+    __builtin_memcpy(&lo, &v[0], 8);
+    __builtin_memcpy(&hi, &v[4], 8);
+    if (n >= 4) {
+        lo = hi;
+        hi = 0;
+    }
+    const int bits = (n & 3) * 16;
+    lo = n >= 8 ? 0 : (lo >> bits) | (hi << 1 << (63 - bits));
+    hi = hi >> bits;
+    __builtin_memcpy(&v[0], &lo, 8);
+    __builtin_memcpy(&v[4], &hi, 8);
+}
+
+// One operand's way from memory to LDS: R rows (or columns) of BK values per
+// step, in units of 8 neighbouring values of k (row) or r (col).  A unit that
+// would reach over the end of k or over the last column is read from 8 values
+// before that end and moved down in its registers: one load either way.  So
+// there have to be 8 values of k (row) or 8 columns (col); TINY tiles, for
+// operands that have fewer, read value by value instead.
+template <typename S, int P, int R, int BK, int NT, bool COL, bool TINY>
 struct Stage {
     typedef typename Part<S, P>::E E;
-    static constexpr int kChunks = BK / 8;
-    static constexpr int kUnits = COL ? R * BK / 32 : R * BK / 8;
+    static constexpr int kSide = (COL ? R : BK) / 8;   // units side by side
+    static constexpr int kStep = NT / kSide;           // rows (of k, where col) from a thread's unit to its next
+    static constexpr int kUnits = R * BK / 8;
     static constexpr int kPer = (kUnits + NT - 1) / NT;
     static constexpr bool kExact = kUnits % NT == 0;
-    const S* at[kPer];    // the unit's first value at k = 0
-    int64_t ld;
-    int edge;             // COL: bit u: unit u reaches over the last column
-    int64_t left[COL ? kPer : 1];
+    const S* at;          // the thread's first unit at k = 0
+    const S* p;
+    int64_t ld, rows, r0;
     float scale;
-    S v[kPer][COL ? 8 : 1][COL ? 4 : 8];
+    int32_t gate;
+    int32_t over;         // col: places that the thread's units reach over the last column
+    S v[kPer][8];
+    static_assert(NT % kSide == 0, "a thread's units share their columns");
+    static_assert(COL || kStep % 32 == 0 || kPer == 1, "gate and up rows alternate by 16");
 
     __device__ __forceinline__ bool mine(int u) const { return kExact || (int)threadIdx.x + u * NT < kUnits; }
+    __device__ __forceinline__ static int side() { return threadIdx.x % kSide; }
+    __device__ __forceinline__ static int row(int u) { return threadIdx.x / kSide + u * kStep; }
 
-    __device__ __forceinline__ void init(const Operand& o, int64_t r0)
+    __device__ __forceinline__ void init(const Operand& o, int64_t tile0)
     {
         ld = o.ld;
-        edge = 0;
+        rows = o.rows;
         scale = o.scale;
-#pragma unroll
-        for (int u = 0; u < kPer; ++u) {
-            const int id = (threadIdx.x + u * NT) % (kExact ? 1 << 30 : kUnits);
-            if constexpr (COL) {
-                const int64_t r = r0 + (id % (R / 4)) * 4;
-                const int64_t c = min(r, o.rows - 1);
-                at[u] = (const S*)o.p + (int64_t)(id / (R / 4)) * 8 * ld + c;
-                left[u] = o.rows - 1 - c;      // columns after it
-                if (left[u] < 3) edge |= 1 << u;
-            } else {
-                at[u] = (const S*)o.p + row_of_tile(o, r0, id / kChunks) * ld + (id % kChunks) * 8;
-            }
+        gate = o.gate;
+        r0 = tile0;
+        p = (const S*)o.p;
+        over = 0;
+        if constexpr (COL) {
+            const int64_t r = r0 + side() * 8, from = TINY ? min(r, rows - 1) : min(r, rows - 8);
+            over = (int)min((int64_t)8, TINY ? 8 - (rows - from) : r - from);
+            at = p + (int64_t)row(0) * ld + from;
+        } else {
+            at = p + row_of_tile(o, r0, row(0)) * ld + side() * 8;
         }
     }
 
-    // the values of k in [k, k + BK); TAIL: those from kend on are zero
-    template <bool TAIL>
+    // The values of k in [k, k + BK).  EDGE: those from kend on are zero, and
+    // the tile may reach over the last row or column (what it holds there is
+    // any of the operand's values).
+    template <bool EDGE>
     __device__ __forceinline__ void load(int64_t k, int64_t kend)
     {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             if (!mine(u)) continue;
-            const int id = threadIdx.x + u * NT;
             if constexpr (COL) {
-                const int64_t kk = k + (id / (R / 4)) * 8;
-                const S* p = at[u] + k * ld;
+                const int64_t kk = k + row(u);
+                const S* q = at + (k + u * kStep) * ld;
+                if (EDGE && kk >= kend) {
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    if (TAIL && kk + q >= kend) {
+                    for (int j = 0; j < 8; ++j) v[u][j] = (S)0.0f;
+                } else if (TINY) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[u][q][j] = (S)0.0f;
-                    } else if (!((edge >> u) & 1)) {
-                        const gst::Pack<S, 4> x = gst::load<S, 4>(p + q * ld);
+                    for (int j = 0; j < 8; ++j) v[u][j] = q[min(j, 7 - over)];
+                } else {
+                    take(u, q);
+                    if (EDGE && over) move_down(v[u], over);
+                }
+            } else if constexpr (EDGE) {
+                const int64_t kk = k + side() * 8, n = kk + 8 - kend;
+                const Operand o = {nullptr, ld, rows, scale, gate};
+                const S* q = p + row_of_tile(o, r0, row(u)) * ld + kk;
+                if (TINY) {
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) v[u][q][j] = x.v[j];
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) v[u][q][j] = p[q * ld + min((int64_t)j, left[u])];
-                    }
+                    for (int j = 0; j < 8; ++j) v[u][j] = kk + j < kend ? q[j] : (S)0.0f;
+                } else {
+                    take(u, q - max(n, (int64_t)0));
+                    if (n > 0) move_down(v[u], (int)min(n, (int64_t)8));
                 }
             } else {
-                const int64_t kk = k + (id % kChunks) * 8;
-                const S* p = at[u] + k;
-                if (!TAIL || kk + 8 <= kend) {
-                    const gst::Pack<S, 8> x = gst::load<S, 8>(p);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[u][0][j] = x.v[j];
-                } else {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[u][0][j] = kk + j < kend ? p[j] : (S)0.0f;
-                }
+                take(u, at + k + u * (gate ? kStep / 2 : kStep) * ld);
             }
         }
+    }
+    __device__ __forceinline__ void take(int u, const S* q)
+    {
+        const gst::Pack<S, 8> x = gst::load<S, 8>(q);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) v[u][j] = x.v[j];
     }
 
     // to LDS: plane p of the tile at lds + p R BK
@@ -199,21 +249,52 @@ struct Stage {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             if (!mine(u)) continue;
-            const int id = threadIdx.x + u * NT;
+            const int r = row(u), c = side();
+            const int to = COL ? r * R + ((c >> 1) ^ unit_swap<R>(r)) * 16 + (c & 1) * 8 : r * BK + place<BK>(r, c) * 8;
+            gst::Pack<E, 8> part[P];
+            split<S, P>(v[u], scale, part);
 #pragma unroll
-            for (int j = 0; j < (COL ? 4 : 1); ++j) {
-                S x[8];
+            for (int p = 0; p < P; ++p)
+                *reinterpret_cast<gst::Pack<E, 8>*>(__builtin_assume_aligned(lds + p * R * BK + to, 16)) = part[p];
+        }
+    }
+};
+
+// A wave's N blocks of 16 rows (columns) of a tile, as matrix operands.
+template <typename E, int P, int R, int BK, int N, bool COL>
+struct Fragments {
+    int base[COL ? N : BK / 32];
+
+    // r0: the wave's first row, a multiple of 16
+    __device__ __forceinline__ void init(int r0, int lane)
+    {
+        if constexpr (COL) {
+            const int k = (lane >> 4) * 8 + ((lane >> 2) & 3);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) x[q] = COL ? v[u][COL ? q : 0][COL ? j : 0] : v[u][0][COL ? 0 : q];
-                const int r = COL ? (id % (R / 4)) * 4 + j : id / kChunks;
-                const int c = COL ? id / (R / 4) : id % kChunks;
-                gst::Pack<E, 8> part[P];
-                split<S, P>(x, scale, part);
+            for (int i = 0; i < N; ++i) base[i] = k * R + ((r0 / 16 + i) ^ unit_swap<R>(k)) * 16 + (lane & 3) * 4;
+        } else {
+            const int r = r0 + (lane & 15);
 #pragma unroll
-                for (int p = 0; p < P; ++p)
-                    *reinterpret_cast<gst::Pack<E, 8>*>(__builtin_assume_aligned(
-                        lds + p * R * BK + r * BK + place<BK>(r, c) * 8, 16)) = part[p];
-            }
+            for (int kk = 0; kk < BK / 32; ++kk) base[kk] = r * BK + place<BK>(r, kk * 4 + (lane >> 4)) * 8;
+        }
+    }
+
+    // block i at k = 32 kk of plane p
+    __device__ __forceinline__ gst::Pack<E, 8> get(const E* lds, int p, int i, int kk) const
+    {
+        if constexpr (COL) {
+            typedef short v4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) v4* at;
+            const E* q = lds + p * R * BK + kk * 32 * R + base[i];
+            const v4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)q);
+            const v4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(q + 4 * R));
+            gst::Pack<E, 8> both;
+            __builtin_memcpy(&both.v[0], &lo, 8);
+            __builtin_memcpy(&both.v[4], &hi, 8);
+            return both;
+        } else {
+            return *reinterpret_cast<const gst::Pack<E, 8>*>(
+                __builtin_assume_aligned(lds + p * R * BK + base[kk] + i * 16 * BK, 16));
         }
     }
 };
@@ -234,12 +315,19 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
     typedef typename Part<S, P>::E E;
     constexpr int BK = T::BK;
     if (k0 >= k1) return;
-    Stage<S, P, T::BM, BK, T::NT, ACOL> sa;
-    Stage<S, P, T::BN, BK, T::NT, BCOL> sb;
+    Stage<S, P, T::BM, BK, T::NT, ACOL, T::TINY> sa;
+    Stage<S, P, T::BN, BK, T::NT, BCOL, T::TINY> sb;
     sa.init(A, m0);
     sb.init(B, n0);
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    Fragments<E, P, T::BM, BK, T::MI, ACOL> fa;
+    Fragments<E, P, T::BN, BK, T::NI, BCOL> fb;
+    fa.init((wave % T::WM) * T::MI * 16, lane);
+    fb.init((wave / T::WM) * T::NI * 16, lane);
+    const int64_t bn = B.gate ? T::BN / 2 : T::BN, n1 = B.gate ? n0 / 2 : n0;
+    const bool edge = m0 + T::BM > A.rows || n1 + bn > (B.gate ? B.gate : B.rows);
     auto load = [&](int64_t k) {
-        if (k + BK <= k1) {
+        if (k + BK <= k1 && !edge) {
             sb.template load<false>(k, k1);
             sa.template load<false>(k, k1);
         } else {
@@ -250,9 +338,6 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
     load(k0);
     sb.commit(lds.b[0]);
     sa.commit(lds.a[0]);
-
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int am = (wave % T::WM) * T::MI * 16 + (lane & 15), bn = (wave / T::WM) * T::NI * 16 + (lane & 15);
     int buf = 0;
     for (int64_t k = k0; k < k1; k += BK) {
         __syncthreads();
@@ -261,33 +346,28 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
         const E *la = lds.a[buf], *lb = lds.b[buf];
 #pragma unroll
         for (int kk = 0; kk < BK / 32; ++kk) {
-            gst::Pack<E, 8> fa[P][T::MI], fb[P][T::NI];
-            const int ca = place<BK>(am, kk * 4 + (lane >> 4)) * 8, cb = place<BK>(bn, kk * 4 + (lane >> 4)) * 8;
+            gst::Pack<E, 8> a[P][T::MI], b[P][T::NI];
 #pragma unroll
             for (int p = 0; p < P; ++p) {
 #pragma unroll
-                for (int i = 0; i < T::NI; ++i)
-                    fb[p][i] = *reinterpret_cast<const gst::Pack<E, 8>*>(
-                        __builtin_assume_aligned(lb + p * T::BN * BK + (bn + i * 16) * BK + cb, 16));
+                for (int i = 0; i < T::NI; ++i) b[p][i] = fb.get(lb, p, i, kk);
 #pragma unroll
-                for (int j = 0; j < T::MI; ++j)
-                    fa[p][j] = *reinterpret_cast<const gst::Pack<E, 8>*>(
-                        __builtin_assume_aligned(la + p * T::BM * BK + (am + j * 16) * BK + ca, 16));
+                for (int j = 0; j < T::MI; ++j) a[p][j] = fa.get(la, p, j, kk);
             }
 #pragma unroll
             for (int i = 0; i < T::NI; ++i)
 #pragma unroll
                 for (int j = 0; j < T::MI; ++j) {
                     if constexpr (P == 3) {
-                        acc[i][j] = mfma(fb[2][i], fa[0][j], acc[i][j]);
-                        acc[i][j] = mfma(fb[0][i], fa[2][j], acc[i][j]);
-                        acc[i][j] = mfma(fb[1][i], fa[1][j], acc[i][j]);
+                        acc[i][j] = mfma(b[2][i], a[0][j], acc[i][j]);
+                        acc[i][j] = mfma(b[0][i], a[2][j], acc[i][j]);
+                        acc[i][j] = mfma(b[1][i], a[1][j], acc[i][j]);
                     }
                     if constexpr (P >= 2) {
-                        acc[i][j] = mfma(fb[1][i], fa[0][j], acc[i][j]);
-                        acc[i][j] = mfma(fb[0][i], fa[1][j], acc[i][j]);
+                        acc[i][j] = mfma(b[1][i], a[0][j], acc[i][j]);
+                        acc[i][j] = mfma(b[0][i], a[1][j], acc[i][j]);
                     }
-                    acc[i][j] = mfma(fb[0][i], fa[0][j], acc[i][j]);
+                    acc[i][j] = mfma(b[0][i], a[0][j], acc[i][j]);
                 }
         }
         if constexpr (T::STAGES == 2) buf ^= 1;

@@ -166,8 +166,10 @@ __global__ __launch_bounds__(kThreads) void k_apply(const Job job, const MuonCon
 enum { kGram, kPoly, kNext };
 
 // One tile of a matrix's product: G (kGram), P from G (kPoly) or the next X.
+// G and P are symmetric: their tiles on and below the diagonal are computed and
+// those below it written to both places.
 template <int KIND, bool TALL, typename T>
-__global__ __launch_bounds__(T::NT) void k_newton(const MmJob job, const float* __restrict__ from, float* __restrict__ to,
+__global__ __launch_bounds__(T::NT, 2) void k_newton(const MmJob job, const float* __restrict__ from, float* __restrict__ to,
                                                   const float* __restrict__ poly)
 {
     constexpr bool ACOL = KIND == kGram && TALL, BCOL = ACOL || (KIND == kNext && !TALL);
@@ -179,7 +181,17 @@ __global__ __launch_bounds__(T::NT) void k_newton(const MmJob job, const float* 
     const int64_t m = KIND == kNext ? t.rows : side, n = KIND == kNext ? t.cols : side;
     const int64_t k = KIND == kGram ? length : side;
     int64_t i, j;
-    tile_at(b - before, (m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, i, j);
+    if constexpr (KIND == kNext) {
+        tile_at(b - before, (m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, i, j);
+    } else {
+        static_assert(T::BM == T::BN, "square tiles");
+        const int t = (int)(b - before);
+        int r = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
+        while (r * (r + 1) / 2 > t) --r;
+        while ((r + 1) * (r + 2) / 2 <= t) ++r;
+        i = r;
+        j = t - r * (r + 1) / 2;
+    }
     const float* src = from + (KIND == kPoly ? t.s : t.x);
     const Operand x = {src, KIND == kPoly ? side : t.cols, KIND == kPoly ? side : KIND == kGram ? side : TALL ? m : n,
                        kScaleX, 0};
@@ -223,34 +235,78 @@ __global__ __launch_bounds__(T::NT) void k_newton(const MmJob job, const float* 
                 for (int w = 0; w < 4; ++w)
                     if (w < valid) dst[at + w] = y[w];
             }
+            if (KIND != kNext && i != j) {
+#pragma unroll
+                for (int w = 0; w < 4; ++w)
+                    if (w < valid) dst[(col + w) * n + row] = y[w];
+            }
         }
     }
 }
 
-typedef Tile<128, 128, 32, 2, 2, 2> Large;
+typedef Tile<256, 256, 32, 2, 4, 2> Large;
+typedef Tile<128, 128, 32, 2, 2, 1> Medium;
+typedef Tile<64, 64, 32, 2, 2, 2> Small;
+typedef Tile<64, 64, 32, 2, 2, 2, true> Tiny;
+
+// tiles of a matrix's product
+template <int KIND>
+int64_t tiles_of(const Matrix& t, int bm, int bn)
+{
+    const int64_t side = std::min(t.rows, t.cols), s = ceil_div(side, bm);
+    return KIND == kNext ? ceil_div(t.rows, bm) * ceil_div(t.cols, bn) : s * (s + 1) / 2;
+}
 
 template <int KIND, bool TALL, typename T>
-void launch_newton(gs_ctx* ctx, const Job& job, const float* from, float* to, const float* poly)
+void launch_tiles(gs_ctx* ctx, const Job& job, const float* from, float* to, const float* poly)
 {
     MmJob mm{};
     uint32_t tiles = 0;
     for (int32_t k = 0; k < job.count; ++k) {
         const Matrix& t = job.t[k];
-        const int64_t side = std::min(t.rows, t.cols);
-        const int64_t m = KIND == kNext ? t.rows : side, n = KIND == kNext ? t.cols : side;
-        tiles += (uint32_t)(ceil_div(m, T::BM) * ceil_div(n, T::BN));
+        tiles += (uint32_t)tiles_of<KIND>(t, T::BM, T::BN);
         mm.t[mm.count++] = Shape{t.x, t.s, t.rows, t.cols, tiles};
     }
     hipLaunchKernelGGL((k_newton<KIND, TALL, T>), dim3(tiles), dim3(T::NT), 0, ctx->stream, mm, from, to, poly);
 }
 
+// What a group's product takes with a tile of which per_cu blocks run on a
+// compute unit, each in step_us for 32 values of k (large matrices: 256 x 256
+// at 345 TFLOP/s, 128 x 128 at 295).
+template <int KIND, typename T>
+double cost_us(const gs_ctx* ctx, const Job& job, int per_cu, double step_us)
+{
+    int64_t work = 0, longest = 0, tiles = 0;
+    for (int32_t k = 0; k < job.count; ++k) {
+        const Matrix& t = job.t[k];
+        const int64_t steps = ceil_div(KIND == kGram ? std::max(t.rows, t.cols) : std::min(t.rows, t.cols), T::BK);
+        const int64_t n = tiles_of<KIND>(t, T::BM, T::BN);
+        tiles += n;
+        work += n * steps;
+        longest = std::max(longest, steps);
+    }
+    const double rounds = (double)ceil_div(tiles, (int64_t)per_cu * ctx->num_cu);
+    return rounds * std::max((double)work / (double)tiles, (double)longest / rounds) * step_us;
+}
+
+template <int KIND, bool TALL>
+void launch_newton(gs_ctx* ctx, const Job& job, bool tiny, const float* from, float* to, const float* poly)
+{
+    if (tiny) return launch_tiles<KIND, TALL, Tiny>(ctx, job, from, to, poly);
+    const double large = cost_us<KIND, Large>(ctx, job, 1, 3.1), medium = cost_us<KIND, Medium>(ctx, job, 2, 1.8),
+                 small = cost_us<KIND, Small>(ctx, job, 3, 0.9);
+    if (large <= medium && large <= small) launch_tiles<KIND, TALL, Large>(ctx, job, from, to, poly);
+    else if (medium <= small) launch_tiles<KIND, TALL, Medium>(ctx, job, from, to, poly);
+    else launch_tiles<KIND, TALL, Small>(ctx, job, from, to, poly);
+}
+
 template <bool TALL>
-void newton_schulz(gs_ctx* ctx, const Job& job, int steps, float** x, float** other, float* gram, float* poly)
+void newton_schulz(gs_ctx* ctx, const Job& job, bool tiny, int steps, float** x, float** other, float* gram, float* poly)
 {
     for (int s = 0; s < steps; ++s) {
-        launch_newton<kGram, TALL, Large>(ctx, job, *x, gram, nullptr);
-        launch_newton<kPoly, TALL, Large>(ctx, job, gram, poly, nullptr);
-        launch_newton<kNext, TALL, Large>(ctx, job, *x, *other, poly);
+        launch_newton<kGram, TALL>(ctx, job, tiny, *x, gram, nullptr);
+        launch_newton<kPoly, TALL>(ctx, job, tiny, gram, poly, nullptr);
+        launch_newton<kNext, TALL>(ctx, job, tiny, *x, *other, poly);
         std::swap(*x, *other);
     }
 }
@@ -260,7 +316,7 @@ struct Group {
     Job job;
     int64_t x, s;
     uint32_t pieces;
-    bool tall;
+    bool tall, tiny;              // more rows than columns; a side below 8 (Stage in mm.h)
 };
 constexpr int64_t kGroupValues = 1 << 27;   // of X: one 512 MB workspace, of which a step needs four
 
@@ -273,15 +329,17 @@ gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
     const MuonConst c = {(float)o->momentum, (float)o->lr, (float)(1.0 - o->lr * o->weight_decay), o->nesterov};
     std::vector<Group> groups;
     int64_t x = 0, s = 0, pieces = 0;
-    for (int tall = 0; tall < 2; ++tall) {
+    for (int kind = 0; kind < 4; ++kind) {
+        const bool tall = kind & 1, tiny = kind & 2;
         bool open = false;
         for (int32_t k = 0; k < n; ++k) {
             const int64_t rows = p[k].rows, cols = p[k].cols, values = rows * cols, side = std::min(rows, cols);
-            if (values == 0 || (rows > cols) != (tall == 1)) continue;
+            if (values == 0 || (rows > cols) != tall || (side < 8) != tiny) continue;
             if (open && (groups.back().job.count == kGroup || groups.back().x + values > kGroupValues)) open = false;
             if (!open) {
                 groups.push_back(Group{});
                 groups.back().tall = tall;
+                groups.back().tiny = tiny;
                 open = true;
             }
             Group& q = groups.back();
@@ -308,8 +366,8 @@ gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
         const dim3 grid(q.pieces), block(kThreads);
         hipLaunchKernelGGL(k_momentum, grid, block, 0, ctx->stream, q.job, c, norm, part);
         hipLaunchKernelGGL(k_start, grid, block, 0, ctx->stream, q.job, c, norm, part, now);
-        if (q.tall) newton_schulz<true>(ctx, q.job, o->steps, &now, &other, ss, ss + s);
-        else newton_schulz<false>(ctx, q.job, o->steps, &now, &other, ss, ss + s);
+        if (q.tall) newton_schulz<true>(ctx, q.job, q.tiny, o->steps, &now, &other, ss, ss + s);
+        else newton_schulz<false>(ctx, q.job, q.tiny, o->steps, &now, &other, ss, ss + s);
         hipLaunchKernelGGL(k_apply, grid, block, 0, ctx->stream, q.job, c, norm, now);
         GS_HIP(ctx, hipGetLastError());
     }
