@@ -81,6 +81,9 @@ struct LayerMm {
 gs_status launch_layer_mm_f32(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_f16(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_bf16(gs_ctx* ctx, const LayerMm& g);
+// x w^T of few rows (layer_few.hip)
+bool few_rows(const LayerMm& g);
+gs_status launch_layer_few(gs_ctx* ctx, int type, const LayerMm& g);
 
 typedef Tile<256, 256, 64, 2, 4, 2> Large16;
 typedef Tile<128, 128, 64, 2, 2, 1> Medium16;
