@@ -103,22 +103,24 @@ __global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ sums
     }
 }
 
-// What a block of each tile takes for one step of k when `slots` of them run at
-// once (measured on large products: 256 x 256 x 64 at 900 TFLOP/s, 128 x 128 x
-// 64 at 740; f32: 256 x 128 x 32 at 205, 128 x 128 x 32 at 195).
+// What n tiles on each compute unit take for one step of k: once us for
+// every round of `resident` blocks and each us for every tile (measured, with
+// one to eight tiles a unit: 128 x 128 x 64 takes 1.0, 1.45 and 2.25 us for
+// one, two and three, 64 x 64 x 64 0.72, 1.2 and 2.2 for two, four and eight,
+// 256 x 256 x 64 2.4 for one).
 struct TileCost {
-    int32_t m, n, k, per_cu;
-    double step_us;
+    int32_t m, n, k, resident;
+    double once, each;
 };
 template <typename T>
-constexpr TileCost cost(int per_cu, double step_us)
+constexpr TileCost cost(int resident, double once, double each)
 {
-    return TileCost{T::BM, T::BN, T::BK, per_cu, step_us};
+    return TileCost{T::BM, T::BN, T::BK, resident, once, each};
 }
-constexpr TileCost kCost16[] = {cost<Large16>(1, 2.4), cost<Medium16>(2, 1.45), cost<Small16>(3, 0.9),
-                                cost<Tiny16>(3, 0.9)};
-constexpr TileCost kCost32[] = {cost<Large32>(1, 2.6), cost<Medium32>(2, 2.7), cost<Small32>(3, 1.3),
-                                cost<Tiny32>(3, 1.3)};
+constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.3), cost<Medium16>(2, 0.5, 0.48), cost<Small16>(5, 0.2, 0.25),
+                                cost<Tiny16>(3, 0.3, 0.3)};
+constexpr TileCost kCost32[] = {cost<Large32>(1, 0.1, 2.5), cost<Medium32>(2, 0.5, 1.35), cost<Small32>(3, 0.3, 0.48),
+                                cost<Tiny32>(3, 0.4, 0.5)};
 constexpr double kJoinUs = 4.0;          // a further launch
 constexpr double kJoinRate = 4e6;        // bytes per us of sums written and read
 
@@ -135,11 +137,12 @@ int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
     for (int t = tiny ? kTiny : kLarge; t <= (tiny ? kTiny : kSmall); ++t) {
         const TileCost& c = f32 ? kCost32[t] : kCost16[t];
         const int64_t tiles = ceil_div(g->m, c.m) * ceil_div(n, c.n), steps = std::max<int64_t>(1, ceil_div(g->k, c.k));
-        const int64_t slots = (int64_t)c.per_cu * ctx->num_cu;
+        const int64_t slots = (int64_t)c.resident * ctx->num_cu;
         for (int64_t s = 1; s <= steps; s += std::max<int64_t>(1, s / 4)) {
             if (s > 1 && (tiles * s > 2 * slots || s * g->m * wn > (1ll << 28))) break;
             const int64_t each = ceil_div(steps, s);
-            const double us = (double)ceil_div(tiles * s, slots) * (each + 1) * c.step_us +
+            const double us = (double)(each + 1) * (ceil_div(tiles * s, slots) * c.once +
+                                                    ceil_div(tiles * s, ctx->num_cu) * c.each) +
                               (s > 1 ? kJoinUs + 8.0 * s * g->m * wn / kJoinRate : 0.0);
             if (best > 0.0 && us >= best) continue;
             best = us;

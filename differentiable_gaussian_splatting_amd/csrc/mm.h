@@ -32,6 +32,8 @@
 // the other LDS buffer afterwards (one barrier per BK).
 #pragma once
 
+#include <type_traits>
+
 #include "gs_tensor.h"
 
 namespace gsm {
@@ -49,6 +51,7 @@ struct Operand {
     int32_t gate;     // > 0: row r of the tile is a gate or an up row (see row_of_tile)
 };
 
+// BM x BN results of WM x WN waves, BK values of k a step, in STAGES LDS buffers
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int STAGES_, bool TINY_ = false>
 struct Tile {
     static constexpr bool TINY = TINY_;   // operands with fewer than 8 values of k or columns (see Stage)
@@ -198,9 +201,9 @@ struct Stage {
         }
     }
 
-    // The values of k in [k, k + BK).  EDGE: those from kend on are zero, and
-    // the tile may reach over the last row or column (what it holds there is
-    // any of the operand's values).
+    // Loads the values of k in [k, k + BK).  EDGE: k + BK may lie behind kend,
+    // and the tile may reach over the last row or column (what it holds there
+    // is any of the operand's values).  Nothing here waits for what it loads.
     template <bool EDGE>
     __device__ __forceinline__ void load(int64_t k, int64_t kend)
     {
@@ -208,48 +211,56 @@ struct Stage {
         for (int u = 0; u < kPer; ++u) {
             if (!mine(u)) continue;
             if constexpr (COL) {
-                const int64_t kk = k + row(u);
-                const S* q = at + (k + u * kStep) * ld;
-                if (EDGE && kk >= kend) {
+                const int64_t kk = EDGE ? min(k + row(u), kend - 1) - row(0) : k + u * kStep;
+                if constexpr (TINY) {
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) v[u][j] = (S)0.0f;
-                } else if (TINY) {
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) v[u][j] = q[min(j, 7 - over)];
+                    for (int j = 0; j < 8; ++j) v[u][j] = at[kk * ld + min(j, 7 - over)];
                 } else {
-                    take(u, q);
-                    if (EDGE && over) move_down(v[u], over);
+                    take(v[u], at + kk * ld);
                 }
             } else if constexpr (EDGE) {
-                const int64_t kk = k + side() * 8, n = kk + 8 - kend;
+                const int64_t kk = k + side() * 8;
                 const Operand o = {nullptr, ld, rows, scale, gate};
                 const S* q = p + row_of_tile(o, r0, row(u)) * ld + kk;
-                if (TINY) {
+                if constexpr (TINY) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) v[u][j] = kk + j < kend ? q[j] : (S)0.0f;
                 } else {
-                    take(u, q - max(n, (int64_t)0));
-                    if (n > 0) move_down(v[u], (int)min(n, (int64_t)8));
+                    take(v[u], q - max(kk + 8 - kend, (int64_t)0));
                 }
             } else {
-                take(u, at + k + u * (gate ? kStep / 2 : kStep) * ld);
+                take(v[u], at + k + u * (gate ? kStep / 2 : kStep) * ld);
             }
         }
     }
-    __device__ __forceinline__ void take(int u, const S* q)
+    __device__ __forceinline__ static void take(S (&v)[8], const S* q)
     {
         const gst::Pack<S, 8> x = gst::load<S, 8>(q);
 #pragma unroll
-        for (int j = 0; j < 8; ++j) v[u][j] = x.v[j];
+        for (int j = 0; j < 8; ++j) v[j] = x.v[j];
     }
 
-    // to LDS: plane p of the tile at lds + p R BK
-    __device__ __forceinline__ void commit(E* lds) const
+    // To LDS: plane p of the tile at lds + p R BK.  EDGE: with the values that
+    // a unit has brought from before an end moved down, and zeros from `left`
+    // values of k on.
+    template <bool EDGE>
+    __device__ __forceinline__ void commit(E* lds, int64_t left)
     {
 #pragma unroll
         for (int u = 0; u < kPer; ++u) {
             if (!mine(u)) continue;
             const int r = row(u), c = side();
+            if constexpr (EDGE && COL) {
+                if (r >= left) {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) v[u][j] = (S)0.0f;
+                } else if (!TINY && over) {
+                    move_down(v[u], over);
+                }
+            } else if constexpr (EDGE && !TINY) {
+                const int64_t n = c * 8 + 8 - left;
+                if (n > 0) move_down(v[u], (int)min(n, (int64_t)8));
+            }
             const int to = COL ? r * R + ((c >> 1) ^ unit_swap<R>(r)) * 16 + (c & 1) * 8 : r * BK + place<BK>(r, c) * 8;
             gst::Pack<E, 8> part[P];
             split<S, P>(v[u], scale, part);
@@ -326,56 +337,62 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
     fb.init((wave / T::WM) * T::NI * 16, lane);
     const int64_t bn = B.gate ? T::BN / 2 : T::BN, n1 = B.gate ? n0 / 2 : n0;
     const bool edge = m0 + T::BM > A.rows || n1 + bn > (B.gate ? B.gate : B.rows);
-    auto load = [&](int64_t k) {
-        if (k + BK <= k1 && !edge) {
-            sb.template load<false>(k, k1);
-            sa.template load<false>(k, k1);
-        } else {
-            sb.template load<true>(k, k1);
-            sa.template load<true>(k, k1);
+    int buf = 0;
+    // steps from `from` up to `to`, both loops' code apart: what the edges need
+    // would cost the whole tiles' loop its registers
+    auto steps = [&](auto is_edge, int64_t from, int64_t to) {
+        constexpr bool EDGE = decltype(is_edge)::value;
+        sb.template load<EDGE>(from, to);
+        sa.template load<EDGE>(from, to);
+        sb.template commit<EDGE>(lds.b[buf], to - from);
+        sa.template commit<EDGE>(lds.a[buf], to - from);
+        for (int64_t k = from; k < to; k += BK) {
+            __syncthreads();
+            const bool more = k + BK < to;
+            if (more) {
+                sb.template load<EDGE>(k + BK, to);
+                sa.template load<EDGE>(k + BK, to);
+            }
+            const E *la = lds.a[buf], *lb = lds.b[buf];
+#pragma unroll
+            for (int kk = 0; kk < BK / 32; ++kk) {
+                gst::Pack<E, 8> a[P][T::MI], b[P][T::NI];
+#pragma unroll
+                for (int p = 0; p < P; ++p) {
+#pragma unroll
+                    for (int i = 0; i < T::NI; ++i) b[p][i] = fb.get(lb, p, i, kk);
+#pragma unroll
+                    for (int j = 0; j < T::MI; ++j) a[p][j] = fa.get(la, p, j, kk);
+                }
+#pragma unroll
+                for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+                    for (int j = 0; j < T::MI; ++j) {
+                        if constexpr (P == 3) {
+                            acc[i][j] = mfma(b[2][i], a[0][j], acc[i][j]);
+                            acc[i][j] = mfma(b[0][i], a[2][j], acc[i][j]);
+                            acc[i][j] = mfma(b[1][i], a[1][j], acc[i][j]);
+                        }
+                        if constexpr (P >= 2) {
+                            acc[i][j] = mfma(b[1][i], a[0][j], acc[i][j]);
+                            acc[i][j] = mfma(b[0][i], a[1][j], acc[i][j]);
+                        }
+                        acc[i][j] = mfma(b[0][i], a[0][j], acc[i][j]);
+                    }
+            }
+            if constexpr (T::STAGES == 2) buf ^= 1;
+            else __syncthreads();
+            if (more) {
+                sb.template commit<EDGE>(lds.b[buf], to - k - BK);
+                sa.template commit<EDGE>(lds.a[buf], to - k - BK);
+            }
         }
     };
-    load(k0);
-    sb.commit(lds.b[0]);
-    sa.commit(lds.a[0]);
-    int buf = 0;
-    for (int64_t k = k0; k < k1; k += BK) {
-        __syncthreads();
-        const bool more = k + BK < k1;
-        if (more) load(k + BK);
-        const E *la = lds.a[buf], *lb = lds.b[buf];
-#pragma unroll
-        for (int kk = 0; kk < BK / 32; ++kk) {
-            gst::Pack<E, 8> a[P][T::MI], b[P][T::NI];
-#pragma unroll
-            for (int p = 0; p < P; ++p) {
-#pragma unroll
-                for (int i = 0; i < T::NI; ++i) b[p][i] = fb.get(lb, p, i, kk);
-#pragma unroll
-                for (int j = 0; j < T::MI; ++j) a[p][j] = fa.get(la, p, j, kk);
-            }
-#pragma unroll
-            for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-                for (int j = 0; j < T::MI; ++j) {
-                    if constexpr (P == 3) {
-                        acc[i][j] = mfma(b[2][i], a[0][j], acc[i][j]);
-                        acc[i][j] = mfma(b[0][i], a[2][j], acc[i][j]);
-                        acc[i][j] = mfma(b[1][i], a[1][j], acc[i][j]);
-                    }
-                    if constexpr (P >= 2) {
-                        acc[i][j] = mfma(b[1][i], a[0][j], acc[i][j]);
-                        acc[i][j] = mfma(b[0][i], a[1][j], acc[i][j]);
-                    }
-                    acc[i][j] = mfma(b[0][i], a[0][j], acc[i][j]);
-                }
-        }
-        if constexpr (T::STAGES == 2) buf ^= 1;
-        else __syncthreads();
-        if (more) {
-            sb.commit(lds.b[buf]);
-            sa.commit(lds.a[buf]);
-        }
+    const int64_t whole = edge ? k0 : k0 + (k1 - k0) / BK * BK;
+    if (whole > k0) steps(std::false_type{}, k0, whole);
+    if (whole < k1) {
+        if (whole > k0) __syncthreads();
+        steps(std::true_type{}, whole, k1);
     }
 }
 

@@ -338,11 +338,12 @@ void launch_tiles(gs_ctx* ctx, const Group& q, const float* from, float* to, con
                            dim3(kThreads), 0, ctx->stream, to, q.s, splits);
 }
 
-// What a group's product takes with a tile of which per_cu blocks run on a
-// compute unit, each in step_us for 32 values of k (large matrices: 256 x 256
-// at 345 TFLOP/s, 128 x 128 at 295).
+// What a group's product takes with a tile: for a step of 32 values of k,
+// once us for every round of `resident` tiles on each compute unit and each us
+// for every tile (measured: 128 x 128 takes 1.3 and 2.0 us for one and two a
+// unit, 64 x 64 0.9, 1.5 and 3.1 for two, four and eight, 256 x 256 3.1).
 template <int KIND, typename T>
-double cost_us(const gs_ctx* ctx, const Job& job, int splits, int per_cu, double step_us)
+double cost_us(const gs_ctx* ctx, const Job& job, int splits, int resident, double once, double each)
 {
     int64_t work = 0, longest = 0, tiles = 0;
     for (int32_t k = 0; k < job.count; ++k) {
@@ -350,19 +351,21 @@ double cost_us(const gs_ctx* ctx, const Job& job, int splits, int per_cu, double
         const int64_t steps = ceil_div(ceil_div(KIND == kGram ? std::max(t.rows, t.cols) : std::min(t.rows, t.cols), T::BK), splits);
         const int64_t n = tiles_of<KIND>(t, T::BM, T::BN) * splits;
         tiles += n;
-        work += n * steps;
-        longest = std::max(longest, steps);
+        work += n * (steps + 1);
+        longest = std::max(longest, steps + 1);
     }
-    const double rounds = (double)ceil_div(tiles, (int64_t)per_cu * ctx->num_cu);
-    return rounds * std::max((double)work / (double)tiles, (double)longest / rounds) * step_us;
+    const int64_t rounds = ceil_div(tiles, (int64_t)resident * ctx->num_cu), on_each = ceil_div(tiles, ctx->num_cu);
+    return std::max((double)work / (double)tiles * ((double)rounds * once + (double)on_each * each),
+                    (double)longest * (once + each));
 }
 
 // the cheapest tile, and its cost
 template <int KIND>
 int choose_tile(const gs_ctx* ctx, const Job& job, int splits, double* us)
 {
-    const double cost[3] = {cost_us<KIND, Large>(ctx, job, splits, 1, 3.1), cost_us<KIND, Medium>(ctx, job, splits, 2, 1.8),
-                            cost_us<KIND, Small>(ctx, job, splits, 3, 0.9)};
+    const double cost[3] = {cost_us<KIND, Large>(ctx, job, splits, 1, 0.1, 3.0),
+                            cost_us<KIND, Medium>(ctx, job, splits, 2, 0.5, 0.75),
+                            cost_us<KIND, Small>(ctx, job, splits, 5, 0.25, 0.33)};
     int best = 0;
     for (int k = 1; k < 3; ++k)
         if (cost[k] < cost[best]) best = k;
