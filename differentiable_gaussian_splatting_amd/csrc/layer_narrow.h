@@ -1,0 +1,366 @@
+// layer_narrow.h -- linear layers between narrow rows (features of a Gaussian
+// to its attributes), of any number of rows: the weights stay in registers and
+// the rows stream by, so that memory alone counts.
+//
+// A wave takes 16 rows at a time (32 in the 16-bit backward pass) straight from
+// memory in the layout of the matrix instruction (lane: row l % 16, 16 bytes of
+// it at k = 16 bytes x (l / 16)), with the next rows on their way meanwhile.
+//   forward:  out = act(x w^T + bias) + residual, one read of x, one write of out.
+//   backward: dz is formed from dout and pre as they are read; it is an operand
+//             of dx = dz w as it stands, and passes through a piece of LDS of the
+//             wave's own, as x does, to be read down its columns for dw = dz^T x
+//             and summed for dbias.  So dout, pre and x are read once, dx is
+//             written once, dz never.  The waves' sums of dw and dbias are added
+//             up in the block, and the blocks' by a second launch, in order.
+// f32 uses the f32 matrix instruction (exact products; at these widths its rate
+// is above what memory feeds it).
+#pragma once
+
+#include "layer_mm.h"
+
+namespace gsm {
+
+// 16 x 16 results from 16 bytes of k per lane
+__device__ __forceinline__ f32x4 mfma16(gst::Pack<float, 4> a, gst::Pack<float, 4> b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+    return c;
+}
+template <typename E>
+__device__ __forceinline__ f32x4 mfma16(gst::Pack<E, 8> a, gst::Pack<E, 8> b, f32x4 c)
+{
+    return mfma(a, b, c);
+}
+
+// N values from p on, zeros from the n-th one on (n may be negative)
+template <typename S, int N>
+__device__ __forceinline__ gst::Pack<S, N> upto(const S* p, int64_t n)
+{
+    if (n >= N) return gst::load<S, N>(p);
+    gst::Pack<S, N> v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v.v[j] = j < n ? p[j] : (S)0.0f;
+    return v;
+}
+
+// N values of f32 or S, as f32
+template <typename S, int N>
+__device__ __forceinline__ void load_f32(const void* p, int64_t at, int type, int64_t valid, float (&v)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; j += 4) {
+        const int n = (int)min((int64_t)4, valid - j);
+        const f32x4 x = n > 0 ? load4<S>(p, at + j, type, n) : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[j + q] = x[q];
+    }
+}
+
+constexpr int kNarrowThreads = 256;
+
+template <typename S, int KS, int NI>
+__global__ __launch_bounds__(kNarrowThreads) void k_narrow_fwd(const LayerMm g)
+{
+    constexpr int N = 16 / sizeof(S), kStep = 4 * N;
+    const int lane = threadIdx.x & 63, k0 = (lane >> 4) * N;
+    gst::Pack<S, N> b[NI][KS];
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const S* w = (const S*)g.b.p + min((int64_t)(i * 16 + (lane & 15)), g.e.n - 1) * g.b.ld;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) b[i][s] = upto<S, N>(w + s * kStep + k0, g.k - s * kStep - k0);
+    }
+    const int64_t groups = (g.m + 15) / 16, stride = (int64_t)gridDim.x * (kNarrowThreads / 64);
+    int64_t at = (int64_t)blockIdx.x * (kNarrowThreads / 64) + (threadIdx.x >> 6);
+    gst::Pack<S, N> a[KS], next[KS];
+    auto load = [&](int64_t group, gst::Pack<S, N>(&v)[KS]) {
+        const S* x = (const S*)g.a.p + min(group * 16 + (lane & 15), g.m - 1) * g.a.ld;
+#pragma unroll
+        for (int s = 0; s < KS; ++s) v[s] = upto<S, N>(x + s * kStep + k0, g.k - s * kStep - k0);
+    };
+    if (at < groups) load(at, a);
+    for (; at < groups; at += stride) {
+        if (at + stride < groups) load(at + stride, next);
+        const int64_t m = at * 16 + (lane & 15);
+#pragma unroll
+        for (int i = 0; i < NI; ++i) {
+            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s) acc = mfma16(b[i][s], a[s], acc);
+            const int64_t n = i * 16 + (lane >> 4) * 4;
+            if (m < g.m && n < g.e.n) epilogue<S>(g.e, m, n, acc);
+        }
+#pragma unroll
+        for (int s = 0; s < KS; ++s) a[s] = next[s];
+    }
+}
+
+// What the backward pass of a narrow layer reads and writes; f values of dz and
+// k of x a row.
+struct NarrowBwd {
+    const void *x, *w, *pre, *dout;
+    void* dx;                       // null: not wanted
+    float* sums;                    // [blocks][f k + f]: dw, then dbias; null: neither is wanted
+    int64_t ldx, ldw, ldpre, lddout, lddx;
+    int64_t m;
+    int32_t f, k, act, dout_type;
+};
+
+template <typename S, int FI, int KI>
+struct NarrowSize {
+    static constexpr int N = 16 / sizeof(S), kStep = 4 * N;          // values of a lane; of a step along a row
+    static constexpr int kRows = sizeof(S) == 4 ? 16 : 32;           // of an iteration
+    static constexpr int FS = (FI * 16 + kStep - 1) / kStep, XS = (KI * 16 + kStep - 1) / kStep;
+    // rows of LDS: columns of 16 neighbouring rows are read at once (f32: 4
+    // rows x 16 columns, which 16 words modulo 64 keep apart)
+    static constexpr int pad(int cols) { return sizeof(S) == 4 ? cols + (80 - cols % 64) % 64 : cols + 8; }
+    static constexpr int ldz = pad(FS * kStep), ldx = pad(XS * kStep);
+};
+
+// A wave's rows on their way
+template <typename S, int FI, int KI>
+struct NarrowRows {
+    typedef NarrowSize<S, FI, KI> Z;
+    float d[Z::kRows / 16][Z::FS][Z::N];
+    gst::Pack<S, Z::N> z[Z::kRows / 16][Z::FS], x[Z::kRows / 16][Z::XS];
+
+    __device__ __forceinline__ void load(const NarrowBwd& g, int64_t row0, int lane)
+    {
+        const int at = (lane >> 4) * Z::N;
+#pragma unroll
+        for (int h = 0; h < Z::kRows / 16; ++h) {
+            const int64_t m = row0 + h * 16 + (lane & 15);
+            const bool there = m < g.m;
+            const int64_t r = there ? m : g.m - 1;
+#pragma unroll
+            for (int s = 0; s < Z::FS; ++s) {
+                const int c = s * Z::kStep + at;
+                load_f32<S, Z::N>(g.dout, r * g.lddout + c, g.dout_type, there ? g.f - c : 0, d[h][s]);
+                if (g.act != GS_ACT_NONE)
+                    z[h][s] = upto<S, Z::N>((const S*)g.pre + r * g.ldpre + c, there ? g.f - c : 0);
+            }
+            if (g.sums) {
+#pragma unroll
+                for (int s = 0; s < Z::XS; ++s) {
+                    const int c = s * Z::kStep + at;
+                    x[h][s] = upto<S, Z::N>((const S*)g.x + r * g.ldx + c, there ? g.k - c : 0);
+                }
+            }
+        }
+    }
+};
+
+// acc += 16 columns of x (from cx on) and of dz (from cz on) over a wave's rows
+template <typename S, typename Z>
+__device__ __forceinline__ f32x4 column_product(const S* x, int cx, const S* z, int cz, int lane, f32x4 acc)
+{
+    if constexpr (sizeof(S) == 4) {
+#pragma unroll
+        for (int q = 0; q < Z::kRows / 4; ++q) {
+            const int r = q * 4 + (lane >> 4);
+            acc = __builtin_amdgcn_mfma_f32_16x16x4f32(x[r * Z::ldx + cx + (lane & 15)], z[r * Z::ldz + cz + (lane & 15)],
+                                                       acc, 0, 0, 0);
+        }
+        return acc;
+    } else {
+        auto part = [&](const S* p, int ld, int c) {
+            typedef short v4 __attribute__((ext_vector_type(4)));
+            typedef __attribute__((address_space(3))) v4* at;
+            const S* q = p + ((lane >> 4) * 8 + ((lane >> 2) & 3)) * ld + c + (lane & 3) * 4;
+            const v4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)q);
+            const v4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((at)(q + 4 * ld));
+            gst::Pack<S, 8> both;
+            __builtin_memcpy(&both.v[0], &lo, 8);
+            __builtin_memcpy(&both.v[4], &hi, 8);
+            return both;
+        };
+        return mfma(part(x, Z::ldx, cx), part(z, Z::ldz, cz), acc);
+    }
+}
+
+template <typename S, int FI, int KI>
+__global__ __launch_bounds__(kNarrowThreads) void k_narrow_bwd(const NarrowBwd g)
+{
+    typedef NarrowSize<S, FI, KI> Z;
+    constexpr int W = kNarrowThreads / 64, N = Z::N;
+    __shared__ __align__(16) union {
+        S rows[W][Z::kRows * (Z::ldz + Z::ldx)];
+        float sums[FI * KI * 256 + FI * 16];
+    } lds;
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, at = (lane >> 4) * N;
+    gst::Pack<S, N> w[KI][Z::FS];   // w^T as an operand: row k, values of f
+    if (g.dx) {
+#pragma unroll
+        for (int i = 0; i < KI; ++i) {
+            const int k = min(i * 16 + (lane & 15), g.k - 1);
+#pragma unroll
+            for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int f = s * Z::kStep + at + j;
+                    w[i][s].v[j] = f < g.f ? ((const S*)g.w)[(int64_t)f * g.ldw + k] : (S)0.0f;
+                }
+        }
+    }
+    f32x4 dw[FI][KI];
+#pragma unroll
+    for (int f = 0; f < FI; ++f)
+#pragma unroll
+        for (int k = 0; k < KI; ++k) dw[f][k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    float db[Z::FS][N];
+#pragma unroll
+    for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+        for (int j = 0; j < N; ++j) db[s][j] = 0.0f;
+    S* const lz = lds.rows[wave];
+    S* const lx = lz + Z::kRows * Z::ldz;
+    const int64_t stride = (int64_t)gridDim.x * W * Z::kRows;
+    int64_t row0 = ((int64_t)blockIdx.x * W + wave) * Z::kRows;
+    NarrowRows<S, FI, KI> now, next;
+    if (row0 < g.m) now.load(g, row0, lane);
+    for (; row0 < g.m; row0 += stride) {
+        if (row0 + stride < g.m) next.load(g, row0 + stride, lane);
+#pragma unroll
+        for (int h = 0; h < Z::kRows / 16; ++h) {
+            gst::Pack<S, N> dz[Z::FS];
+#pragma unroll
+            for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    float v = now.d[h][s][j];
+                    if (g.act != GS_ACT_NONE) v *= act_both((float)now.z[h][s].v[j], g.act).y;
+                    // past the last value of a row, and past the last row, pre is 0 and dout too
+                    db[s][j] += v;
+                    dz[s].v[j] = gst::narrow<S>(v);
+                }
+            if (g.dx) {
+                const int64_t m = row0 + h * 16 + (lane & 15);
+#pragma unroll
+                for (int i = 0; i < KI; ++i) {
+                    f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int s = 0; s < Z::FS; ++s) acc = mfma16(w[i][s], dz[s], acc);
+                    const int c = i * 16 + (lane >> 4) * 4;
+                    if (m < g.m && c < g.k) store4<S>(g.dx, m * g.lddx + c, sizeof(S) == 4 ? GS_F32 : -1, g.k - c, acc);
+                }
+            }
+            if (g.sums) {
+                const int r = h * 16 + (lane & 15);
+#pragma unroll
+                for (int s = 0; s < Z::FS; ++s)
+                    *reinterpret_cast<gst::Pack<S, N>*>(__builtin_assume_aligned(lz + r * Z::ldz + s * Z::kStep + at, 16)) = dz[s];
+#pragma unroll
+                for (int s = 0; s < Z::XS; ++s)
+                    *reinterpret_cast<gst::Pack<S, N>*>(__builtin_assume_aligned(lx + r * Z::ldx + s * Z::kStep + at, 16)) =
+                        now.x[h][s];
+            }
+        }
+        if (g.sums) {
+            wave_fence();
+#pragma unroll
+            for (int f = 0; f < FI; ++f)
+#pragma unroll
+                for (int k = 0; k < KI; ++k) dw[f][k] = column_product<S, Z>(lx, k * 16, lz, f * 16, lane, dw[f][k]);
+            wave_fence();
+        }
+        now = next;
+    }
+    if (!g.sums) return;
+    // the block's sums, wave after wave
+#pragma unroll
+    for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) db[s][j] += __shfl_xor(db[s][j], d);
+    for (int v = 0; v < W; ++v) {
+        __syncthreads();
+        if (wave != v) continue;
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int k = 0; k < KI; ++k) {
+                f32x4* to = reinterpret_cast<f32x4*>(lds.sums + (f * KI + k) * 256 + lane * 4);
+                *to = v ? *to + dw[f][k] : dw[f][k];
+            }
+        if ((lane & 15) == 0) {
+#pragma unroll
+            for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+                for (int j = 0; j < N; ++j) {
+                    const int f = s * Z::kStep + at + j;
+                    if (f < FI * 16) lds.sums[FI * KI * 256 + f] = db[s][j] + (v ? lds.sums[FI * KI * 256 + f] : 0.0f);
+                }
+        }
+    }
+    __syncthreads();
+    float* out = g.sums + (int64_t)blockIdx.x * ((int64_t)g.f * g.k + g.f);
+    for (int t = threadIdx.x; t < g.f * g.k + g.f; t += kNarrowThreads) {
+        int from = FI * KI * 256 + t - g.f * g.k;
+        if (t < g.f * g.k) {
+            const int f = t / g.k, k = t % g.k;   // of the lane's place: f its l % 16, k its 4 (l / 16) + 0..3
+            from = ((f >> 4) * KI + (k >> 4)) * 256 + (((k & 15) >> 2) * 16 + (f & 15)) * 4 + (k & 3);
+        }
+        out[t] = lds.sums[from];
+    }
+}
+
+// the widths that have kernels, in blocks of 16: f(constants) for the least that hold them
+template <int MOST, typename F>
+bool with_blocks(int64_t a, int64_t b, F&& f)
+{
+    auto second = [&](auto i) {
+        constexpr int A = decltype(i)::value;
+        if constexpr (A * 1 <= MOST) { if (b <= 1) { f(i, std::integral_constant<int, 1>{}); return true; } }
+        if constexpr (A * 2 <= MOST) { if (b <= 2) { f(i, std::integral_constant<int, 2>{}); return true; } }
+        if constexpr (A * 3 <= MOST) { if (b <= 3) { f(i, std::integral_constant<int, 3>{}); return true; } }
+        if constexpr (A * 4 <= MOST) { if (b <= 4) { f(i, std::integral_constant<int, 4>{}); return true; } }
+        if constexpr (A * 8 <= MOST) { if (b <= 8) { f(i, std::integral_constant<int, 8>{}); return true; } }
+        return false;
+    };
+    if (a <= 1) return second(std::integral_constant<int, 1>{});
+    if (a <= 2) return second(std::integral_constant<int, 2>{});
+    if (a <= 3) return second(std::integral_constant<int, 3>{});
+    if (a <= 4) return second(std::integral_constant<int, 4>{});
+    if (a <= 8) return second(std::integral_constant<int, 8>{});
+    return false;
+}
+
+constexpr int kNarrowFwd = 24, kNarrowBwd = 16;   // operands of w, and results of dw, that a wave holds in registers
+
+// whether the backward pass of f x k weights has a kernel
+inline bool narrow_bwd(int64_t f, int64_t k)
+{
+    return with_blocks<kNarrowBwd>(ceil_div(f, 16), ceil_div(k, 16), [](auto, auto) {});
+}
+
+// one type each (layer_narrow_*.hip); false: too wide
+bool launch_narrow_fwd_f32(gs_ctx* ctx, const LayerMm& g);
+bool launch_narrow_fwd_f16(gs_ctx* ctx, const LayerMm& g);
+bool launch_narrow_fwd_bf16(gs_ctx* ctx, const LayerMm& g);
+bool launch_narrow_bwd_f32(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+bool launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+bool launch_narrow_bwd_bf16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+
+template <typename S>
+bool launch_narrow_fwd(gs_ctx* ctx, const LayerMm& g)
+{
+    constexpr int kStep = 64 / sizeof(S);
+    return with_blocks<kNarrowFwd>(ceil_div(g.k, kStep), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
+        const int64_t groups = ceil_div(g.m, 16 * (kNarrowThreads / 64));
+        hipLaunchKernelGGL((k_narrow_fwd<S, decltype(ks)::value, decltype(ni)::value>),
+                           dim3((uint32_t)std::min<int64_t>(groups, 6 * ctx->num_cu)), dim3(kNarrowThreads), 0, ctx->stream, g);
+    });
+}
+
+template <typename S>
+bool launch_narrow_bwd(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks)
+{
+    return with_blocks<kNarrowBwd>(ceil_div(g.f, 16), ceil_div(g.k, 16), [&](auto fi, auto ki) {
+        hipLaunchKernelGGL((k_narrow_bwd<S, decltype(fi)::value, decltype(ki)::value>), dim3((uint32_t)blocks),
+                           dim3(kNarrowThreads), 0, ctx->stream, g);
+    });
+}
+
+}  // namespace gsm

@@ -8,7 +8,7 @@
 //           dg = dout u act'(g), du = dout act(g), then as above
 #include <algorithm>
 
-#include "layer_mm.h"
+#include "layer_narrow.h"
 
 namespace {
 
@@ -78,29 +78,53 @@ __global__ __launch_bounds__(kDzThreads) void k_dz(const DzJob g)
     }
 }
 
-// out[n] = (old out[n]) + sum over `blocks` rows of sums[..][n]: 64 columns a
-// block, four quarters of the rows
+// Sums over `blocks` rows of f k + f values each, plus the old values when
+// accumulate: the first f k of them to dw [f][k], the others to dbias (either
+// null: not wanted).  64 columns a block, four quarters of the rows.
+struct SumJob {
+    const float* sums;
+    void *dw, *dbias;
+    int64_t blocks, f, k, lddw;
+    int32_t dw_type, dbias_type, accumulate;
+};
+
 template <typename S>
-__global__ __launch_bounds__(256) void k_sum_rows(const float* __restrict__ sums, int64_t blocks, int64_t n, void* out,
-                                                  int out_type, int accumulate)
+__global__ __launch_bounds__(256) void k_sum_rows(const SumJob g)
 {
     __shared__ float part[4][64];
     const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int64_t c = (int64_t)blockIdx.x * 64 + x;
+    const int64_t n = g.f * g.k + g.f, c = (int64_t)blockIdx.x * 64 + x;
+    const bool weight = c < g.f * g.k, wanted = c < n && (weight ? g.dw : g.dbias);
     float s = 0.0f;
-    if (c < n)
-        for (int64_t b = q; b < blocks; b += 4) s += sums[b * n + c];
+    if (wanted) {
+#pragma unroll 8
+        for (int64_t b = q; b < g.blocks; b += 4) s += g.sums[b * n + c];
+    }
     part[q][x] = s;
     __syncthreads();
-    if (q || c >= n) return;
+    if (q || !wanted) return;
     s = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
-    if (out_type == GS_F32) {
-        float* o = (float*)out + c;
-        *o = accumulate ? *o + s : s;
+    const int type = weight ? g.dw_type : g.dbias_type;
+    const int64_t at = weight ? c / g.k * g.lddw + c % g.k : c - g.f * g.k;
+    void* out = weight ? g.dw : g.dbias;
+    if (type == GS_F32) {
+        float* o = (float*)out + at;
+        *o = g.accumulate ? *o + s : s;
     } else {
-        S* o = (S*)out + c;
-        *o = gst::narrow<S>(accumulate ? (float)*o + s : s);
+        S* o = (S*)out + at;
+        *o = gst::narrow<S>(g.accumulate ? (float)*o + s : s);
     }
+}
+
+gs_status launch_sum_rows(gs_ctx* ctx, int type, const SumJob& g)
+{
+    GsTimerScope ts(ctx, "layer_sum");
+    gst::with_type(type, [&](auto s) {
+        hipLaunchKernelGGL((k_sum_rows<decltype(s)>), dim3((uint32_t)ceil_div(g.f * g.k + g.f, 64)), dim3(256), 0,
+                           ctx->stream, g);
+    });
+    GS_HIP(ctx, hipGetLastError());
+    return GS_OK;
 }
 
 // What n tiles on each compute unit take for one step of k: once us for
@@ -174,6 +198,26 @@ Operand operand(const void* p, int64_t ld, int64_t rows, int64_t gate = 0)
 
 }  // namespace
 
+static gs_status check_launch(gs_ctx* ctx)
+{
+    GS_HIP(ctx, hipGetLastError());
+    return GS_OK;
+}
+
+static bool launch_narrow(gs_ctx* ctx, int type, const LayerMm& g)
+{
+    GsTimerScope ts(ctx, "layer_narrow");
+    return type == GS_F32 ? launch_narrow_fwd_f32(ctx, g) :
+           type == GS_F16 ? launch_narrow_fwd_f16(ctx, g) : launch_narrow_fwd_bf16(ctx, g);
+}
+
+static bool launch_narrow(gs_ctx* ctx, int type, const NarrowBwd& g, int64_t blocks)
+{
+    GsTimerScope ts(ctx, "layer_narrow");
+    return type == GS_F32 ? launch_narrow_bwd_f32(ctx, g, blocks) :
+           type == GS_F16 ? launch_narrow_bwd_f16(ctx, g, blocks) : launch_narrow_bwd_bf16(ctx, g, blocks);
+}
+
 gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int act,
                             const gs_tensor* residual, const gs_tensor* pre, const gs_tensor* out, bool gated,
                             std::vector<GsAlloc>* tmp)
@@ -192,6 +236,7 @@ gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     g.e.out = out->data, g.e.ldout = out->stride, g.e.out_type = (int8_t)out->type;
     if (g.m == 0 || g.e.n == 0) return GS_OK;
     if (few_rows(g)) return launch_layer_few(ctx, x->type, g);
+    if (!gated && launch_narrow(ctx, x->type, g)) return check_launch(ctx);
     const int64_t ws = plan(ctx, x->type == GS_F32, &g);
     if (ws && !(g.ws = (float*)gs_malloc(ctx, 4 * ws, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
     return launch_mm(ctx, x->type, g);
@@ -203,6 +248,25 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
 {
     const int type = x->type;
     const int64_t size = type == GS_F32 ? 4 : 2, m = x->rows, k = x->cols, n = w->rows;
+    if (!gated && m > 0 && n > 0 && k > 0 && narrow_bwd(n, k)) {
+        const bool sums = dw || dbias;
+        const int rows = (type == GS_F32 ? 16 : 32) * (kNarrowThreads / 64);
+        NarrowBwd z{};
+        z.x = x->data, z.ldx = x->stride;
+        z.w = w->data, z.ldw = w->stride;
+        if (pre) z.pre = pre->data, z.ldpre = pre->stride;
+        z.dout = dout->data, z.lddout = dout->stride, z.dout_type = dout->type;
+        if (dx) z.dx = dx->data, z.lddx = dx->stride;
+        z.m = m, z.f = (int32_t)n, z.k = (int32_t)k, z.act = act;
+        const int64_t blocks = std::min<int64_t>(ceil_div(m, rows), 2 * ctx->num_cu);
+        if (!sums && !dx) return GS_OK;
+        if (sums && !(z.sums = (float*)gs_malloc(ctx, 4 * blocks * (n * k + n), GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+        launch_narrow(ctx, type, z, blocks);
+        gs_status st = check_launch(ctx);
+        if (st != GS_OK || !sums) return st;
+        return launch_sum_rows(ctx, type, SumJob{z.sums, dw ? dw->data : nullptr, dbias ? dbias->data : nullptr, blocks, n, k,
+                                                 dw ? dw->stride : 0, dw ? dw->type : 0, dbias ? dbias->type : 0, accumulate});
+    }
     // dz, the layer's dout itself where nothing changes it
     const bool own = m * n > 0 && (gated || act != GS_ACT_NONE || dout->type != type) && (dx || dw);
     DzJob z{};
@@ -266,16 +330,10 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         gst::with_type(type, go);
         GS_HIP(ctx, hipGetLastError());
     }
-    if (dbias && n > 0) {
-        GsTimerScope ts(ctx, "layer_dz");
-        gst::with_type(type, [&](auto s) {
-            hipLaunchKernelGGL((k_sum_rows<decltype(s)>), dim3((uint32_t)ceil_div(n, 64)), dim3(256), 0, ctx->stream,
-                               z.sums, row_blocks, n, dbias->data, dbias->type, accumulate);
-        });
-        GS_HIP(ctx, hipGetLastError());
-    }
     gs_status st = GS_OK;
-    if (gw.m > 0) st = launch_mm(ctx, type, gw);
+    if (dbias && n > 0)
+        st = launch_sum_rows(ctx, type, SumJob{z.sums, nullptr, dbias->data, row_blocks, n, 0, 0, 0, dbias->type, accumulate});
+    if (st == GS_OK && gw.m > 0) st = launch_mm(ctx, type, gw);
     if (st == GS_OK && gx.m > 0) st = launch_mm(ctx, type, gx);
     return st;
 }
