@@ -62,8 +62,13 @@ constexpr int kNarrowThreads = 256;
 template <typename S, int KS, int NI>
 __global__ __launch_bounds__(kNarrowThreads) void k_narrow_fwd(const LayerMm g)
 {
-    constexpr int N = 16 / sizeof(S), kStep = 4 * N;
+    constexpr int N = 16 / sizeof(S), kStep = 4 * N, kCols = NI * 16, kRow = kCols + 4;
+    // A 16-bit result of four columns is 8 bytes: those go through LDS, so that
+    // neighbouring lanes write neighbouring columns (64 -> 64 bf16, 1M rows: 123 -> 65 us).
+    constexpr bool kTurn = sizeof(S) == 2;
+    __shared__ __align__(16) float lds[kTurn ? kNarrowThreads / 64 : 1][kTurn ? 16 * kRow : 4];
     const int lane = threadIdx.x & 63, k0 = (lane >> 4) * N;
+    float* const mine = lds[kTurn ? threadIdx.x >> 6 : 0];
     gst::Pack<S, N> b[NI][KS];
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
@@ -82,14 +87,24 @@ __global__ __launch_bounds__(kNarrowThreads) void k_narrow_fwd(const LayerMm g)
     if (at < groups) load(at, a);
     for (; at < groups; at += stride) {
         if (at + stride < groups) load(at + stride, next);
-        const int64_t m = at * 16 + (lane & 15);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
             f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int s = 0; s < KS; ++s) acc = mfma16(b[i][s], a[s], acc);
-            const int64_t n = i * 16 + (lane >> 4) * 4;
-            if (m < g.m && n < g.e.n) epilogue<S>(g.e, m, n, acc);
+            const int row = lane & 15, c = i * 16 + (lane >> 4) * 4;
+            if constexpr (kTurn) *reinterpret_cast<f32x4*>(mine + row * kRow + c) = acc;
+            else if (at * 16 + row < g.m && c < g.e.n) epilogue<S>(g.e, at * 16 + row, c, acc);
+        }
+        if constexpr (kTurn) {
+            wave_fence();
+#pragma unroll
+            for (int t = 0; t < NI; ++t) {
+                const int q = t * 64 + lane, row = q / (kCols / 4), c = q % (kCols / 4) * 4;
+                if (at * 16 + row < g.m && c < g.e.n)
+                    epilogue<S>(g.e, at * 16 + row, c, *reinterpret_cast<const f32x4*>(mine + row * kRow + c));
+            }
+            wave_fence();
         }
 #pragma unroll
         for (int s = 0; s < KS; ++s) a[s] = next[s];
@@ -180,10 +195,14 @@ __device__ __forceinline__ f32x4 column_product(const S* x, int cx, const S* z, 
 }
 
 template <typename S, int FI, int KI>
-__global__ __launch_bounds__(kNarrowThreads) void k_narrow_bwd(const NarrowBwd g)
+__global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBwd g)
 {
     typedef NarrowSize<S, FI, KI> Z;
     constexpr int W = kNarrowThreads / 64, N = Z::N;
+    // The next rows are on their way while these are worked on, where registers
+    // for both leave two waves a SIMD (1M x 32 -> 64 f32: 167 us, 182 without;
+    // 64 -> 64 f32: 425, 270 without; the 16-bit types lose at every width).
+    constexpr bool PRE = sizeof(S) == 4 && FI * KI <= 9;
     __shared__ __align__(16) union {
         S rows[W][Z::kRows * (Z::ldz + Z::ldx)];
         float sums[FI * KI * 256 + FI * 16];
@@ -218,9 +237,13 @@ __global__ __launch_bounds__(kNarrowThreads) void k_narrow_bwd(const NarrowBwd g
     const int64_t stride = (int64_t)gridDim.x * W * Z::kRows;
     int64_t row0 = ((int64_t)blockIdx.x * W + wave) * Z::kRows;
     NarrowRows<S, FI, KI> now, next;
-    if (row0 < g.m) now.load(g, row0, lane);
+    if (PRE && row0 < g.m) now.load(g, row0, lane);
     for (; row0 < g.m; row0 += stride) {
-        if (row0 + stride < g.m) next.load(g, row0 + stride, lane);
+        if constexpr (PRE) {
+            if (row0 + stride < g.m) next.load(g, row0 + stride, lane);
+        } else {
+            now.load(g, row0, lane);
+        }
 #pragma unroll
         for (int h = 0; h < Z::kRows / 16; ++h) {
             gst::Pack<S, N> dz[Z::FS];
@@ -264,7 +287,7 @@ __global__ __launch_bounds__(kNarrowThreads) void k_narrow_bwd(const NarrowBwd g
                 for (int k = 0; k < KI; ++k) dw[f][k] = column_product<S, Z>(lx, k * 16, lz, f * 16, lane, dw[f][k]);
             wave_fence();
         }
-        now = next;
+        if constexpr (PRE) now = next;
     }
     if (!g.sums) return;
     // the block's sums, wave after wave
@@ -329,6 +352,14 @@ bool with_blocks(int64_t a, int64_t b, F&& f)
 
 constexpr int kNarrowFwd = 24, kNarrowBwd = 16;   // operands of w, and results of dw, that a wave holds in registers
 
+// Blocks of the backward pass: two a compute unit, four for the least widths
+// (1M rows of 32 -> 3 f32: 73 us, 95 with two; of 64 -> 64: 270 with two, 292).
+inline int64_t narrow_blocks(const gs_ctx* ctx, int type, int64_t m, int64_t f, int64_t k)
+{
+    const int64_t rows = (type == GS_F32 ? 16 : 32) * (kNarrowThreads / 64);
+    return std::min(ceil_div(m, rows), (ceil_div(f, 16) * ceil_div(k, 16) <= 2 ? 4 : 2) * (int64_t)ctx->num_cu);
+}
+
 // whether the backward pass of f x k weights has a kernel
 inline bool narrow_bwd(int64_t f, int64_t k)
 {
@@ -348,9 +379,13 @@ bool launch_narrow_fwd(gs_ctx* ctx, const LayerMm& g)
 {
     constexpr int kStep = 64 / sizeof(S);
     return with_blocks<kNarrowFwd>(ceil_div(g.k, kStep), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
-        const int64_t groups = ceil_div(g.m, 16 * (kNarrowThreads / 64));
+        // waves that come back for more rows: 6 blocks a compute unit, and where
+        // w takes few registers 24 (32 -> 48 f32: 86 us, 106 with 6; 64 -> 64: 184, 170)
+        constexpr int kOps = decltype(ks)::value * decltype(ni)::value;
+        const int64_t groups = ceil_div(g.m, 16 * (kNarrowThreads / 64)),
+                      most = (sizeof(S) == 2 || kOps > 8 ? 6 : 24) * ctx->num_cu;
         hipLaunchKernelGGL((k_narrow_fwd<S, decltype(ks)::value, decltype(ni)::value>),
-                           dim3((uint32_t)std::min<int64_t>(groups, 6 * ctx->num_cu)), dim3(kNarrowThreads), 0, ctx->stream, g);
+                           dim3((uint32_t)std::min(groups, most)), dim3(kNarrowThreads), 0, ctx->stream, g);
     });
 }
 

@@ -21,9 +21,13 @@ constexpr float kGelu1 = 1.5957691216057308f, kGelu3 = 0.044715f;
 struct Sigma {
     float p, t;   // sigma(v), sigma(v) sigma(-v)
 };
+// The hardware's exponential and reciprocal are within an ulp or so; rounding
+// the exponent's argument costs |v| 2^-24 of q, where q itself is exp(-|v|).
+// (With expf and a division an activation costs 40 operations, not 10: 1M rows
+// of 64 silu values 52 us.)
 __device__ __forceinline__ Sigma sigma(float v)
 {
-    const float q = expf(-fabsf(v)), r = 1.0f / (1.0f + q);
+    const float q = __builtin_amdgcn_exp2f(-fabsf(v) * 1.44269504f), r = __builtin_amdgcn_rcpf(1.0f + q);
     return Sigma{v >= 0.0f ? r : q * r, q * r * r};
 }
 __device__ __forceinline__ float gelu_arg(float z) { return kGelu1 * (z + kGelu3 * z * z * z); }

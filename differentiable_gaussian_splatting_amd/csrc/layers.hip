@@ -250,7 +250,6 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     const int64_t size = type == GS_F32 ? 4 : 2, m = x->rows, k = x->cols, n = w->rows;
     if (!gated && m > 0 && n > 0 && k > 0 && narrow_bwd(n, k)) {
         const bool sums = dw || dbias;
-        const int rows = (type == GS_F32 ? 16 : 32) * (kNarrowThreads / 64);
         NarrowBwd z{};
         z.x = x->data, z.ldx = x->stride;
         z.w = w->data, z.ldw = w->stride;
@@ -258,7 +257,7 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         z.dout = dout->data, z.lddout = dout->stride, z.dout_type = dout->type;
         if (dx) z.dx = dx->data, z.lddx = dx->stride;
         z.m = m, z.f = (int32_t)n, z.k = (int32_t)k, z.act = act;
-        const int64_t blocks = std::min<int64_t>(ceil_div(m, rows), 2 * ctx->num_cu);
+        const int64_t blocks = narrow_blocks(ctx, type, m, n, k);
         if (!sums && !dx) return GS_OK;
         if (sums && !(z.sums = (float*)gs_malloc(ctx, 4 * blocks * (n * k + n), GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
         launch_narrow(ctx, type, z, blocks);
