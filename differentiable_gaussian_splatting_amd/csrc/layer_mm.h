@@ -110,9 +110,9 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
-// Tiles of the product, each over one of `splits` ranges of k; with more than
-// one, the sums go to ws [split][m][wn] and k_join adds them up.
-template <typename S, int P, bool ACOL, bool BCOL, bool GATED, typename T>
+// Tiles of the product (DIRECT: see mm_tile); those from `full` on in `splits` ranges of k, whose sums
+// k_join adds up.
+template <typename S, int P, bool ACOL, bool BCOL, bool GATED, typename T, bool DIRECT>
 __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
 {
     constexpr int kCols = T::NI * (GATED ? 8 : 16), kRow = T::NI * 16 + 4;   // of a wave's results; padded row in LDS
@@ -120,20 +120,29 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
         Lds<S, P, T> tile;
         float out[T::NT / 64 * 32 * kRow];
     } lds;
-    const int64_t tiles = g.tm * g.tn, total = tiles * g.splits;
+    const int64_t rest = g.tm * g.tn - g.full, total = g.full + rest * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
-        const int64_t at = xcd_order(b, total), s = at / tiles;
-        int64_t i, j;
-        tile_at(at % tiles, g.tm, g.tn, i, j);
-        const int64_t m0 = i * T::BM, n0 = j * T::BN, k0 = s * g.kper;
+        int64_t tile = b, k0 = 0, k1 = g.k, i, j;
+        float* ws = nullptr;
+        if (b < g.full) {
+            tile = xcd_order(b, g.full);
+        } else {
+            const int64_t at = xcd_order(b - g.full, rest * g.splits), s = at / rest;
+            tile = g.full + at % rest;
+            k0 = s * g.kper;
+            k1 = min(g.k, k0 + g.kper);
+            ws = g.ws + at * (T::BM * T::BN);
+        }
+        tile_at(tile, g.tm, g.tn, i, j);
+        const int64_t m0 = i * T::BM, n0 = j * T::BN;
         f32x4 acc[T::NI][T::MI];
 #pragma unroll
         for (int q = 0; q < T::NI; ++q)
 #pragma unroll
             for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (b != (int64_t)blockIdx.x) __syncthreads();   // the previous tile's reads of lds
-        mm_tile<S, P, ACOL, BCOL, T>(g.a, g.b, m0, n0, k0, min(g.k, k0 + g.kper), lds.tile, acc);
+        mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(g.a, g.b, m0, n0, k0, k1, lds.tile, acc);
         // The results go through LDS, 32 rows of each wave at a time, so that a
         // lane takes four columns next to its neighbours' (whole lines are
         // read and written) and the epilogue's code is a loop.
@@ -156,10 +165,10 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
                 if (m >= g.m || n >= g.e.n) continue;
                 const float* v = mine + row * kRow + (GATED ? (c >> 4) * 32 + (c & 15) : c);
                 const f32x4 x = *reinterpret_cast<const f32x4*>(v);
-                if (g.splits > 1) {
-                    float* w = g.ws + (s * g.m + m) * g.wn + n;
-                    gst::store<float, 4>(w, __builtin_bit_cast(Four, x));
-                    if constexpr (GATED) gst::store<float, 4>(w + g.wn / 2, *reinterpret_cast<const Four*>(v + 16));
+                if (ws) {
+                    float* w = ws + (m - m0) * T::BN + (wave / T::WM) * T::NI * 16 + (v - mine - row * kRow);
+                    *reinterpret_cast<f32x4*>(w) = x;
+                    if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = *reinterpret_cast<const f32x4*>(v + 16);
                 } else if constexpr (GATED) {
                     epilogue_gated<S>(g.e, m, n, x, *reinterpret_cast<const f32x4*>(v + 16));
                 } else {
@@ -172,17 +181,24 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
 }
 
 // Sums of the splits in their order, then the epilogue; four columns a thread.
-template <typename S, bool GATED>
+template <typename S, bool GATED, typename T>
 __global__ __launch_bounds__(256) void k_join(const LayerMm g)
 {
-    const int64_t n4 = (g.e.n + 3) / 4, total = g.m * n4;
+    constexpr int kCols = T::BN / (GATED ? 2 : 1), kQuads = T::BM * kCols / 4;
+    const int64_t rest = g.tm * g.tn - g.full, total = rest * kQuads;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
-        const int64_t m = t / n4, n = t % n4 * 4;
-        const float* w = g.ws + m * g.wn + n;
+        const int64_t tile = t / kQuads;
+        const int row = t % kQuads / (kCols / 4), c = t % (kCols / 4) * 4;
+        int64_t i, j;
+        tile_at(g.full + tile, g.tm, g.tn, i, j);
+        const int64_t m = i * T::BM + row, n = j * kCols + c;
+        if (m >= g.m || n >= g.e.n) continue;
+        const float* w = g.ws + tile * (T::BM * T::BN) + row * T::BN + (GATED ? (c >> 4) * 32 + (c & 15) : c);
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
+#pragma unroll 4
         for (int s = 0; s < g.splits; ++s) {
-            x += __builtin_bit_cast(f32x4, gst::load<float, 4>(w + s * g.m * g.wn));
-            if constexpr (GATED) y += __builtin_bit_cast(f32x4, gst::load<float, 4>(w + s * g.m * g.wn + g.wn / 2));
+            x += *reinterpret_cast<const f32x4*>(w + s * rest * (T::BM * T::BN));
+            if constexpr (GATED) y += *reinterpret_cast<const f32x4*>(w + s * rest * (T::BM * T::BN) + 16);
         }
         if constexpr (GATED) epilogue_gated<S>(g.e, m, n, x, y);
         else epilogue<S>(g.e, m, n, x);
@@ -191,29 +207,34 @@ __global__ __launch_bounds__(256) void k_join(const LayerMm g)
 
 constexpr int64_t kMaxGrid = 1 << 22;   // blocks of a launch; larger products loop
 
-template <typename S, int P, typename T>
+template <typename S, int P, typename T, bool DIRECT>
 void launch_mode(gs_ctx* ctx, const LayerMm& g)
 {
-    const dim3 grid((uint32_t)std::min(g.tm * g.tn * g.splits, kMaxGrid)), block(T::NT);
-    if (g.a_col) hipLaunchKernelGGL((k_layer_mm<S, P, true, true, false, T>), grid, block, 0, ctx->stream, g);
-    else if (g.b_col) hipLaunchKernelGGL((k_layer_mm<S, P, false, true, false, T>), grid, block, 0, ctx->stream, g);
-    else if (g.gated) hipLaunchKernelGGL((k_layer_mm<S, P, false, false, true, T>), grid, block, 0, ctx->stream, g);
-    else hipLaunchKernelGGL((k_layer_mm<S, P, false, false, false, T>), grid, block, 0, ctx->stream, g);
+    const int64_t rest = g.tm * g.tn - g.full;
+    const dim3 grid((uint32_t)std::min(g.full + rest * g.splits, kMaxGrid)), block(T::NT);
+    if (g.a_col) hipLaunchKernelGGL((k_layer_mm<S, P, true, true, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
+    else if (g.b_col) hipLaunchKernelGGL((k_layer_mm<S, P, false, true, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
+    else if (g.gated) hipLaunchKernelGGL((k_layer_mm<S, P, false, false, true, T, DIRECT>), grid, block, 0, ctx->stream, g);
+    else hipLaunchKernelGGL((k_layer_mm<S, P, false, false, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
+    if (g.splits == 1) return;
+    const int64_t quads = rest * T::BM * T::BN / (g.gated ? 8 : 4);
+    const dim3 join((uint32_t)std::min(ceil_div(quads, 256), kMaxGrid));
+    if (g.gated) hipLaunchKernelGGL((k_join<S, true, T>), join, dim3(256), 0, ctx->stream, g);
+    else hipLaunchKernelGGL((k_join<S, false, T>), join, dim3(256), 0, ctx->stream, g);
 }
 
 template <typename S, int P, typename Large, typename Medium, typename Small, typename Tiny>
 gs_status launch_layer_mm(gs_ctx* ctx, const LayerMm& g)
 {
     GsTimerScope ts(ctx, "layer_mm");
-    if (g.tile == kLarge) launch_mode<S, P, Large>(ctx, g);
-    else if (g.tile == kMedium) launch_mode<S, P, Medium>(ctx, g);
-    else if (g.tile == kSmall) launch_mode<S, P, Small>(ctx, g);
-    else launch_mode<S, P, Tiny>(ctx, g);
-    if (g.splits > 1) {
-        const dim3 grid((uint32_t)std::min(ceil_div(g.m * ((g.e.n + 3) / 4), 256), kMaxGrid)), block(256);
-        if (g.gated) hipLaunchKernelGGL((k_join<S, true>), grid, block, 0, ctx->stream, g);
-        else hipLaunchKernelGGL((k_join<S, false>), grid, block, 0, ctx->stream, g);
-    }
+    const auto aligned = [](const Operand& o) { return (uintptr_t)o.p % 16 == 0 && o.ld * (int64_t)sizeof(S) % 16 == 0; };
+    const bool direct = P == 1 && aligned(g.a) && aligned(g.b);
+    if (g.tile == kLarge && direct) launch_mode<S, P, Large, P == 1>(ctx, g);
+    else if (g.tile == kLarge) launch_mode<S, P, Large, false>(ctx, g);
+    else if (g.tile == kMedium && direct) launch_mode<S, P, Medium, P == 1>(ctx, g);
+    else if (g.tile == kMedium) launch_mode<S, P, Medium, false>(ctx, g);
+    else if (g.tile == kSmall) launch_mode<S, P, Small, false>(ctx, g);
+    else launch_mode<S, P, Tiny, false>(ctx, g);
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;
 }

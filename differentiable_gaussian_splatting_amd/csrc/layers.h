@@ -74,10 +74,10 @@ struct LayerMm {
     int64_t m, k;
     Epilogue e;
     int64_t tm, tn;              // tiles
-    int64_t kper;                // values of k of a split, a multiple of the tile's step
-    float* ws;                   // sums of the splits (splits > 1), wn floats per row
-    int64_t wn;
-    int32_t splits, tile;
+    int64_t full;                // the first `full` tiles are formed whole, each by one block;
+    int32_t splits, tile;        // the others in `splits` ranges of kper values of k,
+    int64_t kper;                // a multiple of the tile's step,
+    float* ws;                   // whose sums are kept here: [splits][tiles - full][rows][columns of a tile]
     bool a_col, b_col, gated;    // a_col only with b_col
 };
 
@@ -90,7 +90,7 @@ bool few_rows(const LayerMm& g);
 gs_status launch_layer_few(gs_ctx* ctx, int type, const LayerMm& g);
 
 typedef Tile<256, 256, 64, 2, 4, 2> Large16;
-typedef Tile<128, 128, 64, 2, 2, 1> Medium16;
+typedef Tile<128, 128, 64, 2, 2, 2> Medium16;
 typedef Tile<64, 64, 64, 2, 2, 2> Small16;
 typedef Tile<64, 64, 64, 2, 2, 2, true> Tiny16;
 typedef Tile<256, 128, 32, 4, 2, 2> Large32;

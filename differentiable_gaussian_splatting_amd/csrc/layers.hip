@@ -26,7 +26,7 @@ struct DzJob {
     void* dz;            // null: the sums alone
     float* sums;         // [row blocks][n], null: none
     int64_t m, n;        // n: columns of dout
-    int64_t ldpre, lddout, rows;
+    int64_t ldpre, lddout, lddz, rows;
     int32_t act, dout_type, tx, col_blocks;
 };
 
@@ -53,15 +53,15 @@ __global__ __launch_bounds__(kDzThreads) void k_dz(const DzJob g)
                     dz[j] = d[j] * u[j] * v.y;
                     du[j] = d[j] * v.x;
                 }
-                store4<S>(g.dz, m * 2 * g.n + g.n + n, type, valid, du);
-                store4<S>(g.dz, m * 2 * g.n + n, type, valid, dz);
+                store4<S>(g.dz, m * g.lddz + g.n + n, type, valid, du);
+                store4<S>(g.dz, m * g.lddz + n, type, valid, dz);
             } else {
                 if (g.act != GS_ACT_NONE) {
                     const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) dz[j] = d[j] * act_both(z[j], g.act).y;
                 }
-                if (g.dz) store4<S>(g.dz, m * g.n + n, type, valid, dz);
+                if (g.dz) store4<S>(g.dz, m * g.lddz + n, type, valid, dz);
                 sum += dz;
             }
         }
@@ -141,47 +141,62 @@ constexpr TileCost cost(int resident, double once, double each)
 {
     return TileCost{T::BM, T::BN, T::BK, resident, once, each};
 }
-constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.3), cost<Medium16>(2, 0.5, 0.48), cost<Small16>(5, 0.2, 0.25),
+constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.1), cost<Medium16>(2, 0.3, 0.46), cost<Small16>(5, 0.2, 0.25),
                                 cost<Tiny16>(3, 0.3, 0.3)};
 constexpr TileCost kCost32[] = {cost<Large32>(1, 0.1, 2.5), cost<Medium32>(2, 0.5, 1.35), cost<Small32>(3, 0.3, 0.48),
                                 cost<Tiny32>(3, 0.4, 0.5)};
 constexpr double kJoinUs = 4.0;          // a further launch
 constexpr double kJoinRate = 4e6;        // bytes per us of sums written and read
 
-// Tiles and splits of a product of m x n (n of the tiles: both halves of a
-// gated layer) over k, those that the costs above make fastest, and the floats
-// of its workspace.
+// What the tiles from `full` on cost: `tiles` of them, in s ranges of k.
+double cost_us(const gs_ctx* ctx, const TileCost& c, int64_t tiles, int64_t steps, int64_t s)
+{
+    const int64_t blocks = tiles * s;
+    const double step = ceil_div(blocks, (int64_t)c.resident * ctx->num_cu) * c.once + ceil_div(blocks, ctx->num_cu) * c.each;
+    return (double)(ceil_div(steps, s) + 1) * step + (s > 1 ? kJoinUs + 8.0 * blocks * c.m * c.n / kJoinRate : 0.0);
+}
+
+// The tile of a product of m x n (n of the tiles: both halves of a gated layer)
+// over k, and the tiles that are split, as the costs above make fastest.  Whole
+// rounds of the card are formed whole; a last round that would leave most of
+// it idle, or the only one, is split over k (8191 x 4097 over 2049 f16: 544
+// tiles of 256 x 256 on 256 units).  Returns the floats of its workspace.
 int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
 {
-    const int64_t n = g->e.n * (g->gated ? 2 : 1), wn = (g->e.n + 3) / 4 * 4 * (g->gated ? 2 : 1);
+    const int64_t n = g->e.n * (g->gated ? 2 : 1);
     const bool tiny = (!g->a_col && g->k < 8) || (g->a_col && g->m < 8) || (!g->b_col && g->k < 8) ||
                       (g->b_col && g->e.n < 8);
     double best = 0.0;
-    int64_t best_each = 1;
+    int64_t best_s = 1;
     for (int t = tiny ? kTiny : kLarge; t <= (tiny ? kTiny : kSmall); ++t) {
         const TileCost& c = f32 ? kCost32[t] : kCost16[t];
         const int64_t tiles = ceil_div(g->m, c.m) * ceil_div(n, c.n), steps = std::max<int64_t>(1, ceil_div(g->k, c.k));
         const int64_t slots = (int64_t)c.resident * ctx->num_cu;
-        for (int64_t s = 1; s <= steps; s += std::max<int64_t>(1, s / 4)) {
-            if (s > 1 && (tiles * s > 2 * slots || s * g->m * wn > (1ll << 28))) break;
-            const int64_t each = ceil_div(steps, s);
-            const double us = (double)(each + 1) * (ceil_div(tiles * s, slots) * c.once +
-                                                    ceil_div(tiles * s, ctx->num_cu) * c.each) +
-                              (s > 1 ? kJoinUs + 8.0 * s * g->m * wn / kJoinRate : 0.0);
-            if (best > 0.0 && us >= best) continue;
-            best = us;
-            best_each = each;
+        const double whole = cost_us(ctx, c, tiles, steps, 1);
+        if (best == 0.0 || whole < best) {
+            best = whole;
+            best_s = 1;
             g->tile = t;
+            g->full = tiles;
+        }
+        const int64_t rest = tiles % slots, full = tiles - rest;
+        for (int64_t s = 2; rest > 0 && s <= steps && rest * s <= 2 * slots; s += std::max<int64_t>(1, s / 4)) {
+            const double us = (full ? cost_us(ctx, c, full, steps, 1) : 0.0) + cost_us(ctx, c, rest, steps, s);
+            if (us >= best) continue;
+            best = us;
+            best_s = s;
+            g->tile = t;
+            g->full = full;
         }
     }
     const TileCost& c = f32 ? kCost32[g->tile] : kCost16[g->tile];
     g->tm = ceil_div(g->m, c.m);
     g->tn = ceil_div(n, c.n);
-    g->kper = best_each * c.k;
+    g->kper = ceil_div(std::max<int64_t>(1, ceil_div(g->k, c.k)), best_s) * c.k;
     g->splits = (int32_t)std::max<int64_t>(1, ceil_div(g->k, g->kper));
+    if (g->splits == 1) g->full = g->tm * g->tn;
     g->ws = nullptr;
-    g->wn = wn;
-    return g->splits > 1 ? g->splits * g->m * wn : 0;
+    return g->splits > 1 ? g->splits * (g->tm * g->tn - g->full) * c.m * c.n : 0;
 }
 
 gs_status launch_mm(gs_ctx* ctx, int type, const LayerMm& g)
@@ -286,11 +301,12 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         const int ny = kDzThreads / z.tx;
         z.rows = ceil_div(std::max<int64_t>(ceil_div(m * z.col_blocks, 2048), 4 * ny), ny) * ny;
         row_blocks = ceil_div(m, z.rows);
-        if (own && !(z.dz = gs_malloc(ctx, m * n * size, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+        z.lddz = (n + 7) / 8 * 8;   // rows that start on 16 bytes
+        if (own && !(z.dz = gs_malloc(ctx, m * z.lddz * size, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
         if (dbias && !(z.sums = (float*)gs_malloc(ctx, 4 * row_blocks * n, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
     }
     const void* dz = own ? z.dz : dout->data;
-    const int64_t lddz = own ? n : dout->stride;
+    const int64_t lddz = own ? z.lddz : dout->stride;
     LayerMm gx{}, gw{};
     int64_t ws = 0;
     if (dx && m * k > 0) {

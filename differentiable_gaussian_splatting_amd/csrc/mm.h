@@ -28,8 +28,10 @@
 // 16 rows meet different banks.  It holds a col tile as BK rows of R values,
 // with 16-value unit q of row k at place q ^ h(k), so that the 16 rows of k
 // that a transposing read touches spread over the banks.  A tile's successor
-// is loaded into registers while the matrix instructions run and is written to
-// the other LDS buffer afterwards (one barrier per BK).
+// is on its way while the matrix instructions run, to the other LDS buffer (one
+// barrier per BK): 16-bit operands whose rows start on 16 bytes are loaded into
+// LDS directly (Direct), others through registers (Stage), which also move
+// values at the operands' edges and split f32 ones.
 #pragma once
 
 #include <type_traits>
@@ -108,7 +110,7 @@ __device__ __forceinline__ void split(const S (&v)[8], float scale, gst::Pack<ty
 template <int BK>
 __device__ __forceinline__ int place(int r, int c)
 {
-    if constexpr (BK == 64) return c ^ ((r & 7) ^ ((r >> 3) & 1));
+    if constexpr (BK >= 64) return c ^ ((r & 7) ^ ((r >> 3) & 1));
     else return c ^ (((r >> 1) & 3) ^ ((r >> 3) & 1));
 }
 // what is xored into the 16-value unit of row k of a col tile of R values
@@ -271,6 +273,49 @@ struct Stage {
     }
 };
 
+// The same way without registers, for whole tiles of a 16-bit operand whose rows
+// start on 16 bytes: each lane's 16 bytes go straight to LDS, the wave's 64
+// chunks to 1 KB in lane order, so the lane fetches the chunk that belongs to
+// its place.  The compiler does not see these loads: done() waits for all of
+// them.  (With the builtin for this load it waits for them before the next LDS
+// read, whose buffer is another one, and the loads hide behind nothing: 256 x 256
+// tiles 900 TFLOP/s, 990 this way; 128 x 128 790 and 890; through registers 915
+// and 740.)
+template <typename S, int R, int BK, int NT, bool COL>
+struct Direct {
+    static constexpr int kSide = (COL ? R : BK) / 8, kStep = NT / kSide, kPer = R * BK / 8 / NT;
+    static_assert(NT % kSide == 0 && R * BK / 8 % NT == 0 && kStep % 16 == 0, "places repeat every 16 rows");
+    const S* at;
+    int64_t step;   // from a thread's chunk to its next
+
+    __device__ __forceinline__ void init(const Operand& o, int64_t r0)
+    {
+        const int row = threadIdx.x / kSide, c = threadIdx.x % kSide;
+        if constexpr (COL) {
+            at = (const S*)o.p + (int64_t)row * o.ld + r0 + ((c >> 1) ^ unit_swap<R>(row)) * 16 + (c & 1) * 8;
+            step = kStep * o.ld;
+        } else {
+            static_assert(kStep % 32 == 0, "gate and up rows alternate by 16");
+            at = (const S*)o.p + row_of_tile(o, r0, row) * o.ld + place<BK>(row, c) * 8;
+            step = (o.gate ? kStep / 2 : kStep) * o.ld;
+        }
+    }
+    __device__ __forceinline__ void load(int64_t k, int64_t ld, S* lds) const
+    {
+        const S* p = at + (COL ? k * ld : k);
+        S* const to = lds + (threadIdx.x >> 6) * 512;
+#pragma unroll
+        for (int u = 0; u < kPer; ++u) {
+            const uint32_t m0 = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) void*)(to + u * NT * 8);
+            asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+                         :
+                         : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(p + u * step)
+                         : "memory", "m0");
+        }
+    }
+};
+__device__ __forceinline__ void done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
 // A wave's N blocks of 16 rows (columns) of a tile, as matrix operands.
 template <typename E, int P, int R, int BK, int N, bool COL>
 struct Fragments {
@@ -319,7 +364,9 @@ struct alignas(16) Lds {
 
 // acc[i][j] += the 16 x 16 results of the calling wave: row j's m is its
 // lane's (lane & 15), column i's n its lane's 4 (lane >> 4) + 0..3.
-template <typename S, int P, bool ACOL, bool BCOL, typename T>
+// WHOLE: the caller's tiles and k end with whole tiles and steps.  DIRECT: the
+// rows of both operands start on 16 bytes.
+template <typename S, int P, bool ACOL, bool BCOL, typename T, bool WHOLE = false, bool DIRECT = false>
 __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int64_t m0, int64_t n0, int64_t k0,
                                         int64_t k1, Lds<S, P, T>& lds, f32x4 (&acc)[T::NI][T::MI])
 {
@@ -338,6 +385,35 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
     const int64_t bn = B.gate ? T::BN / 2 : T::BN, n1 = B.gate ? n0 / 2 : n0;
     const bool edge = m0 + T::BM > A.rows || n1 + bn > (B.gate ? B.gate : B.rows);
     int buf = 0;
+    auto compute = [&]() {
+        const E *la = lds.a[buf], *lb = lds.b[buf];
+#pragma unroll
+        for (int kk = 0; kk < BK / 32; ++kk) {
+            gst::Pack<E, 8> a[P][T::MI], b[P][T::NI];
+#pragma unroll
+            for (int p = 0; p < P; ++p) {
+#pragma unroll
+                for (int i = 0; i < T::NI; ++i) b[p][i] = fb.get(lb, p, i, kk);
+#pragma unroll
+                for (int j = 0; j < T::MI; ++j) a[p][j] = fa.get(la, p, j, kk);
+            }
+#pragma unroll
+            for (int i = 0; i < T::NI; ++i)
+#pragma unroll
+                for (int j = 0; j < T::MI; ++j) {
+                    if constexpr (P == 3) {
+                        acc[i][j] = mfma(b[2][i], a[0][j], acc[i][j]);
+                        acc[i][j] = mfma(b[0][i], a[2][j], acc[i][j]);
+                        acc[i][j] = mfma(b[1][i], a[1][j], acc[i][j]);
+                    }
+                    if constexpr (P >= 2) {
+                        acc[i][j] = mfma(b[1][i], a[0][j], acc[i][j]);
+                        acc[i][j] = mfma(b[0][i], a[1][j], acc[i][j]);
+                    }
+                    acc[i][j] = mfma(b[0][i], a[0][j], acc[i][j]);
+                }
+        }
+    };
     // steps from `from` up to `to`, both loops' code apart: what the edges need
     // would cost the whole tiles' loop its registers
     auto steps = [&](auto is_edge, int64_t from, int64_t to) {
@@ -353,33 +429,7 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
                 sb.template load<EDGE>(k + BK, to);
                 sa.template load<EDGE>(k + BK, to);
             }
-            const E *la = lds.a[buf], *lb = lds.b[buf];
-#pragma unroll
-            for (int kk = 0; kk < BK / 32; ++kk) {
-                gst::Pack<E, 8> a[P][T::MI], b[P][T::NI];
-#pragma unroll
-                for (int p = 0; p < P; ++p) {
-#pragma unroll
-                    for (int i = 0; i < T::NI; ++i) b[p][i] = fb.get(lb, p, i, kk);
-#pragma unroll
-                    for (int j = 0; j < T::MI; ++j) a[p][j] = fa.get(la, p, j, kk);
-                }
-#pragma unroll
-                for (int i = 0; i < T::NI; ++i)
-#pragma unroll
-                    for (int j = 0; j < T::MI; ++j) {
-                        if constexpr (P == 3) {
-                            acc[i][j] = mfma(b[2][i], a[0][j], acc[i][j]);
-                            acc[i][j] = mfma(b[0][i], a[2][j], acc[i][j]);
-                            acc[i][j] = mfma(b[1][i], a[1][j], acc[i][j]);
-                        }
-                        if constexpr (P >= 2) {
-                            acc[i][j] = mfma(b[1][i], a[0][j], acc[i][j]);
-                            acc[i][j] = mfma(b[0][i], a[1][j], acc[i][j]);
-                        }
-                        acc[i][j] = mfma(b[0][i], a[0][j], acc[i][j]);
-                    }
-            }
+            compute();
             if constexpr (T::STAGES == 2) buf ^= 1;
             else __syncthreads();
             if (more) {
@@ -388,8 +438,43 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
             }
         }
     };
+    if constexpr (WHOLE) {
+        steps(std::false_type{}, k0, k1);
+        return;
+    }
     const int64_t whole = edge ? k0 : k0 + (k1 - k0) / BK * BK;
-    if (whole > k0) steps(std::false_type{}, k0, whole);
+    if constexpr (DIRECT) {
+        static_assert(P == 1 && T::STAGES == 2 && BK == 64, "direct loads");
+        Direct<S, T::BM, BK, T::NT, ACOL> da;
+        Direct<S, T::BN, BK, T::NT, BCOL> db;
+        da.init(A, m0);
+        db.init(B, n0);
+        // LDS reads of the second half of a step between the products of the first
+        constexpr int kReads = T::MI * (ACOL ? 2 : 1) + T::NI * (BCOL ? 2 : 1), kProducts = T::MI * T::NI;
+        auto next = [&](int64_t k) {
+            db.load(k, B.ld, lds.b[buf]);
+            da.load(k, A.ld, lds.a[buf]);
+        };
+        if (whole > k0) next(k0);
+        for (int64_t k = k0; k < whole; k += BK) {
+            done();
+            __syncthreads();
+            buf ^= 1;
+            if (k + BK < whole) next(k + BK);
+            buf ^= 1;
+            compute();
+            __builtin_amdgcn_sched_group_barrier(0x100, kReads, 0);
+#pragma unroll
+            for (int g = 0; g < kReads; ++g) {
+                __builtin_amdgcn_sched_group_barrier(0x008, kProducts / kReads > 0 ? kProducts / kReads : 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, 2 * kProducts, 0);
+            buf ^= 1;
+        }
+    } else {
+        if (whole > k0) steps(std::false_type{}, k0, whole);
+    }
     if (whole < k1) {
         if (whole > k0) __syncthreads();
         steps(std::true_type{}, whole, k1);

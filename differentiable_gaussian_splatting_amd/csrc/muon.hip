@@ -32,15 +32,15 @@ constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr double kEps = 1e-7;
 constexpr float kScaleX = 32768.0f, kScaleP = 16384.0f;   // of X and G, and of P
 
-// floats from a row of X, G or P to the next
-__host__ __device__ constexpr int64_t padded(int64_t cols) { return (cols + 31) / 32 * 32; }
+__host__ __device__ constexpr int64_t padded(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 constexpr int kThreads = 256;
 constexpr int kPiece = 4096;      // values of a block of the elementwise kernels
 constexpr int kGroup = 40;        // matrices of a launch (kernel arguments within 4 KB)
 
 // A matrix of a group.  Its X, G and P start at x, s and s in the group's
-// workspaces; their rows start on cache lines (padded).
+// workspaces, with zeros around them up to whole tiles of the group (unit):
+// the products need no edges, and the zeros stay zeros.
 struct Matrix {
     float *p, *m;
     const void* g;
@@ -49,11 +49,13 @@ struct Matrix {
     int64_t x, s;
     int32_t rows, cols;
     uint32_t piece_end;           // pieces of the matrices up to this one
+    uint32_t start_end;           // of their padded X
     int8_t gtype, ctype;
 };
 struct Job {
     Matrix t[kGroup];
     int32_t count;
+    int32_t unit;                 // to whose multiples the sides in the workspaces are rounded up
 };
 struct MuonConst {
     float mu, lr, keep;           // keep = 1 - lr weight_decay
@@ -62,7 +64,8 @@ struct MuonConst {
 
 struct Shape {
     int64_t x, s;
-    int32_t rows, cols;
+    int32_t rows, cols;           // padded
+    int32_t side, length;         // the shorter and the longer side up to a whole step of k: beyond are zeros
     uint32_t tile_end;            // tiles of the matrices up to this one
 };
 struct MmJob {
@@ -100,24 +103,54 @@ __device__ __forceinline__ float gradient(const Matrix& t, int64_t r, int64_t c)
     return x;
 }
 
-// The calling thread's values of a piece: f(flat index, row, column).
+// The calling thread's values of a piece, four neighbours at a time:
+// f(flat index, values, row, column of the first).
 template <typename F>
-__device__ __forceinline__ void each_value(const Matrix& t, uint32_t piece, F&& f)
+__device__ __forceinline__ void each_four(int64_t n, int32_t cols, uint32_t piece, F&& f)
 {
-    const int64_t first = (int64_t)piece * kPiece, end = min((int64_t)t.rows * t.cols, first + kPiece);
-    const int32_t down = kThreads / t.cols, along = kThreads % t.cols;
-    int64_t i = first + threadIdx.x, r = i / t.cols;
-    int32_t c = (int32_t)(i - r * t.cols);
-#pragma unroll 4
-    for (; i < end; i += kThreads) {
-        f(i, r, c);
+    const int64_t first = (int64_t)piece * kPiece, end = min(n, first + kPiece);
+    const int32_t down = kThreads * 4 / cols, along = kThreads * 4 % cols;
+    int64_t i = first + threadIdx.x * 4, r = i / cols;
+    int32_t c = (int32_t)(i - r * cols);
+#pragma unroll 2
+    for (; i < end; i += kThreads * 4) {
+        f(i, (int)min((int64_t)4, end - i), r, c);
         r += down;
         c += along;
-        if (c >= t.cols) {
-            c -= t.cols;
+        if (c >= cols) {
+            c -= cols;
             ++r;
         }
     }
+}
+
+// four neighbours from (r, c) on of a matrix whose rows are ld apart
+template <typename S>
+__device__ __forceinline__ f32x4 four_of(const S* p, int64_t ld, int32_t cols, int64_t i, int valid, int64_t r, int32_t c)
+{
+    f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+    if (ld == cols && valid == 4) {
+        const gst::Pack<S, 4> x = gst::load<S, 4>(p + i);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) v[j] = (float)x.v[j];
+        return v;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        if (j < valid) v[j] = (float)p[r * ld + c];
+        if (++c == cols) {
+            c = 0;
+            ++r;
+        }
+    }
+    return v;
+}
+
+__device__ __forceinline__ f32x4 four_gradients(const Matrix& t, int64_t i, int valid, int64_t r, int32_t c)
+{
+    f32x4 v;
+    with_type_device(t.gtype, [&](auto s) { v = four_of((const decltype(s)*)t.g, t.gld, t.cols, i, valid, r, c); });
+    return v;
 }
 
 // sum over a block of W waves, in a fixed order
@@ -144,17 +177,25 @@ __global__ __launch_bounds__(kThreads) void k_momentum(const Job job, const Muon
     uint32_t before;
     const Matrix& t = job.t[matrix_of(job, blockIdx.x, [](const Matrix& q) { return q.piece_end; }, before)];
     double sum = 0.0;
-    each_value(t, blockIdx.x - before, [&](int64_t i, int64_t r, int32_t c) {
-        const float g = f * gradient(t, r, c), m = o.mu * t.m[i] + g;
-        t.m[i] = m;
-        const float u = o.nesterov ? g + o.mu * m : m;
-        sum += (double)u * u;
+    each_four((int64_t)t.rows * t.cols, t.cols, blockIdx.x - before, [&](int64_t i, int valid, int64_t r, int32_t c) {
+        const f32x4 g = f * four_gradients(t, i, valid, r, c);
+        const f32x4 m = o.mu * four_of(t.m, t.cols, t.cols, i, valid, r, c) + g;
+        const f32x4 u = o.nesterov ? g + o.mu * m : m;
+        if (valid == 4) {
+            gst::store<float, 4>(t.m + i, __builtin_bit_cast(Four, m));
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < valid) t.m[i + j] = m[j];
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum += j < valid ? (double)u[j] * u[j] : 0.0;
     });
     sum = block_sum<4>(sum, sums);
     if (threadIdx.x == 0) part[blockIdx.x] = sum;
 }
 
-// X = u / (|u| + eps)
+// X = u / (|u| + eps), zeros around it; a block per piece of padded X
 __global__ __launch_bounds__(kThreads) void k_start(const Job job, const MuonConst o, const float* __restrict__ norm,
                                                     const double* __restrict__ part, float* __restrict__ x)
 {
@@ -162,14 +203,30 @@ __global__ __launch_bounds__(kThreads) void k_start(const Job job, const MuonCon
     if (norm && !isfinite(norm[0])) return;
     const float f = norm ? norm[1] : 1.0f;
     uint32_t before;
-    const Matrix& t = job.t[matrix_of(job, blockIdx.x, [](const Matrix& q) { return q.piece_end; }, before)];
+    const int k = matrix_of(job, blockIdx.x, [](const Matrix& q) { return q.start_end; }, before);
+    const Matrix& t = job.t[k];
     double sum = 0.0;
-    for (uint32_t b = before + threadIdx.x; b < t.piece_end; b += kThreads) sum += part[b];
+    for (uint32_t b = (k ? job.t[k - 1].piece_end : 0u) + threadIdx.x; b < t.piece_end; b += kThreads) sum += part[b];
     const float inv = (float)(1.0 / (sqrt(block_sum<4>(sum, sums)) + kEps));
-    const int64_t ld = padded(t.cols);
-    each_value(t, blockIdx.x - before, [&](int64_t i, int64_t r, int32_t c) {
-        const float m = t.m[i];
-        x[t.x + r * ld + c] = (o.nesterov ? f * gradient(t, r, c) + o.mu * m : m) * inv;
+    const int32_t ld = (int32_t)padded(t.cols, job.unit);
+    each_four(padded(t.rows, job.unit) * ld, ld, blockIdx.x - before, [&](int64_t i, int, int64_t r, int32_t c) {
+        const int valid = r < t.rows ? min(4, t.cols - c) : 0;   // ld is a multiple of 4: the four share a row
+        f32x4 u = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (valid > 0) {
+            const int64_t at = r * t.cols + c;
+            u = four_of(t.m, t.cols, t.cols, at, valid, r, c);
+            if (o.nesterov) {
+                f32x4 g;
+                with_type_device(t.gtype, [&](auto s) {
+                    typedef decltype(s) S;
+                    g = four_of((const S*)t.g + r * t.gld, t.cols, t.cols, c, valid, 0, c);
+                });
+                u = f * g + o.mu * u;
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j) u[j] = j < valid ? u[j] * inv : 0.0f;
+        }
+        *reinterpret_cast<f32x4*>(x + t.x + i) = u;
     });
 }
 
@@ -192,9 +249,25 @@ __global__ __launch_bounds__(kThreads) void k_apply(const Job job, const MuonCon
     uint32_t before;
     const Matrix& t = job.t[matrix_of(job, blockIdx.x, [](const Matrix& q) { return q.piece_end; }, before)];
     const float rate = update_rate(o, t.rows, t.cols);
-    const int64_t ld = padded(t.cols);
-    each_value(t, blockIdx.x - before, [&](int64_t i, int64_t r, int32_t c) {
-        write_parameter(t, i, t.p[i] * o.keep - rate * x[t.x + r * ld + c]);
+    const int32_t ld = (int32_t)padded(t.cols, job.unit);
+    each_four((int64_t)t.rows * t.cols, t.cols, blockIdx.x - before, [&](int64_t i, int valid, int64_t r, int32_t c) {
+        const f32x4 p = four_of(t.p, t.cols, t.cols, i, valid, r, c) * o.keep -
+                        rate * four_of(x + t.x, ld, t.cols, i, valid, r, c);
+        if (valid == 4) {
+            gst::store<float, 4>(t.p + i, __builtin_bit_cast(Four, p));
+            if (!t.copy) return;
+            with_type_device(t.ctype, [&](auto s) {
+                typedef decltype(s) S;
+                gst::Pack<S, 4> v;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) v.v[j] = gst::narrow<S>(p[j]);
+                gst::store<S, 4>((S*)t.copy + i, v);
+            });
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (j < valid) write_parameter(t, i + j, p[j]);
+        }
     });
 }
 
@@ -202,10 +275,10 @@ enum { kGram, kPoly, kNext };
 
 // One tile of a matrix's product: G (kGram), P from G (kPoly) or the next X.
 // G and P are symmetric: their tiles on and below the diagonal are computed and
-// those below it written to both places.
+// those below it written to both places.  Sides are the padded ones.
 template <int KIND, bool TALL, typename T>
 __global__ __launch_bounds__(T::NT, 2) void k_newton(const MmJob job, const float* __restrict__ from, float* __restrict__ to,
-                                                  const float* __restrict__ poly, int splits, int64_t split_size)
+                                                     const float* __restrict__ poly, int splits, int64_t split_size)
 {
     constexpr bool ACOL = KIND == kGram && TALL, BCOL = ACOL || (KIND == kNext && !TALL);
     __shared__ Lds<float, 2, T> lds;
@@ -213,76 +286,57 @@ __global__ __launch_bounds__(T::NT, 2) void k_newton(const MmJob job, const floa
     const uint32_t tiles = gridDim.x / (uint32_t)splits, split = KIND == kGram ? b / tiles : 0;
     if constexpr (KIND == kGram) b -= split * tiles;
     const Shape t = job.t[matrix_of(job, b, [](const Shape& q) { return q.tile_end; }, before)];
-    const int64_t side = TALL ? t.cols : t.rows, length = TALL ? t.rows : t.cols;
+    const int64_t side = TALL ? t.cols : t.rows;
     const int64_t m = KIND == kNext ? t.rows : side, n = KIND == kNext ? t.cols : side;
-    const int64_t k = KIND == kGram ? length : side;
     int64_t i, j;
     if constexpr (KIND == kNext) {
-        tile_at(b - before, (m + T::BM - 1) / T::BM, (n + T::BN - 1) / T::BN, i, j);
+        tile_at(b - before, m / T::BM, n / T::BN, i, j);
     } else {
         static_assert(T::BM == T::BN, "square tiles");
-        const int t = (int)(b - before);
-        int r = (int)((sqrtf(8.0f * (float)t + 1.0f) - 1.0f) * 0.5f);
-        while (r * (r + 1) / 2 > t) --r;
-        while ((r + 1) * (r + 2) / 2 <= t) ++r;
+        const int q = (int)(b - before);
+        int r = (int)((sqrtf(8.0f * (float)q + 1.0f) - 1.0f) * 0.5f);
+        while (r * (r + 1) / 2 > q) --r;
+        while ((r + 1) * (r + 2) / 2 <= q) ++r;
         i = r;
-        j = t - r * (r + 1) / 2;
+        j = q - r * (r + 1) / 2;
     }
     const float* src = from + (KIND == kPoly ? t.s : t.x);
-    const int64_t lds_ = padded(side), ldx = padded(t.cols);   // of G and P, of X
-    const Operand x = {src, KIND == kPoly ? lds_ : ldx, KIND == kPoly ? side : KIND == kGram ? side : TALL ? m : n,
-                       kScaleX, 0};
+    const Operand x = {src, KIND == kPoly ? side : t.cols, 0, kScaleX, 0};
     Operand a = x, bo = x;
-    if constexpr (KIND == kNext) (TALL ? bo : a) = Operand{poly + t.s, lds_, side, kScaleP, 0};
+    if constexpr (KIND == kNext) (TALL ? bo : a) = Operand{poly + t.s, side, 0, kScaleP, 0};
+    a.rows = m;
+    bo.rows = n;
     f32x4 acc[T::NI][T::MI];
 #pragma unroll
     for (int q = 0; q < T::NI; ++q)
 #pragma unroll
         for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t k0 = 0, k1 = k;
+    int64_t k0 = 0, k1 = KIND == kGram ? t.length : t.side;
     if constexpr (KIND == kGram) {
-        const int64_t each = ((k + T::BK - 1) / T::BK + splits - 1) / splits * T::BK;
-        k0 = min(k, split * each);
-        k1 = min(k, k0 + each);
+        const int64_t each = (t.length / T::BK + splits - 1) / splits * T::BK;
+        k0 = min((int64_t)t.length, split * each);
+        k1 = min((int64_t)t.length, k0 + each);
     }
-    mm_tile<float, 2, ACOL, BCOL, T>(a, bo, i * T::BM, j * T::BN, k0, k1, lds, acc);
+    mm_tile<float, 2, ACOL, BCOL, T, true>(a, bo, i * T::BM, j * T::BN, k0, k1, lds, acc);
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t mw = i * T::BM + (wave % T::WM) * T::MI * 16 + (lane & 15);
-    const int64_t nw = j * T::BN + (wave / T::WM) * T::NI * 16 + (lane >> 4) * 4;
+    const int64_t row0 = i * T::BM + (wave % T::WM) * T::MI * 16 + (lane & 15);
+    const int64_t col0 = j * T::BN + (wave / T::WM) * T::NI * 16 + (lane >> 4) * 4;
     const float down = 1.0f / kScaleX / (KIND == kNext ? kScaleP : kScaleX);
     float* dst = to + (KIND == kNext ? t.x : t.s) + (KIND == kGram ? split * split_size : 0);
-    const int64_t ld = KIND == kNext ? ldx : lds_;
 #pragma unroll
     for (int r = 0; r < T::MI; ++r) {
-        const int64_t row = mw + r * 16;
-        if (row >= m) continue;
 #pragma unroll
         for (int q = 0; q < T::NI; ++q) {
-            const int64_t col = nw + q * 16, at = row * ld + col;
-            if (col >= n) continue;
-            const int valid = (int)min((int64_t)4, n - col);
-            f32x4 y = acc[q][r] * down, old = y;
+            const int64_t row = row0 + r * 16, col = col0 + q * 16, at = row * n + col;
+            f32x4 y = acc[q][r] * down;
             if constexpr (KIND != kGram) {
-                if (valid == 4) {
-                    old = __builtin_bit_cast(f32x4, gst::load<float, 4>(src + at));
-                } else {
-#pragma unroll
-                    for (int w = 0; w < 4; ++w)
-                        if (w < valid) old[w] = src[at + w];
-                }
+                const f32x4 old = *reinterpret_cast<const f32x4*>(src + at);
                 y = KIND == kPoly ? kC * y + kB * old : y + kA * old;
             }
-            if (valid == 4) {
-                gst::store<float, 4>(dst + at, __builtin_bit_cast(Four, y));
-            } else {
-#pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (w < valid) dst[at + w] = y[w];
-            }
+            *reinterpret_cast<f32x4*>(dst + at) = y;
             if (KIND != kNext && i != j) {
 #pragma unroll
-                for (int w = 0; w < 4; ++w)
-                    if (w < valid) dst[(col + w) * ld + row] = y[w];
+                for (int w = 0; w < 4; ++w) dst[(col + w) * n + row] = y[w];
             }
         }
     }
@@ -300,36 +354,37 @@ __global__ __launch_bounds__(kThreads) void k_sum_splits(float* __restrict__ g, 
 
 typedef Tile<256, 256, 32, 2, 4, 2> Large;
 typedef Tile<128, 128, 32, 2, 2, 1> Medium;
-typedef Tile<64, 64, 32, 2, 2, 2> Small;
-typedef Tile<64, 64, 32, 2, 2, 2, true> Tiny;
+typedef Tile<64, 64, 64, 2, 2, 1> Small;
 
-// tiles of a matrix's product
+// tiles of a matrix's product, of its padded sides
 template <int KIND>
-int64_t tiles_of(const Matrix& t, int bm, int bn)
+int64_t tiles_of(const Matrix& t, int64_t unit, int b)
 {
-    const int64_t side = std::min(t.rows, t.cols), s = ceil_div(side, bm);
-    return KIND == kNext ? ceil_div(t.rows, bm) * ceil_div(t.cols, bn) : s * (s + 1) / 2;
+    const int64_t rows = padded(t.rows, unit) / b, cols = padded(t.cols, unit) / b, s = std::min(rows, cols);
+    return KIND == kNext ? rows * cols : s * (s + 1) / 2;
 }
 
 // the matrices whose products share launches, and the floats of their X and G
 struct Group {
     Job job;
     int64_t x, s;
-    uint32_t pieces;
-    bool tall, tiny;              // more rows than columns; a side below 8 (Stage in mm.h)
+    uint32_t pieces, starts;
+    bool tall;                    // more rows than columns
     int splits;                   // of G's products
 };
 
 template <int KIND, bool TALL, typename T>
 void launch_tiles(gs_ctx* ctx, const Group& q, const float* from, float* to, const float* poly)
 {
-    const int splits = KIND == kGram ? q.splits : 1;
+    const int splits = KIND == kGram ? q.splits : 1, unit = q.job.unit;
     MmJob mm{};
     uint32_t tiles = 0;
     for (int32_t k = 0; k < q.job.count; ++k) {
         const Matrix& t = q.job.t[k];
-        tiles += (uint32_t)tiles_of<KIND>(t, T::BM, T::BN);
-        mm.t[mm.count++] = Shape{t.x, t.s, t.rows, t.cols, tiles};
+        tiles += (uint32_t)tiles_of<KIND>(t, unit, T::BM);
+        mm.t[mm.count++] = Shape{t.x, t.s, (int32_t)padded(t.rows, unit), (int32_t)padded(t.cols, unit),
+                               (int32_t)padded(std::min(t.rows, t.cols), T::BK), (int32_t)padded(std::max(t.rows, t.cols), T::BK),
+                               tiles};
     }
     hipLaunchKernelGGL((k_newton<KIND, TALL, T>), dim3(tiles * splits), dim3(T::NT), 0, ctx->stream, mm, from, to, poly,
                        splits, q.s);
@@ -342,34 +397,41 @@ void launch_tiles(gs_ctx* ctx, const Group& q, const float* from, float* to, con
 // once us for every round of `resident` tiles on each compute unit and each us
 // for every tile (measured: 128 x 128 takes 1.3 and 2.0 us for one and two a
 // unit, 64 x 64 0.9, 1.5 and 3.1 for two, four and eight, 256 x 256 3.1).
-template <int KIND, typename T>
-double cost_us(const gs_ctx* ctx, const Job& job, int splits, int resident, double once, double each)
+struct TileCost {
+    int b, resident;
+    double once, each;
+};
+constexpr TileCost kCosts[3] = {{Large::BM, 1, 0.1, 3.0}, {Medium::BM, 2, 0.5, 0.75}, {Small::BM, 4, 0.2, 0.33}};
+
+template <int KIND>
+double cost_us(const gs_ctx* ctx, const Job& job, int64_t unit, int splits, const TileCost& c)
 {
-    int64_t work = 0, longest = 0, tiles = 0;
+    double work = 0.0, longest = 0.0;
+    int64_t tiles = 0;
     for (int32_t k = 0; k < job.count; ++k) {
         const Matrix& t = job.t[k];
-        const int64_t steps = ceil_div(ceil_div(KIND == kGram ? std::max(t.rows, t.cols) : std::min(t.rows, t.cols), T::BK), splits);
-        const int64_t n = tiles_of<KIND>(t, T::BM, T::BN) * splits;
+        const double steps = (double)ceil_div(KIND == kGram ? std::max(t.rows, t.cols) : std::min(t.rows, t.cols), 32 * splits) + 2.0;
+        const int64_t n = tiles_of<KIND>(t, unit, c.b) * splits;
         tiles += n;
-        work += n * (steps + 1);
-        longest = std::max(longest, steps + 1);
+        work += (double)n * steps;
+        longest = std::max(longest, steps);
     }
-    const int64_t rounds = ceil_div(tiles, (int64_t)resident * ctx->num_cu), on_each = ceil_div(tiles, ctx->num_cu);
-    return std::max((double)work / (double)tiles * ((double)rounds * once + (double)on_each * each),
-                    (double)longest * (once + each));
+    const int64_t rounds = ceil_div(tiles, (int64_t)c.resident * ctx->num_cu), on_each = ceil_div(tiles, ctx->num_cu);
+    return std::max(work / (double)tiles * ((double)rounds * c.once + (double)on_each * c.each), longest * (c.once + c.each));
 }
 
-// the cheapest tile, and its cost
+// the cheapest tile of those that the unit is a multiple of, and its cost
 template <int KIND>
-int choose_tile(const gs_ctx* ctx, const Job& job, int splits, double* us)
+int choose_tile(const gs_ctx* ctx, const Job& job, int64_t unit, int splits, double* us)
 {
-    const double cost[3] = {cost_us<KIND, Large>(ctx, job, splits, 1, 0.1, 3.0),
-                            cost_us<KIND, Medium>(ctx, job, splits, 2, 0.5, 0.75),
-                            cost_us<KIND, Small>(ctx, job, splits, 5, 0.25, 0.33)};
-    int best = 0;
-    for (int k = 1; k < 3; ++k)
-        if (cost[k] < cost[best]) best = k;
-    *us = cost[best];
+    int best = 2;
+    *us = cost_us<KIND>(ctx, job, unit, splits, kCosts[2]);
+    for (int k = 1; k >= 0 && unit % kCosts[k].b == 0; --k) {
+        const double c = cost_us<KIND>(ctx, job, unit, splits, kCosts[k]);
+        if (c >= *us) continue;
+        *us = c;
+        best = k;
+    }
     return best;
 }
 
@@ -377,29 +439,38 @@ template <int KIND, bool TALL>
 void launch_newton(gs_ctx* ctx, const Group& q, const float* from, float* to, const float* poly)
 {
     double us;
-    const int tile = choose_tile<KIND>(ctx, q.job, KIND == kGram ? q.splits : 1, &us);
-    if (q.tiny) launch_tiles<KIND, TALL, Tiny>(ctx, q, from, to, poly);
-    else if (tile == 0) launch_tiles<KIND, TALL, Large>(ctx, q, from, to, poly);
+    const int tile = choose_tile<KIND>(ctx, q.job, q.job.unit, KIND == kGram ? q.splits : 1, &us);
+    if (tile == 0) launch_tiles<KIND, TALL, Large>(ctx, q, from, to, poly);
     else if (tile == 1) launch_tiles<KIND, TALL, Medium>(ctx, q, from, to, poly);
     else launch_tiles<KIND, TALL, Small>(ctx, q, from, to, poly);
 }
 
-// How often G's product is split over its long k: few tiles, a few matrices of
-// one long side each, leave the card idle otherwise.
-int choose_splits(const gs_ctx* ctx, const Group& q)
+// The unit to which a group's sides are padded (the largest tile it may use),
+// and how often G's product is split over its long k (few tiles, a few
+// matrices of one long side each, leave the card idle otherwise).
+void choose_sizes(const gs_ctx* ctx, Group* q)
 {
-    int best = 1;
     double least = 0.0;
-    for (int s = 1; s <= 32; s *= 2) {
-        if (s > 1 && s * q.s > (1ll << 26)) break;
-        double us;
-        choose_tile<kGram>(ctx, q.job, s, &us);
-        if (s > 1) us += 5.0 + 4.0 * (s + 1) * q.s / 3e6;   // the sums' launch and bytes
-        if (s > 1 && us >= least) continue;
-        least = us;
-        best = s;
+    for (int unit = 64; unit <= 256; unit *= 2) {
+        double poly, next, gram;
+        choose_tile<kPoly>(ctx, q->job, unit, 1, &poly);
+        choose_tile<kNext>(ctx, q->job, unit, 1, &next);
+        int64_t s = 0;
+        for (int32_t k = 0; k < q->job.count; ++k) {
+            const int64_t side = padded(std::min(q->job.t[k].rows, q->job.t[k].cols), unit);
+            s += side * side;
+        }
+        for (int splits = 1; splits <= 32; splits *= 2) {
+            if (splits > 1 && splits * s > (1ll << 26)) break;
+            choose_tile<kGram>(ctx, q->job, unit, splits, &gram);
+            if (splits > 1) gram += 5.0 + 4.0 * (splits + 1) * s / 3e6;   // the sums' launch and bytes
+            const double us = gram + poly + next;
+            if (least > 0.0 && us >= least) continue;
+            least = us;
+            q->job.unit = unit;
+            q->splits = splits;
+        }
     }
-    return best;
 }
 
 template <bool TALL>
@@ -434,7 +505,7 @@ struct SmallLds {
 template <int W>
 constexpr bool fits(int64_t rows, int64_t cols)
 {
-    const int64_t s = padded(std::min(rows, cols)), l = padded(std::max(rows, cols));
+    const int64_t s = padded(std::min(rows, cols), 32), l = padded(std::max(rows, cols), 32);
     return s <= SmallLds<W>::kG && s * l <= SmallLds<W>::kBlock;
 }
 
@@ -507,7 +578,7 @@ __global__ __launch_bounds__(W * 64) void k_small(const Job job, const MuonConst
     const Matrix& t = job.t[blockIdx.x];
     const bool tall = t.rows > t.cols;
     const int s = tall ? t.cols : t.rows, l = tall ? t.rows : t.cols;
-    const int S = (int)padded(s), L = (int)padded(l), ldx = L + 8, ldg = S + 8;
+    const int S = (int)padded(s, 32), L = (int)padded(l, 32), ldx = L + 8, ldg = S + 8;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     // the wave's blocks: row and column of X, and of G
     const int xm = wave % (S / 32) * 32, xn = wave / (S / 32) * 32, gm = xm, gn = xn;
@@ -614,38 +685,42 @@ gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
     const MuonConst c = {(float)o->momentum, (float)o->lr, (float)(1.0 - o->lr * o->weight_decay), o->nesterov};
     const auto describe = [&](int32_t k) {
         return Matrix{(float*)p[k].data, (float*)m[k].data, g[k].data, copies ? copies[k].data : nullptr, g[k].stride, 0, 0,
-                      (int32_t)p[k].rows, (int32_t)p[k].cols, 0, (int8_t)g[k].type, (int8_t)(copies ? copies[k].type : 0)};
+                      (int32_t)p[k].rows, (int32_t)p[k].cols, 0, 0, (int8_t)g[k].type, (int8_t)(copies ? copies[k].type : 0)};
     };
     const auto small = [&](int32_t k) { return fits<16>(p[k].rows, p[k].cols); };
     std::vector<Group> groups;
     int64_t x = 0, s = 0, pieces = 0;
-    for (int kind = 0; kind < 4; ++kind) {
-        const bool tall = kind & 1, tiny = kind & 2;
+    for (int tall = 0; tall < 2; ++tall) {
         bool open = false;
+        int64_t held = 0;
         for (int32_t k = 0; k < n; ++k) {
-            const int64_t rows = p[k].rows, cols = p[k].cols, side = std::min(rows, cols);
-            const int64_t values = rows * padded(cols);
-            if (rows * cols == 0 || small(k) || (rows > cols) != tall || (side < 8) != tiny) continue;
-            if (open && (groups.back().job.count == kGroup || groups.back().x + values > kGroupValues)) open = false;
+            const int64_t rows = p[k].rows, cols = p[k].cols;
+            if (rows * cols == 0 || small(k) || (rows > cols) != (tall == 1)) continue;
+            const int64_t values = padded(rows, 64) * padded(cols, 64);
+            if (open && (groups.back().job.count == kGroup || held + values > kGroupValues)) open = false;
             if (!open) {
                 groups.push_back(Group{});
-                groups.back().tall = tall;
-                groups.back().tiny = tiny;
+                groups.back().tall = tall == 1;
                 open = true;
+                held = 0;
             }
-            Group& q = groups.back();
-            q.pieces += (uint32_t)ceil_div(rows * cols, kPiece);
-            Matrix t = describe(k);
-            t.x = q.x;
-            t.s = q.s;
-            t.piece_end = q.pieces;
-            q.job.t[q.job.count++] = t;
-            q.x += values;
-            q.s += side * padded(side);
+            held += values;
+            Job& job = groups.back().job;
+            job.t[job.count++] = describe(k);
         }
     }
     for (Group& q : groups) {
-        q.splits = choose_splits(ctx, q);
+        choose_sizes(ctx, &q);
+        for (int32_t k = 0; k < q.job.count; ++k) {
+            Matrix& t = q.job.t[k];
+            const int64_t rows = padded(t.rows, q.job.unit), cols = padded(t.cols, q.job.unit), side = std::min(rows, cols);
+            t.x = q.x;
+            t.s = q.s;
+            q.x += rows * cols;
+            q.s += side * side;
+            t.piece_end = q.pieces += (uint32_t)ceil_div((int64_t)t.rows * t.cols, kPiece);
+            t.start_end = q.starts += (uint32_t)ceil_div(rows * cols, kPiece);
+        }
         x = std::max(x, q.x);
         s = std::max(s, (q.splits + 1) * q.s);   // G's splits, then P
         pieces = std::max<int64_t>(pieces, q.pieces);
@@ -674,7 +749,7 @@ gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
         float *now = xs, *other = xs + x;
         const dim3 grid(q.pieces), block(kThreads);
         hipLaunchKernelGGL(k_momentum, grid, block, 0, ctx->stream, q.job, c, norm, part);
-        hipLaunchKernelGGL(k_start, grid, block, 0, ctx->stream, q.job, c, norm, part, now);
+        hipLaunchKernelGGL(k_start, dim3(q.starts), block, 0, ctx->stream, q.job, c, norm, part, now);
         if (q.tall) newton_schulz<true>(ctx, q, o->steps, &now, &other, ss, ss + q.splits * q.s);
         else newton_schulz<false>(ctx, q, o->steps, &now, &other, ss, ss + q.splits * q.s);
         hipLaunchKernelGGL(k_apply, grid, block, 0, ctx->stream, q.job, c, norm, now);
