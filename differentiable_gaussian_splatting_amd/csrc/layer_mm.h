@@ -21,86 +21,87 @@ namespace gsm {
 
 typedef gst::Pack<float, 4> Four;
 
+// Values [first, valid) of the four from p[at] on.
 template <typename S>
-__device__ __forceinline__ f32x4 load4(const void* p, int64_t at, int type, int valid)
+__device__ __forceinline__ f32x4 load4(const void* p, int64_t at, int type, int valid, int first = 0)
 {
     f32x4 r = {0.0f, 0.0f, 0.0f, 0.0f};
     if (type == GS_F32) {
         const float* q = (const float*)p + at;
-        if (valid >= 4) return __builtin_bit_cast(f32x4, gst::load<float, 4>(q));
+        if (valid >= 4 && first == 0) return __builtin_bit_cast(f32x4, gst::load<float, 4>(q));
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            if (j < valid) r[j] = q[j];
+            if (j >= first && j < valid) r[j] = q[j];
     } else {
         const S* q = (const S*)p + at;
-        if (valid >= 4) {
+        if (valid >= 4 && first == 0) {
             const gst::Pack<S, 4> v = gst::load<S, 4>(q);
 #pragma unroll
             for (int j = 0; j < 4; ++j) r[j] = (float)v.v[j];
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < valid) r[j] = (float)q[j];
+                if (j >= first && j < valid) r[j] = (float)q[j];
         }
     }
     return r;
 }
 
 template <typename S>
-__device__ __forceinline__ void store4(void* p, int64_t at, int type, int valid, f32x4 x)
+__device__ __forceinline__ void store4(void* p, int64_t at, int type, int valid, f32x4 x, int first = 0)
 {
     if (type == GS_F32) {
         float* q = (float*)p + at;
-        if (valid >= 4) {
+        if (valid >= 4 && first == 0) {
             gst::store<float, 4>(q, __builtin_bit_cast(Four, x));
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < valid) q[j] = x[j];
+                if (j >= first && j < valid) q[j] = x[j];
         }
     } else {
         S* q = (S*)p + at;
         gst::Pack<S, 4> v;
 #pragma unroll
         for (int j = 0; j < 4; ++j) v.v[j] = gst::narrow<S>(x[j]);
-        if (valid >= 4) {
+        if (valid >= 4 && first == 0) {
             gst::store<S, 4>(q, v);
         } else {
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (j < valid) q[j] = v.v[j];
+                if (j >= first && j < valid) q[j] = v.v[j];
         }
     }
 }
 
-// columns n .. n + 3 of row m of the product
+// columns n + first .. n + 3 of row m of the product
 template <typename S>
-__device__ __forceinline__ void epilogue(const Epilogue& e, int64_t m, int64_t n, f32x4 z)
+__device__ __forceinline__ void epilogue(const Epilogue& e, int64_t m, int64_t n, f32x4 z, int first = 0)
 {
     const int valid = (int)min((int64_t)4, e.n - n);
-    if (e.bias) z += load4<S>(e.bias, n, e.bias_type, valid);
-    if (e.pre) store4<S>(e.pre, m * e.ldpre + n, e.pre_type, valid, z);
+    if (e.bias) z += load4<S>(e.bias, n, e.bias_type, valid, first);
+    if (e.pre) store4<S>(e.pre, m * e.ldpre + n, e.pre_type, valid, z, first);
     if (e.act != GS_ACT_NONE) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) z[j] = act_value(z[j], e.act);
     }
-    if (e.res) z += load4<S>(e.res, m * e.ldres + n, e.res_type, valid);
-    store4<S>(e.out, m * e.ldout + n, e.out_type, valid, z);
+    if (e.res) z += load4<S>(e.res, m * e.ldres + n, e.res_type, valid, first);
+    store4<S>(e.out, m * e.ldout + n, e.out_type, valid, z, first);
 }
 
-// columns f .. f + 3 of row m of both halves
+// columns f + first .. f + 3 of row m of both halves
 template <typename S>
-__device__ __forceinline__ void epilogue_gated(const Epilogue& e, int64_t m, int64_t f, f32x4 g, f32x4 u)
+__device__ __forceinline__ void epilogue_gated(const Epilogue& e, int64_t m, int64_t f, f32x4 g, f32x4 u, int first = 0)
 {
     const int valid = (int)min((int64_t)4, e.n - f);
     if (e.pre) {
-        store4<S>(e.pre, m * e.ldpre + f, e.pre_type, valid, g);
-        store4<S>(e.pre, m * e.ldpre + e.n + f, e.pre_type, valid, u);
+        store4<S>(e.pre, m * e.ldpre + f, e.pre_type, valid, g, first);
+        store4<S>(e.pre, m * e.ldpre + e.n + f, e.pre_type, valid, u, first);
     }
     f32x4 y;
 #pragma unroll
     for (int j = 0; j < 4; ++j) y[j] = act_value(g[j], e.act) * u[j];
-    store4<S>(e.out, m * e.ldout + f, e.out_type, valid, y);
+    store4<S>(e.out, m * e.ldout + f, e.out_type, valid, y, first);
 }
 
 // A wave's LDS writes are there for its own reads.
@@ -120,6 +121,7 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
         Lds<S, P, T> tile;
         float out[T::NT / 64 * 32 * kRow];
     } lds;
+    constexpr int G = GATED ? 2 : 1;
     const int64_t rest = g.tm * g.tn - g.full, total = g.full + rest * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
@@ -135,7 +137,8 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
             ws = g.ws + at * (T::BM * T::BN);
         }
         tile_at(tile, g.tm, g.tn, i, j);
-        const int64_t m0 = i * T::BM, n0 = j * T::BN;
+        const Span sm = span_of(i, T::BM, g.a.rows), sn = span_of(j, T::BN / G, GATED ? g.e.n : g.b.rows);
+        const int64_t m0 = sm.at, n0 = sn.at * G;
         f32x4 acc[T::NI][T::MI];
 #pragma unroll
         for (int q = 0; q < T::NI; ++q)
@@ -149,7 +152,7 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
         __syncthreads();
         float* mine = reinterpret_cast<float*>(&lds) + wave * 32 * kRow;
         const int64_t mw = m0 + (wave % T::WM) * T::MI * 16;
-        const int64_t nw = n0 / (GATED ? 2 : 1) + (wave / T::WM) * kCols;
+        const int64_t nw = sn.at + (wave / T::WM) * kCols;
 #pragma unroll
         for (int r = 0; r < T::MI; r += 2) {
             if (mw + r * 16 >= g.m) break;
@@ -162,7 +165,8 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
             for (int t = lane; t < 32 * kCols / 4; t += 64) {
                 const int row = t / (kCols / 4), c = t % (kCols / 4) * 4;
                 const int64_t m = mw + r * 16 + row, n = nw + c;
-                if (m >= g.m || n >= g.e.n) continue;
+                if (m >= g.m || n >= g.e.n || m < sm.own || n + 3 < sn.own) continue;
+                const int first = (int)max((int64_t)0, sn.own - n);
                 const float* v = mine + row * kRow + (GATED ? (c >> 4) * 32 + (c & 15) : c);
                 const f32x4 x = *reinterpret_cast<const f32x4*>(v);
                 if (ws) {
@@ -170,9 +174,9 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
                     *reinterpret_cast<f32x4*>(w) = x;
                     if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = *reinterpret_cast<const f32x4*>(v + 16);
                 } else if constexpr (GATED) {
-                    epilogue_gated<S>(g.e, m, n, x, *reinterpret_cast<const f32x4*>(v + 16));
+                    epilogue_gated<S>(g.e, m, n, x, *reinterpret_cast<const f32x4*>(v + 16), first);
                 } else {
-                    epilogue<S>(g.e, m, n, x);
+                    epilogue<S>(g.e, m, n, x, first);
                 }
             }
             wave_fence();
@@ -191,8 +195,9 @@ __global__ __launch_bounds__(256) void k_join(const LayerMm g)
         const int row = t % kQuads / (kCols / 4), c = t % (kCols / 4) * 4;
         int64_t i, j;
         tile_at(g.full + tile, g.tm, g.tn, i, j);
-        const int64_t m = i * T::BM + row, n = j * kCols + c;
-        if (m >= g.m || n >= g.e.n) continue;
+        const Span sm = span_of(i, T::BM, g.a.rows), sn = span_of(j, kCols, GATED ? g.e.n : g.b.rows);
+        const int64_t m = sm.at + row, n = sn.at + c;
+        if (m >= g.m || n >= g.e.n || m < sm.own || n + 3 < sn.own) continue;
         const float* w = g.ws + tile * (T::BM * T::BN) + row * T::BN + (GATED ? (c >> 4) * 32 + (c & 15) : c);
         f32x4 x = {0.0f, 0.0f, 0.0f, 0.0f}, y = x;
 #pragma unroll 4
@@ -200,8 +205,9 @@ __global__ __launch_bounds__(256) void k_join(const LayerMm g)
             x += *reinterpret_cast<const f32x4*>(w + s * rest * (T::BM * T::BN));
             if constexpr (GATED) y += *reinterpret_cast<const f32x4*>(w + s * rest * (T::BM * T::BN) + 16);
         }
-        if constexpr (GATED) epilogue_gated<S>(g.e, m, n, x, y);
-        else epilogue<S>(g.e, m, n, x);
+        const int first = (int)max((int64_t)0, sn.own - n);
+        if constexpr (GATED) epilogue_gated<S>(g.e, m, n, x, y, first);
+        else epilogue<S>(g.e, m, n, x, first);
     }
 }
 
@@ -227,8 +233,7 @@ template <typename S, int P, typename Large, typename Medium, typename Small, ty
 gs_status launch_layer_mm(gs_ctx* ctx, const LayerMm& g)
 {
     GsTimerScope ts(ctx, "layer_mm");
-    const auto aligned = [](const Operand& o) { return (uintptr_t)o.p % 16 == 0 && o.ld * (int64_t)sizeof(S) % 16 == 0; };
-    const bool direct = P == 1 && aligned(g.a) && aligned(g.b);
+    const bool direct = P == 1 && loads_direct(g);
     if (g.tile == kLarge && direct) launch_mode<S, P, Large, P == 1>(ctx, g);
     else if (g.tile == kLarge) launch_mode<S, P, Large, false>(ctx, g);
     else if (g.tile == kMedium && direct) launch_mode<S, P, Medium, P == 1>(ctx, g);

@@ -81,6 +81,18 @@ struct LayerMm {
     bool a_col, b_col, gated;    // a_col only with b_col
 };
 
+// Whether the tiles of a product of 16-bit operands load straight into LDS
+// (Direct in mm.h): rows that start on 16 bytes, and for an operand whose k runs
+// down the columns a multiple of 8 columns, so that a tile moved back to end
+// with them still starts on 16 bytes.
+inline bool loads_direct(const LayerMm& g)
+{
+    const auto fits = [](const Operand& o, bool col) {
+        return (uintptr_t)o.p % 16 == 0 && o.ld % 8 == 0 && !(col && o.rows % 8);
+    };
+    return fits(g.a, g.a_col) && fits(g.b, g.b_col);
+}
+
 // one type each (layer_mm_*.hip)
 gs_status launch_layer_mm_f32(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_f16(gs_ctx* ctx, const LayerMm& g);

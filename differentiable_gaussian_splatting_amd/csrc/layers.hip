@@ -129,9 +129,9 @@ gs_status launch_sum_rows(gs_ctx* ctx, int type, const SumJob& g)
 
 // What n tiles on each compute unit take for one step of k: once us for
 // every round of `resident` blocks and each us for every tile (measured, with
-// one to eight tiles a unit: 128 x 128 x 64 takes 1.0, 1.45 and 2.25 us for
-// one, two and three, 64 x 64 x 64 0.72, 1.2 and 2.2 for two, four and eight,
-// 256 x 256 x 64 2.4 for one).
+// one to eight tiles a unit: 128 x 128 x 64 through registers 1.0, 1.45 and 2.25
+// us for one, two and three, 64 x 64 x 64 0.72, 1.2 and 2.2 for two, four and
+// eight, 256 x 256 x 64 2.4 for one, loaded directly 2.15).
 struct TileCost {
     int32_t m, n, k, resident;
     double once, each;
@@ -141,8 +141,10 @@ constexpr TileCost cost(int resident, double once, double each)
 {
     return TileCost{T::BM, T::BN, T::BK, resident, once, each};
 }
-constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.1), cost<Medium16>(2, 0.3, 0.46), cost<Small16>(5, 0.2, 0.25),
+constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.3), cost<Medium16>(2, 0.5, 0.48), cost<Small16>(5, 0.2, 0.25),
                                 cost<Tiny16>(3, 0.3, 0.3)};
+constexpr TileCost kCostDirect[] = {cost<Large16>(1, 0.1, 2.1), cost<Medium16>(2, 0.3, 0.46), cost<Small16>(5, 0.2, 0.25),
+                                    cost<Tiny16>(3, 0.3, 0.3)};
 constexpr TileCost kCost32[] = {cost<Large32>(1, 0.1, 2.5), cost<Medium32>(2, 0.5, 1.35), cost<Small32>(3, 0.3, 0.48),
                                 cost<Tiny32>(3, 0.4, 0.5)};
 constexpr double kJoinUs = 4.0;          // a further launch
@@ -166,10 +168,11 @@ int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
     const int64_t n = g->e.n * (g->gated ? 2 : 1);
     const bool tiny = (!g->a_col && g->k < 8) || (g->a_col && g->m < 8) || (!g->b_col && g->k < 8) ||
                       (g->b_col && g->e.n < 8);
+    const TileCost* costs = f32 ? kCost32 : loads_direct(*g) ? kCostDirect : kCost16;
     double best = 0.0;
     int64_t best_s = 1;
     for (int t = tiny ? kTiny : kLarge; t <= (tiny ? kTiny : kSmall); ++t) {
-        const TileCost& c = f32 ? kCost32[t] : kCost16[t];
+        const TileCost& c = costs[t];
         const int64_t tiles = ceil_div(g->m, c.m) * ceil_div(n, c.n), steps = std::max<int64_t>(1, ceil_div(g->k, c.k));
         const int64_t slots = (int64_t)c.resident * ctx->num_cu;
         const double whole = cost_us(ctx, c, tiles, steps, 1);
@@ -189,7 +192,7 @@ int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
             g->full = full;
         }
     }
-    const TileCost& c = f32 ? kCost32[g->tile] : kCost16[g->tile];
+    const TileCost& c = costs[g->tile];
     g->tm = ceil_div(g->m, c.m);
     g->tn = ceil_div(n, c.n);
     g->kper = ceil_div(std::max<int64_t>(1, ceil_div(g->k, c.k)), best_s) * c.k;
@@ -323,7 +326,7 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         gw.m = n;
         gw.k = m;
         gw.a_col = gw.b_col = true;
-        gw.a = operand(dz, lddz, n);
+        gw.a = operand(dz, lddz, own ? lddz : n);   // own: the columns beside the last are there to be read
         gw.b = operand(x->data, x->stride, k);
         gw.e.n = k;
         gw.e.out = dw->data, gw.e.ldout = dw->stride, gw.e.out_type = (int8_t)dw->type;

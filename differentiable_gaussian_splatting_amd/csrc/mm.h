@@ -455,7 +455,16 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
             db.load(k, B.ld, lds.b[buf]);
             da.load(k, A.ld, lds.a[buf]);
         };
-        if (whole > k0) next(k0);
+        // A last, partial step goes first, through registers, while the first
+        // whole one is on its way to the other buffer.
+        if (whole < k1) {
+            buf ^= 1;
+            if (whole > k0) next(k0);
+            buf ^= 1;
+            steps(std::true_type{}, whole, k1);
+        } else {
+            next(k0);
+        }
         for (int64_t k = k0; k < whole; k += BK) {
             done();
             __syncthreads();
@@ -474,10 +483,10 @@ __device__ __forceinline__ void mm_tile(const Operand& A, const Operand& B, int6
         }
     } else {
         if (whole > k0) steps(std::false_type{}, k0, whole);
-    }
-    if (whole < k1) {
-        if (whole > k0) __syncthreads();
-        steps(std::true_type{}, whole, k1);
+        if (whole < k1) {
+            if (whole > k0) __syncthreads();
+            steps(std::true_type{}, whole, k1);
+        }
     }
 }
 
@@ -489,6 +498,18 @@ __device__ __forceinline__ void tile_at(int64_t t, int64_t tm, int64_t tn, int64
     const int64_t g = t / (G * tn), rows = min(G, tm - g * G), in = t - g * G * tn;
     i = g * G + in % rows;
     j = in / rows;
+}
+
+// Where tile i of `size` rows starts among `rows`: the last one is moved back
+// until it ends with them, as long as there are enough, and then writes its
+// rows from `own` on only.  So edges are left to operands smaller than a tile.
+struct Span {
+    int64_t at, own;
+};
+__device__ __forceinline__ Span span_of(int64_t i, int64_t size, int64_t rows)
+{
+    const int64_t own = i * size;
+    return Span{max((int64_t)0, min(own, rows - size)), own};
 }
 
 // Block b of n as a place in the order of tiles: neighbouring blocks go to
