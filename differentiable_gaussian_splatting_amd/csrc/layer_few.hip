@@ -15,6 +15,8 @@
 // gated: 34 us (5.3 TB/s).  Sixteen waves a block take 9.6 us for the former;
 // without the barrier before the products the compiler keeps two loads under
 // way and the latter takes 40.
+#include <algorithm>
+
 #include "layer_mm.h"
 
 namespace gsm {
@@ -23,29 +25,6 @@ namespace {
 
 constexpr int kWaves = 8;
 
-// 16 x 16 results from 8 values of k per lane, or 4 f32
-__device__ __forceinline__ f32x4 step(gst::Pack<float, 4> a, gst::Pack<float, 4> b, f32x4 c)
-{
-#pragma unroll
-    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
-    return c;
-}
-template <typename E>
-__device__ __forceinline__ f32x4 step(gst::Pack<E, 8> a, gst::Pack<E, 8> b, f32x4 c)
-{
-    return mfma(a, b, c);
-}
-
-// N values from p on, zeros from the n-th one on (n may be negative)
-template <typename S, int N>
-__device__ __forceinline__ gst::Pack<S, N> upto(const S* p, int64_t n)
-{
-    gst::Pack<S, N> v;
-#pragma unroll
-    for (int j = 0; j < N; ++j) v.v[j] = j < n ? p[j] : (S)0.0f;
-    return v;
-}
-
 template <typename S, bool GATED, int MI>
 __global__ __launch_bounds__(kWaves * 64) void k_few(const LayerMm g)
 {
@@ -53,8 +32,6 @@ __global__ __launch_bounds__(kWaves * 64) void k_few(const LayerMm g)
     constexpr int kUnroll = GATED || MI > 2 ? 4 : 8;
     __shared__ f32x4 part[kWaves][G][MI][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
-    const int64_t row = min(n0 + (lane & 15), g.e.n - 1);
     // ranges of whole pieces of kUnroll steps
     const int64_t piece = kStep * kUnroll, pieces = (g.k + piece - 1) / piece;
     const int64_t k0 = pieces * wave / kWaves * piece, k1 = min(pieces * (wave + 1) / kWaves * piece, g.k);
@@ -62,67 +39,70 @@ __global__ __launch_bounds__(kWaves * 64) void k_few(const LayerMm g)
 #pragma unroll
     for (int j = 0; j < MI; ++j)
         x[j] = (const S*)g.a.p + min((int64_t)(j * 16 + (lane & 15)), g.m - 1) * g.a.ld + (lane >> 4) * N;
-    const S* w = (const S*)g.b.p + row * g.b.ld + (lane >> 4) * N;
     const int64_t up = GATED ? g.e.n * g.b.ld : 0;
-    f32x4 acc[G][MI];
+    for (int64_t n0 = (int64_t)blockIdx.x * 16; n0 < g.e.n; n0 += (int64_t)gridDim.x * 16) {
+        const S* w = (const S*)g.b.p + min(n0 + (lane & 15), g.e.n - 1) * g.b.ld + (lane >> 4) * N;
+        f32x4 acc[G][MI];
 #pragma unroll
-    for (int q = 0; q < G; ++q)
+        for (int q = 0; q < G; ++q)
 #pragma unroll
-        for (int j = 0; j < MI; ++j) acc[q][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    int64_t k = k0;
-    for (; k + piece <= k1; k += piece) {
-        gst::Pack<S, N> a[MI][kUnroll], b[G][kUnroll];
+            for (int j = 0; j < MI; ++j) acc[q][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        int64_t k = k0;
+        for (; k + piece <= k1; k += piece) {
+            gst::Pack<S, N> a[MI][kUnroll], b[G][kUnroll];
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+            for (int i = 0; i < kUnroll; ++i)
 #pragma unroll
-            for (int q = 0; q < G; ++q) b[q][i] = gst::load<S, N>(w + q * up + k + i * kStep);
+                for (int q = 0; q < G; ++q) b[q][i] = gst::load<S, N>(w + q * up + k + i * kStep);
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+            for (int i = 0; i < kUnroll; ++i)
 #pragma unroll
-            for (int j = 0; j < MI; ++j) a[j][i] = gst::load<S, N>(x[j] + k + i * kStep);
-        __builtin_amdgcn_sched_barrier(0);   // all loads under way before the first is waited for
+                for (int j = 0; j < MI; ++j) a[j][i] = gst::load<S, N>(x[j] + k + i * kStep);
+            __builtin_amdgcn_sched_barrier(0);   // all loads under way before the first is waited for
 #pragma unroll
-        for (int i = 0; i < kUnroll; ++i)
+            for (int i = 0; i < kUnroll; ++i)
 #pragma unroll
-            for (int q = 0; q < G; ++q)
+                for (int q = 0; q < G; ++q)
 #pragma unroll
-                for (int j = 0; j < MI; ++j) acc[q][j] = step(b[q][i], a[j][i], acc[q][j]);
-    }
-    for (; k < k1; k += kStep) {
-        const int64_t left = k1 - k - (lane >> 4) * N;
-        gst::Pack<S, N> b[G];
-#pragma unroll
-        for (int q = 0; q < G; ++q) b[q] = upto<S, N>(w + q * up + k, left);
-#pragma unroll
-        for (int j = 0; j < MI; ++j) {
-            const gst::Pack<S, N> a = upto<S, N>(x[j] + k, left);
-#pragma unroll
-            for (int q = 0; q < G; ++q) acc[q][j] = step(b[q], a, acc[q][j]);
+                    for (int j = 0; j < MI; ++j) acc[q][j] = mfma16(b[q][i], a[j][i], acc[q][j]);
         }
+        for (; k < k1; k += kStep) {
+            const int64_t left = k1 - k - (lane >> 4) * N;
+            gst::Pack<S, N> b[G];
+#pragma unroll
+            for (int q = 0; q < G; ++q) b[q] = upto<S, N>(w + q * up + k, left);
+#pragma unroll
+            for (int j = 0; j < MI; ++j) {
+                const gst::Pack<S, N> a = upto<S, N>(x[j] + k, left);
+#pragma unroll
+                for (int q = 0; q < G; ++q) acc[q][j] = mfma16(b[q], a, acc[q][j]);
+            }
+        }
+#pragma unroll
+        for (int q = 0; q < G; ++q)
+#pragma unroll
+            for (int j = 0; j < MI; ++j) part[wave][q][j][lane] = acc[q][j];
+        __syncthreads();
+        // wave j adds the results of rows 16 j to 16 j + 15
+        const int64_t n = n0 + (lane >> 4) * 4, m = wave * 16 + (lane & 15);
+        if (wave < MI && m < g.m && n < g.e.n) {
+            f32x4 sum[G];
+#pragma unroll
+            for (int q = 0; q < G; ++q) {
+                sum[q] = part[0][q][wave][lane];
+                for (int v = 1; v < kWaves; ++v) sum[q] += part[v][q][wave][lane];
+            }
+            if constexpr (GATED) epilogue_gated<S>(g.e, m, n, sum[0], sum[1]);
+            else epilogue<S>(g.e, m, n, sum[0]);
+        }
+        __syncthreads();   // part is free again
     }
-#pragma unroll
-    for (int q = 0; q < G; ++q)
-#pragma unroll
-        for (int j = 0; j < MI; ++j) part[wave][q][j][lane] = acc[q][j];
-    __syncthreads();
-    // wave j adds the results of rows 16 j to 16 j + 15
-    if (wave >= MI) return;
-    f32x4 sum[G];
-#pragma unroll
-    for (int q = 0; q < G; ++q) {
-        sum[q] = part[0][q][wave][lane];
-        for (int v = 1; v < kWaves; ++v) sum[q] += part[v][q][wave][lane];
-    }
-    const int64_t n = n0 + (lane >> 4) * 4, m = wave * 16 + (lane & 15);
-    if (m >= g.m || n >= g.e.n) return;
-    if constexpr (GATED) epilogue_gated<S>(g.e, m, n, sum[0], sum[1]);
-    else epilogue<S>(g.e, m, n, sum[0]);
 }
 
 template <typename S, int MI>
 void launch_few(gs_ctx* ctx, const LayerMm& g)
 {
-    const dim3 grid((uint32_t)ceil_div(g.e.n, 16)), block(kWaves * 64);
+    const dim3 grid((uint32_t)std::min<int64_t>(ceil_div(g.e.n, 16), 1 << 20)), block(kWaves * 64);
     if (g.gated) hipLaunchKernelGGL((k_few<S, true, MI>), grid, block, 0, ctx->stream, g);
     else hipLaunchKernelGGL((k_few<S, false, MI>), grid, block, 0, ctx->stream, g);
 }

@@ -74,6 +74,30 @@ __device__ __forceinline__ void store4(void* p, int64_t at, int type, int valid,
     }
 }
 
+// 16 x 16 results from 16 bytes of k per lane
+__device__ __forceinline__ f32x4 mfma16(gst::Pack<float, 4> a, gst::Pack<float, 4> b, f32x4 c)
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a.v[j], b.v[j], c, 0, 0, 0);
+    return c;
+}
+template <typename E>
+__device__ __forceinline__ f32x4 mfma16(gst::Pack<E, 8> a, gst::Pack<E, 8> b, f32x4 c)
+{
+    return mfma(a, b, c);
+}
+
+// N values from p on, zeros from the n-th one on (n may be negative)
+template <typename S, int N>
+__device__ __forceinline__ gst::Pack<S, N> upto(const S* p, int64_t n)
+{
+    if (n >= N) return gst::load<S, N>(p);
+    gst::Pack<S, N> v;
+#pragma unroll
+    for (int j = 0; j < N; ++j) v.v[j] = j < n ? p[j] : (S)0.0f;
+    return v;
+}
+
 // columns n + first .. n + 3 of row m of the product
 template <typename S>
 __device__ __forceinline__ void epilogue(const Epilogue& e, int64_t m, int64_t n, f32x4 z, int first = 0)

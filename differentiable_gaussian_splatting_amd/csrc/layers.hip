@@ -93,26 +93,31 @@ __global__ __launch_bounds__(256) void k_sum_rows(const SumJob g)
 {
     __shared__ float part[4][64];
     const int x = threadIdx.x & 63, q = threadIdx.x >> 6;
-    const int64_t n = g.f * g.k + g.f, c = (int64_t)blockIdx.x * 64 + x;
-    const bool weight = c < g.f * g.k, wanted = c < n && (weight ? g.dw : g.dbias);
-    float s = 0.0f;
-    if (wanted) {
+    const int64_t n = g.f * g.k + g.f;
+    for (int64_t c0 = (int64_t)blockIdx.x * 64; c0 < n; c0 += (int64_t)gridDim.x * 64) {
+        const int64_t c = c0 + x;
+        const bool weight = c < g.f * g.k, wanted = c < n && (weight ? g.dw : g.dbias);
+        float s = 0.0f;
+        if (wanted) {
 #pragma unroll 8
-        for (int64_t b = q; b < g.blocks; b += 4) s += g.sums[b * n + c];
-    }
-    part[q][x] = s;
-    __syncthreads();
-    if (q || !wanted) return;
-    s = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
-    const int type = weight ? g.dw_type : g.dbias_type;
-    const int64_t at = weight ? c / g.k * g.lddw + c % g.k : c - g.f * g.k;
-    void* out = weight ? g.dw : g.dbias;
-    if (type == GS_F32) {
-        float* o = (float*)out + at;
-        *o = g.accumulate ? *o + s : s;
-    } else {
-        S* o = (S*)out + at;
-        *o = gst::narrow<S>(g.accumulate ? (float)*o + s : s);
+            for (int64_t b = q; b < g.blocks; b += 4) s += g.sums[b * n + c];
+        }
+        part[q][x] = s;
+        __syncthreads();
+        if (q == 0 && wanted) {
+            s = (part[0][x] + part[1][x]) + (part[2][x] + part[3][x]);
+            const int type = weight ? g.dw_type : g.dbias_type;
+            const int64_t at = weight ? c / g.k * g.lddw + c % g.k : c - g.f * g.k;
+            void* out = weight ? g.dw : g.dbias;
+            if (type == GS_F32) {
+                float* o = (float*)out + at;
+                *o = g.accumulate ? *o + s : s;
+            } else {
+                S* o = (S*)out + at;
+                *o = gst::narrow<S>(g.accumulate ? (float)*o + s : s);
+            }
+        }
+        __syncthreads();
     }
 }
 
@@ -120,8 +125,8 @@ gs_status launch_sum_rows(gs_ctx* ctx, int type, const SumJob& g)
 {
     GsTimerScope ts(ctx, "layer_sum");
     gst::with_type(type, [&](auto s) {
-        hipLaunchKernelGGL((k_sum_rows<decltype(s)>), dim3((uint32_t)ceil_div(g.f * g.k + g.f, 64)), dim3(256), 0,
-                           ctx->stream, g);
+        hipLaunchKernelGGL((k_sum_rows<decltype(s)>), dim3((uint32_t)std::min<int64_t>(ceil_div(g.f * g.k + g.f, 64), 1 << 20)),
+                           dim3(256), 0, ctx->stream, g);
     });
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;

@@ -500,9 +500,10 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
  *
  * Types: x, w, pre and dx have one type T of GS_F32, GS_F16 and GS_BF16;
  * out, residual, bias, dout, dw and dbias are T or GS_F32 each.  Sums are f32;
- * every output is rounded once.  f32 values are multiplied as three bf16 parts
- * each (six products; what is left out of x y is below 2^-22 |x y|); an f32
- * value of x or w (or dz) that is not finite makes its results NaN. */
+ * every output is rounded once.  f32 values are multiplied exactly or as three
+ * bf16 parts each (six products; what is left out of x y is below 2^-22 |x y|);
+ * with parts, an f32 value of x, w or dz that is infinite, or above bf16's
+ * largest, makes its results NaN. */
 enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3, GS_ACT_SIGMOID = 4 };
 
 /* out = act(z) + residual, z = x w^T + bias, with

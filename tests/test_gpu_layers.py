@@ -336,6 +336,51 @@ def test_offsets_past_32_bits(ctx):
     assert not dx[:-2].any()
 
 
+def test_more_columns_than_a_grid_has_threads_for(ctx):
+    """One row into 2^28 + 5 columns, and the bias gradient of 2^30 + 70."""
+    torch = _t()
+    f = (1 << 28) + 5
+    w = torch.ones((f, 1), dtype=torch.bfloat16, device="cuda")
+    w[-1], w[-7], w[1 << 20] = 3.0, -2.0, 0.5
+    x = torch.full((1, 1), 4.0, dtype=torch.bfloat16, device="cuda")
+    out = B.gs_linear_fwd(ctx, x, w)
+    assert torch.equal(out.view(-1), w.view(-1) * 4)
+    del w, out
+    f = (1 << 30) + 70
+    w = torch.empty((f, 0), dtype=torch.bfloat16, device="cuda")
+    d = torch.ones((1, f), dtype=torch.bfloat16, device="cuda")
+    d[0, -1], d[0, 5] = 3.0, -1.0
+    db = torch.zeros(f, dtype=torch.bfloat16, device="cuda")
+    B.gs_linear_bwd(ctx, x[:, :0], w, d, dbias=db)
+    assert torch.equal(db, d.view(-1))
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+def test_tiles_that_end_with_their_operands(ctx, name):
+    """Last tiles moved back: every output is written once (a residual in place would be added twice), also where some
+    tiles are split over k and some are not, at every kind of alignment."""
+    torch = _t()
+    t = dtype(name)
+    for n, k, f in ((129, 200, 130), (257, 72, 264), (700, 1000, 513), (321, 64, 2056), (1000, 520, 1001)):
+        x, w = torch.randn((n, k), device="cuda").to(t), (torch.randn((f, k), device="cuda") * k ** -0.5).to(t)
+        r = torch.randn((n, f), device="cuda")
+        want = r.double() + x.double() @ w.double().T
+        X, W = x.double(), w.double()
+        B.gs_linear_fwd(ctx, x, w, residual=r, out=r)
+        e = product_bound(name, k, X, W)
+        close(r, want, e + 3 * u * (want.abs() + e))
+        d = torch.randn((n, f), device="cuda").to(t)
+        dw = torch.randn((f, k), device="cuda")
+        want = dw.double() + d.double().T @ X
+        B.gs_linear_bwd(ctx, x, w, d, dw=dw, accumulate=True)
+        e = product_bound(name, n, d.double().T, X.T)
+        close(dw, want, e + 3 * u * (want.abs() + e))
+        # rows further apart than they are long, from an address that is not a multiple of 16
+        check_fwd(ctx, n, k, f, name, "silu", 8, 0, bias="f32", pre=True)
+        check_fwd(ctx, n, k, f, name, "relu", 3, 1, pre=True, gated=True)
+        check_bwd(ctx, n, k, f, name, "gelu", 8, 0, bias="f32")
+
+
 @pytest.mark.parametrize("act", ACTS[2:])
 def test_gradients_are_those_of_the_layers(ctx, act):
     """Derivatives along random directions against differences of the forward pass, linear then gated then linear,
