@@ -137,18 +137,21 @@ __device__ __forceinline__ void wave_fence()
 
 // Tiles of the product (DIRECT: see mm_tile); those from `full` on in `splits` ranges of k, whose sums
 // k_join adds up.
+template <typename S, int P, typename T>
+union LayerLds {
+    Lds<S, P, T> tile;
+    float out[T::NT / 64 * 32 * (T::NI * 16 + 4)];
+};
+
+// block `block` of `blocks` that form the product
 template <typename S, int P, bool ACOL, bool BCOL, bool GATED, typename T, bool DIRECT>
-__global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
+__device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_t blocks, LayerLds<S, P, T>& lds)
 {
     constexpr int kCols = T::NI * (GATED ? 8 : 16), kRow = T::NI * 16 + 4;   // of a wave's results; padded row in LDS
-    __shared__ union {
-        Lds<S, P, T> tile;
-        float out[T::NT / 64 * 32 * kRow];
-    } lds;
     constexpr int G = GATED ? 2 : 1;
     const int64_t rest = g.tm * g.tn - g.full, total = g.full + rest * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    for (int64_t b = blockIdx.x; b < total; b += gridDim.x) {
+    for (int64_t b = block; b < total; b += blocks) {
         int64_t tile = b, k0 = 0, k1 = g.k, i, j;
         float* ws = nullptr;
         if (b < g.full) {
@@ -168,7 +171,7 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
         for (int q = 0; q < T::NI; ++q)
 #pragma unroll
             for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-        if (b != (int64_t)blockIdx.x) __syncthreads();   // the previous tile's reads of lds
+        if (b != block) __syncthreads();   // the previous tile's reads of lds
         mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(g.a, g.b, m0, n0, k0, k1, lds.tile, acc);
         // The results go through LDS, 32 rows of each wave at a time, so that a
         // lane takes four columns next to its neighbours' (whole lines are
@@ -208,6 +211,22 @@ __global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
     }
 }
 
+template <typename S, int P, bool ACOL, bool BCOL, bool GATED, typename T, bool DIRECT>
+__global__ __launch_bounds__(T::NT, 2) void k_layer_mm(const LayerMm g)
+{
+    __shared__ LayerLds<S, P, T> lds;
+    layer_mm<S, P, ACOL, BCOL, GATED, T, DIRECT>(g, blockIdx.x, gridDim.x, lds);
+}
+
+// dx and dw of a small layer in one launch: the first `split` blocks form dx
+template <typename S, int P, typename T>
+__global__ __launch_bounds__(T::NT, 2) void k_layer_pair(const LayerMm x, const LayerMm w, int split)
+{
+    __shared__ LayerLds<S, P, T> lds;
+    if ((int)blockIdx.x < split) layer_mm<S, P, false, true, false, T, false>(x, blockIdx.x, split, lds);
+    else layer_mm<S, P, true, true, false, T, false>(w, blockIdx.x - split, gridDim.x - split, lds);
+}
+
 // Sums of the splits in their order, then the epilogue; four columns a thread.
 template <typename S, bool GATED, typename T>
 __global__ __launch_bounds__(256) void k_join(const LayerMm g)
@@ -237,20 +256,30 @@ __global__ __launch_bounds__(256) void k_join(const LayerMm g)
 
 constexpr int64_t kMaxGrid = 1 << 22;   // blocks of a launch; larger products loop
 
+inline int64_t layer_blocks(const LayerMm& g)
+{
+    return std::min(g.full + (g.tm * g.tn - g.full) * g.splits, kMaxGrid);
+}
+
+template <typename S, typename T>
+void launch_join(gs_ctx* ctx, const LayerMm& g)
+{
+    if (g.splits == 1) return;
+    const int64_t quads = (g.tm * g.tn - g.full) * T::BM * T::BN / (g.gated ? 8 : 4);
+    const dim3 grid((uint32_t)std::min(ceil_div(quads, 256), kMaxGrid));
+    if (g.gated) hipLaunchKernelGGL((k_join<S, true, T>), grid, dim3(256), 0, ctx->stream, g);
+    else hipLaunchKernelGGL((k_join<S, false, T>), grid, dim3(256), 0, ctx->stream, g);
+}
+
 template <typename S, int P, typename T, bool DIRECT>
 void launch_mode(gs_ctx* ctx, const LayerMm& g)
 {
-    const int64_t rest = g.tm * g.tn - g.full;
-    const dim3 grid((uint32_t)std::min(g.full + rest * g.splits, kMaxGrid)), block(T::NT);
+    const dim3 grid((uint32_t)layer_blocks(g)), block(T::NT);
     if (g.a_col) hipLaunchKernelGGL((k_layer_mm<S, P, true, true, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
     else if (g.b_col) hipLaunchKernelGGL((k_layer_mm<S, P, false, true, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
     else if (g.gated) hipLaunchKernelGGL((k_layer_mm<S, P, false, false, true, T, DIRECT>), grid, block, 0, ctx->stream, g);
     else hipLaunchKernelGGL((k_layer_mm<S, P, false, false, false, T, DIRECT>), grid, block, 0, ctx->stream, g);
-    if (g.splits == 1) return;
-    const int64_t quads = rest * T::BM * T::BN / (g.gated ? 8 : 4);
-    const dim3 join((uint32_t)std::min(ceil_div(quads, 256), kMaxGrid));
-    if (g.gated) hipLaunchKernelGGL((k_join<S, true, T>), join, dim3(256), 0, ctx->stream, g);
-    else hipLaunchKernelGGL((k_join<S, false, T>), join, dim3(256), 0, ctx->stream, g);
+    launch_join<S, T>(ctx, g);
 }
 
 template <typename S, int P, typename Large, typename Medium, typename Small, typename Tiny>
@@ -264,6 +293,20 @@ gs_status launch_layer_mm(gs_ctx* ctx, const LayerMm& g)
     else if (g.tile == kMedium) launch_mode<S, P, Medium, false>(ctx, g);
     else if (g.tile == kSmall) launch_mode<S, P, Small, false>(ctx, g);
     else launch_mode<S, P, Tiny, false>(ctx, g);
+    GS_HIP(ctx, hipGetLastError());
+    return GS_OK;
+}
+
+// dx and dw, both of small tiles
+template <typename S, int P, typename Small>
+gs_status launch_layer_pair(gs_ctx* ctx, const LayerMm& x, const LayerMm& w)
+{
+    GsTimerScope ts(ctx, "layer_mm");
+    const int64_t split = layer_blocks(x);
+    hipLaunchKernelGGL((k_layer_pair<S, P, Small>), dim3((uint32_t)(split + layer_blocks(w))), dim3(Small::NT), 0, ctx->stream,
+                       x, w, (int)split);
+    launch_join<S, Small>(ctx, x);
+    launch_join<S, Small>(ctx, w);
     GS_HIP(ctx, hipGetLastError());
     return GS_OK;
 }

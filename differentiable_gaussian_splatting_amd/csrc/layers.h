@@ -97,6 +97,10 @@ inline bool loads_direct(const LayerMm& g)
 gs_status launch_layer_mm_f32(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_f16(gs_ctx* ctx, const LayerMm& g);
 gs_status launch_layer_mm_bf16(gs_ctx* ctx, const LayerMm& g);
+// dx and dw of kSmall tiles in one launch
+gs_status launch_layer_pair_f32(gs_ctx* ctx, const LayerMm& x, const LayerMm& w);
+gs_status launch_layer_pair_f16(gs_ctx* ctx, const LayerMm& x, const LayerMm& w);
+gs_status launch_layer_pair_bf16(gs_ctx* ctx, const LayerMm& x, const LayerMm& w);
 // x w^T of few rows (layer_few.hip)
 bool few_rows(const LayerMm& g);
 gs_status launch_layer_few(gs_ctx* ctx, int type, const LayerMm& g);

@@ -578,9 +578,9 @@ class Net:
         B.gs_gated_fwd(c, self.h1, self.w[1], act="gelu", pre=self.p2, out=self.h2)
         B.gs_linear_fwd(c, self.h2, self.w[2], bias=self.b[1], out=self.y)
 
-    def step(self, c, k=1):
+    def step(self, c, k=1, dy=None):
         self.forward(c)
-        dy = (self.y - self.target) / self.y.numel()
+        dy = (self.y - self.target) / self.y.numel() if dy is None else dy
         B.gs_linear_bwd(c, self.h2, self.w[2], dy, dx=self.dh2, dw=self.dw[2], dbias=self.db[1])
         B.gs_gated_bwd(c, self.h1, self.w[1], self.p2, self.dh2, act="gelu", dx=self.dh1, dw=self.dw[1])
         B.gs_linear_bwd(c, self.x, self.w[0], self.dh1, pre=self.p1, act="silu", dx=self.dx, dw=self.dw[0],
@@ -611,6 +611,31 @@ def test_a_network_trains_and_agrees_with_autograd(ctx):
     for k in range(2, 5):
         net.step(ctx, k)
     assert all(t.isfinite().all() for t in net.state())
+
+
+def test_a_scene_whose_colours_come_from_a_network(ctx):
+    """Lookup, linear, gated and linear layers make a view's SH rows; the view's gradient rows go back through them
+    as they lie (columns of wider rows), and every update runs."""
+    torch = _t()
+    from differentiable_gaussian_splatting_amd import scenes
+    w = scenes.make_workload("c3_gmm4k", n=700, width=96, height=64, seed=3)
+    ds = B.DeviceScene(w.scene, "cuda")
+    assert ds.sh.numel() == 700 * 48
+    target = torch.from_numpy(w.target).cuda()
+    net = Net(n=700, seed=4)
+    net.forward(ctx)
+    ds.sh.view(700, 48).copy_(0.2 * net.y)
+    rows = torch.zeros((700, 59), device="cuda")
+    B.gs_train_view(ctx, w.camera, ds, target, grad3d_out=rows)
+    assert rows[:, 11:].any()
+    keep = net.y.clone()
+    net.step(ctx, dy=rows[:, 11:])
+    assert torch.equal(net.y, keep)
+    d = rows[:, 11:].double()
+    want = d.T @ net.h2.double()
+    e = 2 * (700 + 2) * u * (d.abs().T @ net.h2.double().abs())
+    close(net.dw[2], want, e + u * (want.abs() + e) + 1e-37)
+    assert all(t.isfinite().all() for t in net.state()) and net.m[0].any()
 
 
 def test_results_repeat_and_streams(ctx):
