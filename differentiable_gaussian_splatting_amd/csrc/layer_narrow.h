@@ -14,6 +14,10 @@
 //             up in the block, and the blocks' by a second launch, in order.
 // f32 uses the f32 matrix instruction (exact products; at these widths its rate
 // is above what memory feeds it).
+//
+// 1M rows, f32: 32 -> 48 forward 86 us (3.7 TB/s), 32 -> 64 relu backward 166
+// (4.6 TB/s; 670 with dz in memory and tiles); 64 -> 64 forward 170, where the
+// f32 products take 52 and hide only in part.
 #pragma once
 
 #include "layer_mm.h"

@@ -1,11 +1,14 @@
-// layers.hip -- linear and gated layers: how their matrix products are cut
-// into tiles and splits, and the gradient of the activation with the bias
-// gradient's column sums.
+// layers.hip -- linear and gated layers: which kernel a call takes, how its
+// matrix products are cut into tiles and splits, and the gradient of the
+// activation with the bias gradient's column sums.
 //
 //   linear: out = act(x w^T + bias) + residual
 //           dz = dout act'(pre), dx = dz w, dw = dz^T x, dbias = sum over rows of dz
 //   gated:  [g u] = x w^T, out = act(g) u
 //           dg = dout u act'(g), du = dout act(g), then as above
+//
+// Forward: few rows (layer_few.hip), narrow rows (layer_narrow.h), else tiles
+// (layer_mm.h).  Backward: narrow rows in one pass, else dz, then two products.
 #include <algorithm>
 
 #include "layer_narrow.h"
