@@ -244,6 +244,55 @@ def test_sizes_around_the_tiles(ctx, n, k, f):
         check_fwd(ctx, n, k, f, name, "gelu", gated=True)
 
 
+@pytest.mark.parametrize("n", [1, 20, 64, 65])
+def test_few_rows_accumulate(ctx, n):
+    for name in ("f32", "bf16"):
+        check_bwd(ctx, n, 300, 333, name, "silu", bias="f32", accumulate=True, dw="f32")
+        check_bwd(ctx, n, 300, 333, name, "none", bias=name, accumulate=True)
+        check_bwd(ctx, n, 40, 24, name, "gelu", bias=name, accumulate=True)
+
+
+@pytest.mark.parametrize("name", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("n,k,f", [(3, 70, 40), (40, 130, 72), (300, 260, 300), (129, 200, 136), (1000, 64, 48), (700, 7, 5),
+                                   (2100, 72, 2056)])
+def test_nothing_around_the_operands_is_read(ctx, n, k, f, name):
+    """Views into buffers of NaN: gaps between rows (aligned ones and others), before the first and behind the last."""
+    torch = _t()
+
+    def view(rows, cols, gap, lead):
+        ld = cols + gap
+        buf = torch.full((lead + rows * ld + 64,), float("nan"), device="cuda").to(dtype(name))
+        v = buf.as_strided((rows, cols), (ld, 1), lead)
+        v.copy_(torch.randn((rows, cols), device="cuda"))
+        return v
+
+    for gap, lead in ((8 - k % 8, 8), (3, 1)):
+        x, w, d, z = view(n, k, gap, lead), view(f, k, gap, lead), view(n, f, 8, lead), view(n, f, 8, lead)
+        b, out = torch.zeros(f, device="cuda"), torch.empty((n, f), device="cuda")
+        dx, dw, db = torch.empty_like(x), torch.empty((f, k), device="cuda"), torch.empty(f, device="cuda")
+        X, W, D = x.double(), w.double(), d.double()
+        B.gs_linear_fwd(ctx, x, w, bias=b, out=out)
+        e = product_bound(name, k, X, W)
+        close(out, X @ W.T, e + 2 * u * ((X @ W.T).abs() + e))
+        for act in ("none", "relu"):
+            B.gs_linear_bwd(ctx, x, w, d, pre=z, act=act, dx=dx, dw=dw, dbias=db)
+            dz = D if act == "none" else D * (z > 0)   # exact in every type
+            e = product_bound(name, n, dz.T, X.T)
+            close(dw, dz.T @ X, e + 2 * u * ((dz.T @ X).abs() + e))
+            e = product_bound(name, f, dz, W.T)
+            T, tiny = unit(name)
+            close(dx, dz @ W, e + T * ((dz @ W).abs() + e) + tiny)
+            close(db, dz.sum(0), (n + 2) * u * dz.abs().sum(0) + 1e-37)
+        if f % 2 == 0:
+            y = torch.empty((n, f // 2), device="cuda")
+            B.gs_gated_fwd(ctx, x, w, act="none", out=y)
+            Z, ez = X @ W.T, product_bound(name, k, X, W)
+            g, q = Z[:, :f // 2], Z[:, f // 2:]
+            eg, eq = ez[:, :f // 2], ez[:, f // 2:]
+            bound = eg * q.abs() + eq * g.abs() + eg * eq
+            close(y, g * q, bound + 2 * u * ((g * q).abs() + bound))
+
+
 def test_layers_of_nothing(ctx):
     torch = _t()
     x, w = torch.randn((5, 4), device="cuda"), torch.randn((6, 4), device="cuda")
@@ -509,6 +558,30 @@ def test_muon_lists(ctx):
     check_muon(ctx, mixed, copy="bf16")
     check_muon(ctx, [(8 + k % 5, 6 + k % 7) for k in range(95)], name="f16")
     check_muon(ctx, [])
+
+
+def test_muon_of_large_matrices(ctx):
+    """Every tile, products split over the long side, more matrices than a launch takes, both orientations."""
+    check_muon(ctx, [(1100, 900), (513, 2000)], copy="bf16")
+    check_muon(ctx, [(2300, 70), (64, 5000)], name="bf16")
+    check_muon(ctx, [(150, 140 + k % 3) for k in range(43)] + [(130 + k % 2, 190) for k in range(41)], steps=3)
+    check_muon(ctx, [(2048, 1536)], steps=2)
+    check_muon(ctx, [(3, 1000), (1000, 3), (1, 4000)])
+
+
+def test_muon_in_more_than_one_group(ctx):
+    """2.01e8 values: two groups, one after the other in the same workspace."""
+    torch = _t()
+    n = 8192
+    p = [torch.zeros((n, n), device="cuda") for _ in range(3)]
+    m = [torch.zeros((n, n), device="cuda") for _ in range(3)]
+    g = [torch.randn((n, n), device="cuda") for _ in range(3)]
+    B.gs_muon_tensors(ctx, p, m, g, lr=-1.0, steps=2, momentum=0.0)
+    for k in (0, 2):
+        X, e = newton_schulz(g[k].double(), 2, 2 * u)
+        assert torch.equal(m[k], g[k])
+        assert float((p[k].double() - X).norm()) <= e + 4 * u * float(X.norm())
+        del X
 
 
 def test_muon_of_zero_and_tiny_gradients(ctx):
