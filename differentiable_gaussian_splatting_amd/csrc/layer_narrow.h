@@ -5,7 +5,8 @@
 // A wave takes 16 rows at a time (32 in the 16-bit backward pass) straight from
 // memory in the layout of the matrix instruction (lane: row l % 16, 16 bytes of
 // it at k = 16 bytes x (l / 16)), with the next rows on their way meanwhile.
-//   forward:  out = act(x w^T + bias) + residual, one read of x, one write of out.
+//   forward:  out = act(x w^T + bias) + residual, or act(g) u with both halves of
+//             w in registers; one read of x, one write of out.
 //   backward: dz is formed from dout and pre as they are read; it is an operand
 //             of dx = dz w as it stands, and passes through a piece of LDS of the
 //             wave's own, as x does, to be read down its columns for dw = dz^T x
@@ -39,23 +40,26 @@ __device__ __forceinline__ void load_f32(const void* p, int64_t at, int type, in
 
 constexpr int kNarrowThreads = 256;
 
-template <typename S, int KS, int NI>
+template <typename S, int KS, int NI, bool GATED>
 __global__ __launch_bounds__(kNarrowThreads) void k_narrow_fwd(const LayerMm g)
 {
     constexpr int N = 16 / sizeof(S), kStep = 4 * N, kCols = NI * 16, kRow = kCols + 4;
     // A 16-bit result of four columns is 8 bytes: those go through LDS, so that
     // neighbouring lanes write neighbouring columns (64 -> 64 bf16, 1M rows: 123 -> 65 us).
-    constexpr bool kTurn = sizeof(S) == 2;
+    constexpr bool kTurn = sizeof(S) == 2 && !GATED;
+    constexpr int G = GATED ? 2 : 1;
     __shared__ __align__(16) float lds[kTurn ? kNarrowThreads / 64 : 1][kTurn ? 16 * kRow : 4];
     const int lane = threadIdx.x & 63, k0 = (lane >> 4) * N;
     float* const mine = lds[kTurn ? threadIdx.x >> 6 : 0];
-    gst::Pack<S, N> b[NI][KS];
+    gst::Pack<S, N> b[G][NI][KS];
 #pragma unroll
-    for (int i = 0; i < NI; ++i) {
-        const S* w = (const S*)g.b.p + min((int64_t)(i * 16 + (lane & 15)), g.e.n - 1) * g.b.ld;
+    for (int q = 0; q < G; ++q)
 #pragma unroll
-        for (int s = 0; s < KS; ++s) b[i][s] = upto<S, N>(w + s * kStep + k0, g.k - s * kStep - k0);
-    }
+        for (int i = 0; i < NI; ++i) {
+            const S* w = (const S*)g.b.p + (q * g.e.n + min((int64_t)(i * 16 + (lane & 15)), g.e.n - 1)) * g.b.ld;
+#pragma unroll
+            for (int s = 0; s < KS; ++s) b[q][i][s] = upto<S, N>(w + s * kStep + k0, g.k - s * kStep - k0);
+        }
     const int64_t groups = (g.m + 15) / 16, stride = (int64_t)gridDim.x * (kNarrowThreads / 64);
     int64_t at = (int64_t)blockIdx.x * (kNarrowThreads / 64) + (threadIdx.x >> 6);
     gst::Pack<S, N> a[KS], next[KS];
@@ -69,12 +73,18 @@ __global__ __launch_bounds__(kNarrowThreads) void k_narrow_fwd(const LayerMm g)
         if (at + stride < groups) load(at + stride, next);
 #pragma unroll
         for (int i = 0; i < NI; ++i) {
-            f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
+            f32x4 acc[G];
 #pragma unroll
-            for (int s = 0; s < KS; ++s) acc = mfma16(b[i][s], a[s], acc);
+            for (int q = 0; q < G; ++q) {
+                acc[q] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < KS; ++s) acc[q] = mfma16(b[q][i][s], a[s], acc[q]);
+            }
             const int row = lane & 15, c = i * 16 + (lane >> 4) * 4;
-            if constexpr (kTurn) *reinterpret_cast<f32x4*>(mine + row * kRow + c) = acc;
-            else if (at * 16 + row < g.m && c < g.e.n) epilogue<S>(g.e, at * 16 + row, c, acc);
+            const bool there = at * 16 + row < g.m && c < g.e.n;
+            if constexpr (kTurn) *reinterpret_cast<f32x4*>(mine + row * kRow + c) = acc[0];
+            else if constexpr (GATED) { if (there) epilogue_gated<S>(g.e, at * 16 + row, c, acc[0], acc[1]); }
+            else if (there) epilogue<S>(g.e, at * 16 + row, c, acc[0]);
         }
         if constexpr (kTurn) {
             wave_fence();
@@ -354,19 +364,25 @@ bool launch_narrow_bwd_f32(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
 bool launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
 bool launch_narrow_bwd_bf16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
 
+template <typename S, bool GATED>
+bool launch_narrow_rows(gs_ctx* ctx, const LayerMm& g)
+{
+    constexpr int kStep = 64 / sizeof(S);
+    return with_blocks<kNarrowFwd / (GATED ? 2 : 1)>(ceil_div(g.k, kStep), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
+        // waves that come back for more rows: 6 blocks a compute unit, and where
+        // w takes few registers 24 (32 -> 48 f32: 86 us, 106 with 6; 64 -> 64: 184, 170)
+        constexpr int kOps = decltype(ks)::value * decltype(ni)::value * (GATED ? 2 : 1);
+        const int64_t groups = ceil_div(g.m, 16 * (kNarrowThreads / 64)),
+                      most = (sizeof(S) == 2 || kOps > 8 ? 6 : 24) * ctx->num_cu;
+        hipLaunchKernelGGL((k_narrow_fwd<S, decltype(ks)::value, decltype(ni)::value, GATED>),
+                           dim3((uint32_t)std::min(groups, most)), dim3(kNarrowThreads), 0, ctx->stream, g);
+    });
+}
+
 template <typename S>
 bool launch_narrow_fwd(gs_ctx* ctx, const LayerMm& g)
 {
-    constexpr int kStep = 64 / sizeof(S);
-    return with_blocks<kNarrowFwd>(ceil_div(g.k, kStep), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
-        // waves that come back for more rows: 6 blocks a compute unit, and where
-        // w takes few registers 24 (32 -> 48 f32: 86 us, 106 with 6; 64 -> 64: 184, 170)
-        constexpr int kOps = decltype(ks)::value * decltype(ni)::value;
-        const int64_t groups = ceil_div(g.m, 16 * (kNarrowThreads / 64)),
-                      most = (sizeof(S) == 2 || kOps > 8 ? 6 : 24) * ctx->num_cu;
-        hipLaunchKernelGGL((k_narrow_fwd<S, decltype(ks)::value, decltype(ni)::value>),
-                           dim3((uint32_t)std::min(groups, most)), dim3(kNarrowThreads), 0, ctx->stream, g);
-    });
+    return g.gated ? launch_narrow_rows<S, true>(ctx, g) : launch_narrow_rows<S, false>(ctx, g);
 }
 
 template <typename S>

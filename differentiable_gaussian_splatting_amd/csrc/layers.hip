@@ -275,7 +275,7 @@ gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     g.e.out = out->data, g.e.ldout = out->stride, g.e.out_type = (int8_t)out->type;
     if (g.m == 0 || g.e.n == 0) return GS_OK;
     if (few_rows(g)) return launch_layer_few(ctx, x->type, g);
-    if (!gated && launch_narrow(ctx, x->type, g)) return check_launch(ctx);
+    if (launch_narrow(ctx, x->type, g)) return check_launch(ctx);
     const int64_t ws = plan(ctx, x->type == GS_F32, &g);
     if (ws && !(g.ws = (float*)gs_malloc(ctx, 4 * ws, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
     return launch_mm(ctx, x->type, g);
