@@ -42,7 +42,7 @@ __host__ __device__ constexpr int64_t padded(int64_t n, int64_t to) { return (n 
 
 constexpr int kThreads = 256;
 constexpr int kPiece = 4096;      // values of a block of the elementwise kernels
-constexpr int kGroup = 40;        // matrices of a launch (kernel arguments within 4 KB)
+constexpr int kGroup = 48;        // matrices of a launch (kernel arguments within 4 KB)
 
 // A matrix of a group.  Its X, G and P start at x, s and s in the group's
 // workspaces, with zeros around them up to whole tiles of the group (unit):
@@ -78,7 +78,7 @@ struct MmJob {
     Shape t[kGroup];
     int32_t count;
 };
-static_assert(sizeof(Job) <= 3840 && sizeof(MmJob) <= 3840, "kernel arguments");
+static_assert(sizeof(Job) <= 3904 && sizeof(MmJob) <= 3904, "kernel arguments");
 
 // the matrix that holds piece (tile) b, and the pieces before it
 template <typename J, typename F>

@@ -556,7 +556,7 @@ def test_muon_steps(ctx, steps):
 def test_muon_lists(ctx):
     mixed = [(64, 48), (0, 5), (48, 64), (7, 300), (300, 7), (5, 0), (200, 140), (1, 64), (64, 64)]
     check_muon(ctx, mixed, copy="bf16")
-    check_muon(ctx, [(8 + k % 5, 6 + k % 7) for k in range(95)], name="f16")
+    check_muon(ctx, [(8 + k % 5, 6 + k % 7) for k in range(105)], name="f16")
     check_muon(ctx, [])
 
 
@@ -564,7 +564,7 @@ def test_muon_of_large_matrices(ctx):
     """Every tile, products split over the long side, more matrices than a launch takes, both orientations."""
     check_muon(ctx, [(1100, 900), (513, 2000)], copy="bf16")
     check_muon(ctx, [(2300, 70), (64, 5000)], name="bf16")
-    check_muon(ctx, [(150, 140 + k % 3) for k in range(43)] + [(130 + k % 2, 190) for k in range(41)], steps=3)
+    check_muon(ctx, [(150, 140 + k % 3) for k in range(50)] + [(130 + k % 2, 190) for k in range(49)], steps=3)
     check_muon(ctx, [(2048, 1536)], steps=2)
     check_muon(ctx, [(3, 1000), (1000, 3), (1, 4000)])
 
