@@ -277,7 +277,7 @@ struct Stage {
 // start on 16 bytes: each lane's 16 bytes go straight to LDS, the wave's 64
 // chunks to 1 KB in lane order, so the lane fetches the chunk that belongs to
 // its place.  The compiler does not see these loads: done() waits for all of
-// them.  (With the builtin for this load it waits for them before the next LDS
+// them (M0, which holds their LDS address, is reserved: no value lives in it).  (With the builtin for this load it waits for them before the next LDS
 // read, whose buffer is another one, and the loads hide behind nothing: 256 x 256
 // tiles 900 TFLOP/s, 990 this way; 128 x 128 790 and 890; through registers 915
 // and 740.)
@@ -310,7 +310,7 @@ struct Direct {
             asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
                          :
                          : "s"(__builtin_amdgcn_readfirstlane(m0)), "v"(p + u * step)
-                         : "memory", "m0");
+                         : "memory");
         }
     }
 };
