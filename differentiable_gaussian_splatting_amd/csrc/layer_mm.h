@@ -109,6 +109,7 @@ template <typename S>
 __device__ __forceinline__ void epilogue(const Epilogue& e, int64_t m, int64_t n, f32x4 z, int first = 0)
 {
     const int valid = (int)min((int64_t)4, e.n - n);
+    if (e.down) z *= e.down[m * e.lddown];
     if (e.bias) z += load4<S>(e.bias, n, e.bias_type, valid, first);
     if (e.pre) store4<S>(e.pre, m * e.ldpre + n, e.pre_type, valid, z, first);
     if (e.act != GS_ACT_NONE) {
@@ -157,6 +158,8 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
     constexpr int G = GATED ? 2 : 1;
     const int64_t rest = g.tm * g.tn - g.full, total = g.full + rest * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    Operand ga = g.a;
+    if (g.other && *g.other) ga.p = g.a_other;
     for (int64_t b = block; b < total; b += blocks) {
         int64_t tile = b, k0 = 0, k1 = g.k, i, j;
         float* ws = nullptr;
@@ -178,7 +181,7 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
 #pragma unroll
             for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (b != block) __syncthreads();   // the previous tile's reads of lds
-        mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(g.a, g.b, m0, n0, k0, k1, lds.tile, acc);
+        mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(ga, g.b, m0, n0, k0, k1, lds.tile, acc);
         // The results go through LDS, 32 rows of each wave at a time, so that a
         // lane takes four columns next to its neighbours' (whole lines are
         // read and written) and the epilogue's code is a loop.

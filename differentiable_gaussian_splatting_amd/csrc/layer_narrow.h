@@ -189,6 +189,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBw
 {
     typedef NarrowSize<S, FI, KI> Z;
     constexpr int W = kNarrowThreads / 64, N = Z::N;
+    constexpr bool kScaled = std::is_same<S, gst::f16>::value;   // dz as in k_dz: by a row's scale for dx, by a wave's for dw
     // The next rows are on their way while these are worked on, where registers
     // for both leave two waves a SIMD (1M x 32 -> 64 f32: 167 us, 182 without;
     // 64 -> 64 f32: 425, 270 without; the 16-bit types lose at every width).
@@ -217,6 +218,7 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBw
     for (int f = 0; f < FI; ++f)
 #pragma unroll
         for (int k = 0; k < KI; ++k) dw[f][k] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    int scale = 126;   // f16: exponent by which dz is scaled in dw's sums
     float db[Z::FS][N];
 #pragma unroll
     for (int s = 0; s < Z::FS; ++s)
@@ -234,19 +236,56 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBw
         } else {
             now.load(g, row0, lane);
         }
-#pragma unroll
-        for (int h = 0; h < Z::kRows / 16; ++h) {
-            gst::Pack<S, N> dz[Z::FS];
+        // dz, in place of dout; f16: all of it before the first is rounded
+        float most[Z::kRows / 16];
+        auto form = [&](int h) {
+            most[h] = 0.0f;
 #pragma unroll
             for (int s = 0; s < Z::FS; ++s)
 #pragma unroll
                 for (int j = 0; j < N; ++j) {
-                    float v = now.d[h][s][j];
+                    float& v = now.d[h][s][j];
                     if (g.act != GS_ACT_NONE) v *= act_both((float)now.z[h][s].v[j], g.act).y;
                     // past the last value of a row, and past the last row, pre is 0 and dout too
                     db[s][j] += v;
-                    dz[s].v[j] = gst::narrow<S>(v);
+                    if constexpr (kScaled) most[h] = larger(most[h], v);
                 }
+        };
+        if constexpr (kScaled) {
+            // each row's largest, and the rows' together; sums so far follow when theirs is the largest yet
+            float all = 0.0f;
+#pragma unroll
+            for (int h = 0; h < Z::kRows / 16; ++h) {
+                form(h);
+                most[h] = fmaxf(most[h], __shfl_xor(most[h], 16));
+                most[h] = fmaxf(most[h], __shfl_xor(most[h], 32));
+                all = fmaxf(all, most[h]);
+            }
+#pragma unroll
+            for (int d = 1; d < 16; d <<= 1) all = fmaxf(all, __shfl_xor(all, d));
+            const int e = __builtin_amdgcn_readfirstlane(all > 0.0f ? scale_exponent(all) : 126);
+            if (e < scale) {
+#pragma unroll
+                for (int f = 0; f < FI; ++f)
+#pragma unroll
+                    for (int k = 0; k < KI; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) dw[f][k][j] = ldexpf(dw[f][k][j], e - scale);
+                scale = e;
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < Z::kRows / 16; ++h) {
+            if constexpr (!kScaled) form(h);
+            const int by_row = kScaled ? scale_exponent(most[h]) : 0;
+            gst::Pack<S, N> dz[Z::FS];
+            auto round = [&](int e) {
+#pragma unroll
+                for (int s = 0; s < Z::FS; ++s)
+#pragma unroll
+                    for (int j = 0; j < N; ++j) dz[s].v[j] = gst::narrow<S>(kScaled ? ldexpf(now.d[h][s][j], e) : now.d[h][s][j]);
+            };
+            round(by_row);
             if (g.dx) {
                 const int64_t m = row0 + h * 16 + (lane & 15);
 #pragma unroll
@@ -254,11 +293,16 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBw
                     f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                     for (int s = 0; s < Z::FS; ++s) acc = mfma16(w[i][s], dz[s], acc);
+                    if constexpr (kScaled) {
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) acc[j] = ldexpf(acc[j], -by_row);
+                    }
                     const int c = i * 16 + (lane >> 4) * 4;
                     if (m < g.m && c < g.k) store4<S>(g.dx, m * g.lddx + c, sizeof(S) == 4 ? GS_F32 : -1, g.k - c, acc);
                 }
             }
             if (g.sums) {
+                if constexpr (kScaled) round(scale);
                 const int r = h * 16 + (lane & 15);
 #pragma unroll
                 for (int s = 0; s < Z::FS; ++s)
@@ -280,6 +324,14 @@ __global__ __launch_bounds__(kNarrowThreads, 2) void k_narrow_bwd(const NarrowBw
         if constexpr (PRE) now = next;
     }
     if (!g.sums) return;
+    if constexpr (kScaled) {
+#pragma unroll
+        for (int f = 0; f < FI; ++f)
+#pragma unroll
+            for (int k = 0; k < KI; ++k)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) dw[f][k][j] = ldexpf(dw[f][k][j], -scale);
+    }
     // the block's sums, wave after wave
 #pragma unroll
     for (int s = 0; s < Z::FS; ++s)

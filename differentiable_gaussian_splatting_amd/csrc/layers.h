@@ -52,9 +52,24 @@ __device__ __forceinline__ float2 act_both(float z, int act)
     return make_float2(s.p == 0.0f ? 0.0f : z * s.p, s.t == 0.0f ? s.p : s.p + z * s.t * dv);
 }
 
+// f16 operands that may lie beyond f16's range are scaled by 2^e, which brings
+// their largest finite |value| to [2^14, 2^15) as far as 2^-e stays a normal float.
+__device__ __forceinline__ int scale_exponent(float most)
+{
+    return most > 0.0f ? min(15 - __builtin_amdgcn_frexp_expf(most), 126) : 0;
+}
+__device__ __forceinline__ float larger(float most, float v)
+{
+    const float a = fabsf(v);
+    return a <= 3.402823466e38f ? fmaxf(most, a) : most;   // not infinity, not NaN
+}
+
 // What follows a product: out = act(z + bias) + residual, with z + bias kept
-// in pre (each null: not there).  Types are GS_F32 or the product's own.
+// in pre (each null: not there).  Types are GS_F32 or the product's own.  down:
+// what the row's sums are multiplied with first, at m lddown.
 struct Epilogue {
+    const float* down;
+    int64_t lddown;
     const void* bias;
     const void* res;
     void* pre;
@@ -71,6 +86,8 @@ enum { kLarge = 0, kMedium = 1, kSmall = 2, kTiny = 3 };
 
 struct LayerMm {
     Operand a, b;                // rows of out, columns of out
+    const void* a_other;         // what a is instead of a.p if *other is not 0 (other null: it stays)
+    const int32_t* other;
     int64_t m, k;
     Epilogue e;
     int64_t tm, tn;              // tiles

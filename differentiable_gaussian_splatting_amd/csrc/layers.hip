@@ -22,58 +22,174 @@ constexpr int kDzThreads = 256;
 // dz, four columns of a row per thread: tx threads side by side, 256 / tx rows
 // at once, a block walks `rows` rows.  dz is rounded to the layer's type, as
 // the matrix instructions take it (a gradient that passes between layers of
-// that type would be rounded the same way); the column sums are of the f32
-// values, one partial row per block row, so they do not depend on timing.
+// that type would be rounded the same way; a second part of each value would
+// double both products); the column sums are of the f32 values, one partial row
+// per block row, so they do not depend on timing.
+//
+// f16 holds 2^-24 to 65504 only, and dout act'(pre), or dout times the other
+// half of a gated layer, may lie anywhere in f32's range.  So f16 values of dz
+// are scaled by a power of two first, which the products' epilogues take back.
+// The call's scale brings the largest finite |dz| to [2^14, 2^15).  It serves
+// dw, which sums over the rows, and dx too if no row's largest is below 2^-14 of
+// that: then the lost part of a value is at most 2^-11 of it or 2^-25 of its
+// row's largest.  Otherwise dx has a dz of its own, scaled row by row, so that
+// rows do not meet.  The largest values are found in a pass of their own
+// (k_dz_max; 8191 x 2049 -> 4097: 57 us of 576).
 struct DzJob {
     const void *pre, *dout;
-    void* dz;            // null: the sums alone
+    void* dz;            // null: not wanted
+    void* dz_rows;       // f16: by the rows' scales where these differ too much; null: not wanted
     float* sums;         // [row blocks][n], null: none
     void* dbias;         // or, where one block holds all rows, the gradient itself
+    float* row_max;      // f16: [m][chunks], the largest |dz| of `chunk` columns,
+    float* all_max;      // and [2][max_blocks], the largest and the least of these but 0 that a block saw
+    float* row_down;     // f16: [m], what takes a row's scale back,
+    float* all_down;     // and the call's
+    int32_t* by_rows;    // f16: 1 if dz_rows is written
     int32_t dbias_type, accumulate;
     int64_t m, n;        // n: columns of dout
-    int64_t ldpre, lddout, lddz, rows;
-    int32_t act, dout_type, tx, col_blocks;
+    int64_t ldpre, lddout, lddz, rows, chunk;
+    int32_t act, dout_type, tx, col_blocks, chunks, max_blocks;
 };
+
+constexpr int kMaxBlocks = 2048;   // of the pass for the largest values
+
+// columns n to n + 3 of row m of dz; gated: of dg, and du
+template <typename S, bool GATED>
+__device__ __forceinline__ void dz_of(const DzJob& g, int64_t m, int64_t n, int valid, f32x4& dz, f32x4& du)
+{
+    const int type = sizeof(S) == 4 ? GS_F32 : -1;
+    dz = load4<S>(g.dout, m * g.lddout + n, g.dout_type, valid);
+    if constexpr (GATED) {
+        const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
+        const f32x4 u = load4<S>(g.pre, m * g.ldpre + g.n + n, type, valid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 v = act_both(z[j], g.act);
+            du[j] = dz[j] * v.x;
+            dz[j] = dz[j] * u[j] * v.y;
+        }
+    } else if (g.act != GS_ACT_NONE) {
+        const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) dz[j] *= act_both(z[j], g.act).y;
+    }
+}
+
+// the largest of a and the least of b over the block
+__device__ __forceinline__ float2 block_range(float a, float b, float2* part)
+{
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        a = fmaxf(a, __shfl_xor(a, d));
+        b = fminf(b, __shfl_xor(b, d));
+    }
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = make_float2(a, b);
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kDzThreads / 64; ++w) {
+        a = fmaxf(a, part[w].x);
+        b = fminf(b, part[w].y);
+    }
+    return make_float2(a, b);
+}
+
+// the largest finite |dz| of each row, by chunks of its columns, and of each block
+template <bool GATED>
+__global__ __launch_bounds__(kDzThreads) void k_dz_max(const DzJob g)
+{
+    __shared__ float2 part[kDzThreads / 64];
+    const int lane = threadIdx.x & 63, x = lane % g.tx, y = lane / g.tx, ny = 64 / g.tx;
+    const int64_t groups = (g.m + ny - 1) / ny * g.chunks, stride = (int64_t)gridDim.x * (kDzThreads / 64);
+    float all = 0.0f, least = INFINITY;
+    for (int64_t t = (int64_t)blockIdx.x * (kDzThreads / 64) + (threadIdx.x >> 6); t < groups; t += stride) {
+        const int64_t m = t / g.chunks * ny + y, c = t % g.chunks, end = min(g.n, (c + 1) * g.chunk);
+        float most = 0.0f;
+        auto take = [&](int64_t n, int valid) {
+            f32x4 dz, du;
+            dz_of<gst::f16, GATED>(g, m, n, valid, dz, du);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                most = larger(most, dz[j]);
+                if constexpr (GATED) most = larger(most, du[j]);
+            }
+        };
+        if (m < g.m) {
+            int64_t n = c * g.chunk + x * 4;
+#pragma unroll 2
+            for (; n + 4 <= end; n += g.tx * 4) take(n, 4);
+            if (n < end) take(n, (int)(end - n));
+        }
+        for (int d = 1; d < g.tx; d <<= 1) most = fmaxf(most, __shfl_xor(most, d));
+        if (x == 0 && m < g.m) g.row_max[m * g.chunks + c] = most;
+        all = fmaxf(all, most);
+        if (most > 0.0f) least = fminf(least, most);
+    }
+    const float2 v = block_range(all, least, part);
+    if (threadIdx.x == 0) {
+        g.all_max[blockIdx.x] = v.x;
+        g.all_max[gridDim.x + blockIdx.x] = v.y;
+    }
+}
 
 template <typename S, bool GATED>
 __global__ __launch_bounds__(kDzThreads) void k_dz(const DzJob g)
 {
+    constexpr bool kScaled = std::is_same<S, gst::f16>::value;
+    __shared__ f32x4 part[kDzThreads];
     const int x = threadIdx.x % g.tx, y = threadIdx.x / g.tx, ny = kDzThreads / g.tx;
     const int type = sizeof(S) == 4 ? GS_F32 : -1;
     const int64_t cb = blockIdx.x % g.col_blocks, rb = blockIdx.x / g.col_blocks;
     const int64_t n = (cb * g.tx + x) * 4, end = min(g.m, (rb + 1) * g.rows);
     const int valid = (int)min((int64_t)4, g.n - n);
+    float up = 1.0f;   // the call's scale
+    bool by_rows = false;
+    if constexpr (kScaled) {
+        if (g.row_max) {
+            float most = 0.0f, least = INFINITY;
+            for (int b = threadIdx.x; b < g.max_blocks; b += kDzThreads) {
+                most = fmaxf(most, g.all_max[b]);
+                least = fminf(least, g.all_max[g.max_blocks + b]);
+            }
+            const float2 v = block_range(most, least, reinterpret_cast<float2*>(part));
+            __syncthreads();   // part is free again
+            const int e = scale_exponent(v.x);
+            up = ldexpf(1.0f, e);
+            by_rows = g.dz_rows && v.y * 16384.0f < v.x;
+            if (blockIdx.x == 0 && threadIdx.x == 0) {
+                *g.all_down = ldexpf(1.0f, -e);
+                *g.by_rows = by_rows;
+            }
+        }
+    }
     f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
     if (valid > 0) {
         for (int64_t m = rb * g.rows + y; m < end; m += ny) {
-            const f32x4 d = load4<S>(g.dout, m * g.lddout + n, g.dout_type, valid);
-            f32x4 dz = d;
+            f32x4 dz, du;
+            float most = 0.0f;
+            if (kScaled && by_rows) most = g.row_max[m * g.chunks];
+            dz_of<S, GATED>(g, m, n, valid, dz, du);
+            if constexpr (kScaled) {
+                float own = up;
+                if (by_rows) {
+                    for (int c = 1; c < g.chunks; ++c) most = fmaxf(most, g.row_max[m * g.chunks + c]);
+                    own = ldexpf(1.0f, scale_exponent(most));
+                    store4<S>(g.dz_rows, m * g.lddz + n, type, valid, dz * own);
+                    if constexpr (GATED) store4<S>(g.dz_rows, m * g.lddz + g.n + n, type, valid, du * own);
+                }
+                if (g.row_down && cb == 0 && x == 0) g.row_down[m] = 1.0f / own;
+            }
             if constexpr (GATED) {
-                const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
-                const f32x4 u = load4<S>(g.pre, m * g.ldpre + g.n + n, type, valid);
-                f32x4 du;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 v = act_both(z[j], g.act);
-                    dz[j] = d[j] * u[j] * v.y;
-                    du[j] = d[j] * v.x;
-                }
-                store4<S>(g.dz, m * g.lddz + g.n + n, type, valid, du);
-                store4<S>(g.dz, m * g.lddz + n, type, valid, dz);
+                store4<S>(g.dz, m * g.lddz + g.n + n, type, valid, kScaled ? du * up : du);
+                store4<S>(g.dz, m * g.lddz + n, type, valid, kScaled ? dz * up : dz);
             } else {
-                if (g.act != GS_ACT_NONE) {
-                    const f32x4 z = load4<S>(g.pre, m * g.ldpre + n, type, valid);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) dz[j] = d[j] * act_both(z[j], g.act).y;
-                }
-                if (g.dz) store4<S>(g.dz, m * g.lddz + n, type, valid, dz);
+                if (g.dz) store4<S>(g.dz, m * g.lddz + n, type, valid, kScaled ? dz * up : dz);
                 sum += dz;
             }
         }
     }
     if constexpr (!GATED) {
         if (!g.sums && !g.dbias) return;
-        __shared__ f32x4 part[kDzThreads];
         part[threadIdx.x] = sum;
         __syncthreads();
         if (y == 0 && valid > 0) {
@@ -307,6 +423,7 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     }
     // dz, the layer's dout itself where nothing changes it
     const bool own = m * n > 0 && (gated || act != GS_ACT_NONE || dout->type != type) && (dx || dw);
+    const bool scaled = own && type == GS_F16;
     DzJob z{};
     int64_t row_blocks = 0;
     if (own || (dbias && m > 0)) {
@@ -327,6 +444,19 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         row_blocks = ceil_div(m, z.rows);
         z.lddz = (n + 7) / 8 * 8;   // rows that start on 16 bytes
         if (own && !(z.dz = gs_malloc(ctx, m * z.lddz * size, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+        if (scaled) {
+            // a wave takes whole rows, or where there are too few of them up to 64 pieces of one
+            z.chunk = m >= 4096 ? ceil_div(z.n, 256) * 256 : std::max<int64_t>(1024, ceil_div(ceil_div(z.n, 64), 256) * 256);
+            z.chunks = (int32_t)ceil_div(z.n, z.chunk);
+            z.max_blocks = (int32_t)std::min<int64_t>(ceil_div(ceil_div(m, 64 / z.tx) * z.chunks, kDzThreads / 64), kMaxBlocks);
+            if (!(z.row_max = (float*)gs_malloc(ctx, 4 * (m * z.chunks + m + 2 * kMaxBlocks + 2), GS_MEM_SCRATCH, tmp)))
+                return GS_ERR_OOM;
+            z.row_down = z.row_max + m * z.chunks;
+            z.all_max = z.row_down + m;
+            z.all_down = z.all_max + 2 * kMaxBlocks;
+            z.by_rows = (int32_t*)(z.all_down + 1);
+            if (dx && !(z.dz_rows = gs_malloc(ctx, m * z.lddz * size, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
+        }
         if (dbias && row_blocks == 1) z.dbias = dbias->data, z.dbias_type = dbias->type, z.accumulate = accumulate;
         else if (dbias && !(z.sums = (float*)gs_malloc(ctx, 4 * row_blocks * n, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
     }
@@ -341,6 +471,12 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         gx.a = operand(dz, lddz, m);
         gx.b = operand(w->data, w->stride, k);
         gx.e.n = k;
+        if (scaled) {
+            gx.a_other = z.dz_rows;
+            gx.other = z.by_rows;
+            gx.e.down = z.row_down;
+            gx.e.lddown = 1;
+        }
         gx.e.out = dx->data, gx.e.ldout = dx->stride, gx.e.out_type = (int8_t)dx->type;
         ws = plan(ctx, type == GS_F32, &gx);
     }
@@ -351,6 +487,7 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
         gw.a = operand(dz, lddz, own ? lddz : n);   // own: the columns beside the last are there to be read
         gw.b = operand(x->data, x->stride, k);
         gw.e.n = k;
+        if (scaled) gw.e.down = z.all_down;
         gw.e.out = dw->data, gw.e.ldout = dw->stride, gw.e.out_type = (int8_t)dw->type;
         if (accumulate) gw.e.res = dw->data, gw.e.ldres = dw->stride, gw.e.res_type = (int8_t)dw->type;
         wsw = plan(ctx, type == GS_F32, &gw);
@@ -370,6 +507,8 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     if (z.m > 0 && z.n > 0) {
         GsTimerScope ts(ctx, "layer_dz");
         const dim3 grid((uint32_t)(row_blocks * z.col_blocks)), block(kDzThreads);
+        if (scaled && gated) hipLaunchKernelGGL((k_dz_max<true>), dim3(z.max_blocks), block, 0, ctx->stream, z);
+        else if (scaled) hipLaunchKernelGGL((k_dz_max<false>), dim3(z.max_blocks), block, 0, ctx->stream, z);
         auto go = [&](auto s) {
             typedef decltype(s) S;
             if (gated) hipLaunchKernelGGL((k_dz<S, true>), grid, block, 0, ctx->stream, z);

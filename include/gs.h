@@ -521,9 +521,12 @@ gs_status gs_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, con
  *   dx = dz w,  dw = dz^T x,  dbias = sum of dz over the rows,
  * dw and dbias plus their old values when accumulate != 0.  The residual's
  * gradient is dout.  pre: as written by gs_linear_fwd; not read (may be NULL)
- * for GS_ACT_NONE.  dz is rounded to T for dx and dw, not for dbias.  dx, dw,
- * dbias: each may be NULL: not wanted.  Without rows, dw and dbias are zero (or
- * stay).  An output overlaps no input and no other output.  Errors: as
+ * for GS_ACT_NONE.  dz is rounded to T for dx and dw, not for dbias; f16, whose
+ * range f32 values may leave, after scaling by powers of two that are taken back
+ * in f32: a finite value stays finite, and its error is at most 2^-11 of itself or,
+ * for dx 2^-25 of its row's largest finite |dz|, for dw 2^-39 of the call's.
+ * dx, dw, dbias: each may be NULL: not wanted.  Without rows, dw and dbias are
+ * zero (or stay).  An output overlaps no input and no other output.  Errors: as
  * gs_linear_fwd. */
 gs_status gs_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
                         const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw,
@@ -537,7 +540,7 @@ gs_status gs_gated_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, int3
 
 /* Gradients of gs_gated_fwd: dg = dout u act'(g), du = dout act(g),
  *   dx = [dg du] w,  dw = [dg du]^T x (plus the old dw when accumulate != 0).
- * dg and du are rounded to T.  pre is required.  Else as gs_linear_bwd. */
+ * dg and du are rounded to T, as dz above.  pre is required.  Else as gs_linear_bwd. */
 gs_status gs_gated_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* pre, int32_t act,
                        const gs_tensor* dout, int32_t accumulate, const gs_tensor* dx, const gs_tensor* dw);
 
