@@ -402,25 +402,37 @@ inline int64_t narrow_blocks(const gs_ctx* ctx, int type, int64_t m, int64_t f, 
     return std::min(ceil_div(m, rows), (ceil_div(f, 16) * ceil_div(k, 16) <= 2 ? 4 : 2) * (int64_t)ctx->num_cu);
 }
 
+// blocks of w that a wave holds: pieces of a row as the matrix instruction takes them, and of 16 columns
+template <typename S>
+inline int64_t narrow_steps(int64_t k)
+{
+    return ceil_div(k, 64 / (int64_t)sizeof(S));
+}
+// whether the forward pass has a kernel
+inline bool narrow_fwd(int type, const LayerMm& g)
+{
+    const int64_t steps = type == GS_F32 ? narrow_steps<float>(g.k) : narrow_steps<gst::f16>(g.k), cols = ceil_div(g.e.n, 16);
+    return g.gated ? with_blocks<kNarrowFwd / 2>(steps, cols, [](auto, auto) {})
+                   : with_blocks<kNarrowFwd>(steps, cols, [](auto, auto) {});
+}
 // whether the backward pass of f x k weights has a kernel
 inline bool narrow_bwd(int64_t f, int64_t k)
 {
     return with_blocks<kNarrowBwd>(ceil_div(f, 16), ceil_div(k, 16), [](auto, auto) {});
 }
 
-// one type each (layer_narrow_*.hip); false: too wide
-bool launch_narrow_fwd_f32(gs_ctx* ctx, const LayerMm& g);
-bool launch_narrow_fwd_f16(gs_ctx* ctx, const LayerMm& g);
-bool launch_narrow_fwd_bf16(gs_ctx* ctx, const LayerMm& g);
-bool launch_narrow_bwd_f32(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
-bool launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
-bool launch_narrow_bwd_bf16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+// one type each (layer_narrow_*.hip), for widths that narrow_fwd or narrow_bwd allow
+void launch_narrow_fwd_f32(gs_ctx* ctx, const LayerMm& g);
+void launch_narrow_fwd_f16(gs_ctx* ctx, const LayerMm& g);
+void launch_narrow_fwd_bf16(gs_ctx* ctx, const LayerMm& g);
+void launch_narrow_bwd_f32(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+void launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
+void launch_narrow_bwd_bf16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks);
 
 template <typename S, bool GATED>
-bool launch_narrow_rows(gs_ctx* ctx, const LayerMm& g)
+void launch_narrow_rows(gs_ctx* ctx, const LayerMm& g)
 {
-    constexpr int kStep = 64 / sizeof(S);
-    return with_blocks<kNarrowFwd / (GATED ? 2 : 1)>(ceil_div(g.k, kStep), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
+    with_blocks<kNarrowFwd / (GATED ? 2 : 1)>(narrow_steps<S>(g.k), ceil_div(g.e.n, 16), [&](auto ks, auto ni) {
         // waves that come back for more rows: 6 blocks a compute unit, and where
         // w takes few registers 24 (32 -> 48 f32: 86 us, 106 with 6; 64 -> 64: 184, 170)
         constexpr int kOps = decltype(ks)::value * decltype(ni)::value * (GATED ? 2 : 1);
@@ -432,15 +444,16 @@ bool launch_narrow_rows(gs_ctx* ctx, const LayerMm& g)
 }
 
 template <typename S>
-bool launch_narrow_fwd(gs_ctx* ctx, const LayerMm& g)
+void launch_narrow_fwd(gs_ctx* ctx, const LayerMm& g)
 {
-    return g.gated ? launch_narrow_rows<S, true>(ctx, g) : launch_narrow_rows<S, false>(ctx, g);
+    if (g.gated) launch_narrow_rows<S, true>(ctx, g);
+    else launch_narrow_rows<S, false>(ctx, g);
 }
 
 template <typename S>
-bool launch_narrow_bwd(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks)
+void launch_narrow_bwd(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks)
 {
-    return with_blocks<kNarrowBwd>(ceil_div(g.f, 16), ceil_div(g.k, 16), [&](auto fi, auto ki) {
+    with_blocks<kNarrowBwd>(ceil_div(g.f, 16), ceil_div(g.k, 16), [&](auto fi, auto ki) {
         hipLaunchKernelGGL((k_narrow_bwd<S, decltype(fi)::value, decltype(ki)::value>), dim3((uint32_t)blocks),
                            dim3(kNarrowThreads), 0, ctx->stream, g);
     });

@@ -3,7 +3,7 @@
 
 namespace gsm {
 
-bool launch_narrow_fwd_f16(gs_ctx* ctx, const LayerMm& g) { return launch_narrow_fwd<f16>(ctx, g); }
-bool launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks) { return launch_narrow_bwd<f16>(ctx, g, blocks); }
+void launch_narrow_fwd_f16(gs_ctx* ctx, const LayerMm& g) { launch_narrow_fwd<f16>(ctx, g); }
+void launch_narrow_bwd_f16(gs_ctx* ctx, const NarrowBwd& g, int64_t blocks) { launch_narrow_bwd<f16>(ctx, g, blocks); }
 
 }  // namespace gsm

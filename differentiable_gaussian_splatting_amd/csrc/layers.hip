@@ -359,18 +359,20 @@ static gs_status check_launch(gs_ctx* ctx)
     return GS_OK;
 }
 
-static bool launch_narrow(gs_ctx* ctx, int type, const LayerMm& g)
+static void launch_narrow(gs_ctx* ctx, int type, const LayerMm& g)
 {
     GsTimerScope ts(ctx, "layer_narrow");
-    return type == GS_F32 ? launch_narrow_fwd_f32(ctx, g) :
-           type == GS_F16 ? launch_narrow_fwd_f16(ctx, g) : launch_narrow_fwd_bf16(ctx, g);
+    if (type == GS_F32) launch_narrow_fwd_f32(ctx, g);
+    else if (type == GS_F16) launch_narrow_fwd_f16(ctx, g);
+    else launch_narrow_fwd_bf16(ctx, g);
 }
 
-static bool launch_narrow(gs_ctx* ctx, int type, const NarrowBwd& g, int64_t blocks)
+static void launch_narrow(gs_ctx* ctx, int type, const NarrowBwd& g, int64_t blocks)
 {
     GsTimerScope ts(ctx, "layer_narrow");
-    return type == GS_F32 ? launch_narrow_bwd_f32(ctx, g, blocks) :
-           type == GS_F16 ? launch_narrow_bwd_f16(ctx, g, blocks) : launch_narrow_bwd_bf16(ctx, g, blocks);
+    if (type == GS_F32) launch_narrow_bwd_f32(ctx, g, blocks);
+    else if (type == GS_F16) launch_narrow_bwd_f16(ctx, g, blocks);
+    else launch_narrow_bwd_bf16(ctx, g, blocks);
 }
 
 gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, const gs_tensor* bias, int act,
@@ -391,7 +393,10 @@ gs_status launch_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     g.e.out = out->data, g.e.ldout = out->stride, g.e.out_type = (int8_t)out->type;
     if (g.m == 0 || g.e.n == 0) return GS_OK;
     if (few_rows(g)) return launch_layer_few(ctx, x->type, g);
-    if (launch_narrow(ctx, x->type, g)) return check_launch(ctx);
+    if (narrow_fwd(x->type, g)) {
+        launch_narrow(ctx, x->type, g);
+        return check_launch(ctx);
+    }
     const int64_t ws = plan(ctx, x->type == GS_F32, &g);
     if (ws && !(g.ws = (float*)gs_malloc(ctx, 4 * ws, GS_MEM_SCRATCH, tmp))) return GS_ERR_OOM;
     return launch_mm(ctx, x->type, g);
