@@ -173,6 +173,15 @@ __device__ __forceinline__ double block_sum(double x, double* part)
     return x;
 }
 
+// 1 / (|u| + eps) from the sum of squares, as two factors: |u| may be anything up
+// to 2^21 times the largest float, and its inverse less than a normal float.
+__device__ __forceinline__ float2 inverse_norm(double squares)
+{
+    const double d = sqrt(squares) + kEps;
+    const double down = d > 0x1p100 ? 0x1p-64 : 1.0;
+    return make_float2((float)(1.0 / (d * down)), (float)down);
+}
+
 // momentum, and the squares of u (f64, one partial per piece)
 __global__ __launch_bounds__(kThreads) void k_momentum(const Job job, const MuonConst o, const float* __restrict__ norm,
                                                        double* __restrict__ part)
@@ -213,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void k_start(const Job job, const MuonCon
     const Matrix& t = job.t[k];
     double sum = 0.0;
     for (uint32_t b = (k ? job.t[k - 1].piece_end : 0u) + threadIdx.x; b < t.piece_end; b += kThreads) sum += part[b];
-    const float inv = (float)(1.0 / (sqrt(block_sum<4>(sum, sums)) + kEps));
+    const float2 inv = inverse_norm(block_sum<4>(sum, sums));
     const int32_t ld = (int32_t)padded(t.cols, job.unit);
     each_four(padded(t.rows, job.unit) * ld, ld, blockIdx.x - before, [&](int64_t i, int, int64_t r, int32_t c) {
         const int valid = r < t.rows ? min(4, t.cols - c) : 0;   // ld is a multiple of 4: the four share a row
@@ -230,7 +239,7 @@ __global__ __launch_bounds__(kThreads) void k_start(const Job job, const MuonCon
                 u = f * g + o.mu * u;
             }
 #pragma unroll
-            for (int j = 0; j < 4; ++j) u[j] = j < valid ? u[j] * inv : 0.0f;
+            for (int j = 0; j < 4; ++j) u[j] = j < valid ? u[j] * inv.x * inv.y : 0.0f;
         }
         *reinterpret_cast<f32x4*>(x + t.x + i) = u;
     });
@@ -610,11 +619,11 @@ __global__ __launch_bounds__(W * 64) void k_small(const Job job, const MuonConst
                 sum += (double)u * u;
             }
         }
-    const float inv = (float)(1.0 / (sqrt(block_sum<W>(sum, lds.sums)) + kEps));
+    const float2 inv = inverse_norm(block_sum<W>(sum, lds.sums));
 #pragma unroll
     for (int i = 0; i < 2; ++i)
 #pragma unroll
-        for (int j = 0; j < 2; ++j) x[i][j] *= inv;
+        for (int j = 0; j < 2; ++j) x[i][j] = x[i][j] * inv.x * inv.y;
     const float down = 1.0f / kScaleX / kScaleX;
     for (int step = 0; step < steps; ++step) {
         f32x4 acc[2][2];
