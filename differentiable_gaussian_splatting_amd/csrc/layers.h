@@ -7,6 +7,7 @@
 #include <cstdint>
 
 #include "gs_internal.h"
+#include "layer_plan.h"
 #include "mm.h"
 
 namespace gsm {
@@ -80,10 +81,6 @@ struct Epilogue {
     int8_t bias_type, res_type, pre_type, out_type;
 };
 
-// The tiles of a product.  kTiny is for operands with fewer than 8 values side
-// by side (Stage in mm.h).
-enum { kLarge = 0, kMedium = 1, kSmall = 2, kTiny = 3 };
-
 struct LayerMm {
     Operand a, b;                // rows of out, columns of out
     const void* a_other;         // what a is instead of a.p if *other is not 0 (other null: it stays)
@@ -130,5 +127,17 @@ typedef Tile<256, 128, 32, 4, 2, 2> Large32;
 typedef Tile<128, 128, 32, 2, 2, 1> Medium32;
 typedef Tile<64, 64, 32, 2, 2, 2> Small32;
 typedef Tile<64, 64, 32, 2, 2, 2, true> Tiny32;
+
+template <typename T>
+constexpr bool planned_as(const TileCost& c)
+{
+    return c.m == T::BM && c.n == T::BN && c.k == T::BK;
+}
+static_assert(planned_as<Large16>(kCost16[kLarge]) && planned_as<Large16>(kCostDirect[kLarge]) &&
+              planned_as<Medium16>(kCost16[kMedium]) && planned_as<Medium16>(kCostDirect[kMedium]) &&
+              planned_as<Small16>(kCost16[kSmall]) && planned_as<Small16>(kCostDirect[kSmall]) &&
+              planned_as<Tiny16>(kCost16[kTiny]) && planned_as<Tiny16>(kCostDirect[kTiny]) &&
+              planned_as<Large32>(kCost32[kLarge]) && planned_as<Medium32>(kCost32[kMedium]) &&
+              planned_as<Small32>(kCost32[kSmall]) && planned_as<Tiny32>(kCost32[kTiny]), "tiles and their costs");
 
 }  // namespace gsm

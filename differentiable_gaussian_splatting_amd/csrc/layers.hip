@@ -258,79 +258,19 @@ gs_status launch_sum_rows(gs_ctx* ctx, int type, const SumJob& g)
     return GS_OK;
 }
 
-// What n tiles on each compute unit take for one step of k: once us for
-// every round of `resident` blocks and each us for every tile (measured, with
-// one to eight tiles a unit: 128 x 128 x 64 through registers 1.0, 1.45 and 2.25
-// us for one, two and three, 64 x 64 x 64 0.72, 1.2 and 2.2 for two, four and
-// eight, 256 x 256 x 64 2.4 for one, loaded directly 2.15).
-struct TileCost {
-    int32_t m, n, k, resident;
-    double once, each;
-};
-template <typename T>
-constexpr TileCost cost(int resident, double once, double each)
-{
-    return TileCost{T::BM, T::BN, T::BK, resident, once, each};
-}
-constexpr TileCost kCost16[] = {cost<Large16>(1, 0.1, 2.3), cost<Medium16>(2, 0.5, 0.48), cost<Small16>(5, 0.2, 0.25),
-                                cost<Tiny16>(3, 0.3, 0.3)};
-constexpr TileCost kCostDirect[] = {cost<Large16>(1, 0.1, 2.1), cost<Medium16>(2, 0.3, 0.46), cost<Small16>(5, 0.2, 0.25),
-                                    cost<Tiny16>(3, 0.3, 0.3)};
-constexpr TileCost kCost32[] = {cost<Large32>(1, 0.1, 2.5), cost<Medium32>(2, 0.5, 1.35), cost<Small32>(3, 0.3, 0.48),
-                                cost<Tiny32>(3, 0.4, 0.5)};
-constexpr double kJoinUs = 4.0;          // a further launch
-constexpr double kJoinRate = 4e6;        // bytes per us of sums written and read
-
-// What the tiles from `full` on cost: `tiles` of them, in s ranges of k.
-double cost_us(const gs_ctx* ctx, const TileCost& c, int64_t tiles, int64_t steps, int64_t s)
-{
-    const int64_t blocks = tiles * s;
-    const double step = ceil_div(blocks, (int64_t)c.resident * ctx->num_cu) * c.once + ceil_div(blocks, ctx->num_cu) * c.each;
-    return (double)(ceil_div(steps, s) + 1) * step + (s > 1 ? kJoinUs + 8.0 * blocks * c.m * c.n / kJoinRate : 0.0);
-}
-
-// The tile of a product of m x n (n of the tiles: both halves of a gated layer)
-// over k, and the tiles that are split, as the costs above make fastest.  Whole
-// rounds of the card are formed whole; a last round that would leave most of
-// it idle, or the only one, is split over k (8191 x 4097 over 2049 f16: 544
-// tiles of 256 x 256 on 256 units).  Returns the floats of its workspace.
+// The tile of a product and the tiles that are split (layer_plan.h).  Returns the floats of its workspace.
 int64_t plan(const gs_ctx* ctx, bool f32, LayerMm* g)
 {
-    const int64_t n = g->e.n * (g->gated ? 2 : 1);
-    const bool tiny = (!g->a_col && g->k < 8) || (g->a_col && g->m < 8) || (!g->b_col && g->k < 8) ||
-                      (g->b_col && g->e.n < 8);
-    const TileCost* costs = f32 ? kCost32 : loads_direct(*g) ? kCostDirect : kCost16;
-    double best = 0.0;
-    int64_t best_s = 1;
-    for (int t = tiny ? kTiny : kLarge; t <= (tiny ? kTiny : kSmall); ++t) {
-        const TileCost& c = costs[t];
-        const int64_t tiles = ceil_div(g->m, c.m) * ceil_div(n, c.n), steps = std::max<int64_t>(1, ceil_div(g->k, c.k));
-        const int64_t slots = (int64_t)c.resident * ctx->num_cu;
-        const double whole = cost_us(ctx, c, tiles, steps, 1);
-        if (best == 0.0 || whole < best) {
-            best = whole;
-            best_s = 1;
-            g->tile = t;
-            g->full = tiles;
-        }
-        const int64_t rest = tiles % slots, full = tiles - rest;
-        for (int64_t s = 2; rest > 0 && s <= steps && rest * s <= 2 * slots; s += std::max<int64_t>(1, s / 4)) {
-            const double us = (full ? cost_us(ctx, c, full, steps, 1) : 0.0) + cost_us(ctx, c, rest, steps, s);
-            if (us >= best) continue;
-            best = us;
-            best_s = s;
-            g->tile = t;
-            g->full = full;
-        }
-    }
-    const TileCost& c = costs[g->tile];
-    g->tm = ceil_div(g->m, c.m);
-    g->tn = ceil_div(n, c.n);
-    g->kper = ceil_div(std::max<int64_t>(1, ceil_div(g->k, c.k)), best_s) * c.k;
-    g->splits = (int32_t)std::max<int64_t>(1, ceil_div(g->k, g->kper));
-    if (g->splits == 1) g->full = g->tm * g->tn;
+    const TilePlan p = plan_tiles(ctx->num_cu, f32, loads_direct(*g),
+                                  ProductShape{g->m, g->e.n, g->k, g->a_col, g->b_col, g->gated});
+    g->tile = p.tile;
+    g->tm = p.tm;
+    g->tn = p.tn;
+    g->full = p.full;
+    g->splits = p.splits;
+    g->kper = p.kper;
     g->ws = nullptr;
-    return g->splits > 1 ? g->splits * (g->tm * g->tn - g->full) * c.m * c.n : 0;
+    return p.floats;
 }
 
 gs_status launch_mm(gs_ctx* ctx, int type, const LayerMm& g)
