@@ -14,7 +14,8 @@ SOURCES = ["layer_mm_f32.hip", "layer_mm_f16.hip", "layer_mm_bf16.hip", "layer_n
            "layer_narrow_bf16.hip", "muon.hip", "gs_api.cpp", "scan.hip", "radix.hip", "project.hip", "binning.hip",
            "raster.hip", "planner.hip", "loss.hip", "adam.hip", "group.hip", "embed.hip", "lists.hip", "layers.hip",
            "layer_few.hip", "tensors_api.cpp", "gate.cpp"]
-HEADERS = ["gs_device.h", "gs_internal.h", "gs_tensor.h", "mm.h", "layers.h", "layer_plan.h", "layer_mm.h", "layer_narrow.h"]
+HEADERS = ["gs_device.h", "gs_internal.h", "gs_tensor.h", "mm.h", "layers.h", "layer_plan.h", "layer_mm.h", "layer_narrow.h",
+           "muon_plan.h"]
 
 # Float discipline of the forward path: no contraction of a*b+c into fma (only
 # explicit fmaf), correctly rounded f32 division and square root, IEEE

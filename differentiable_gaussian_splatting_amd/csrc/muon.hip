@@ -27,6 +27,7 @@
 #include "gs_internal.h"
 #include "gs_tensor.h"
 #include "mm.h"
+#include "muon_plan.h"
 
 namespace {
 
@@ -37,8 +38,6 @@ typedef gst::Pack<float, 4> Four;
 constexpr float kA = 3.4445f, kB = -4.7750f, kC = 2.0315f;
 constexpr double kEps = 1e-7;
 constexpr float kScaleX = 32768.0f, kScaleP = 16384.0f;   // of X and G, and of P
-
-__host__ __device__ constexpr int64_t padded(int64_t n, int64_t to) { return (n + to - 1) / to * to; }
 
 constexpr int kThreads = 256;
 constexpr int kPiece = 4096;      // values of a block of the elementwise kernels
@@ -286,8 +285,6 @@ __global__ __launch_bounds__(kThreads) void k_apply(const Job job, const MuonCon
     });
 }
 
-enum { kGram, kPoly, kNext };
-
 // One tile of a matrix's product: G (kGram), P from G (kPoly) or the next X.
 // G and P are symmetric: their tiles on and below the diagonal are computed and
 // those below it written to both places.  Sides are the padded ones.
@@ -371,13 +368,7 @@ typedef Tile<256, 256, 32, 2, 4, 2> Large;
 typedef Tile<128, 128, 32, 2, 2, 1> Medium;
 typedef Tile<64, 64, 64, 2, 2, 1> Small;
 
-// tiles of a matrix's product, of its padded sides
-template <int KIND>
-int64_t tiles_of(const Matrix& t, int64_t unit, int b)
-{
-    const int64_t rows = padded(t.rows, unit) / b, cols = padded(t.cols, unit) / b, s = std::min(rows, cols);
-    return KIND == kNext ? rows * cols : s * (s + 1) / 2;
-}
+static_assert(Large::BM == kNewtonCosts[0].b && Medium::BM == kNewtonCosts[1].b && Small::BM == kNewtonCosts[2].b, "tiles");
 
 // the matrices whose products share launches, and the floats of their X and G
 struct Group {
@@ -408,84 +399,14 @@ void launch_tiles(gs_ctx* ctx, const Group& q, const float* from, float* to, con
                            dim3(kThreads), 0, ctx->stream, to, q.s, splits);
 }
 
-// What a group's product takes with a tile: for a step of 32 values of k,
-// once us for every round of `resident` tiles on each compute unit and each us
-// for every tile (measured: 128 x 128 takes 1.3 and 2.0 us for one and two a
-// unit, 64 x 64 0.9, 1.5 and 3.1 for two, four and eight, 256 x 256 3.1).
-struct TileCost {
-    int b, resident;
-    double once, each;
-};
-constexpr TileCost kCosts[3] = {{Large::BM, 1, 0.1, 3.0}, {Medium::BM, 2, 0.5, 0.75}, {Small::BM, 4, 0.2, 0.33}};
-
-template <int KIND>
-double cost_us(const gs_ctx* ctx, const Job& job, int64_t unit, int splits, const TileCost& c)
-{
-    double work = 0.0, longest = 0.0;
-    int64_t tiles = 0;
-    for (int32_t k = 0; k < job.count; ++k) {
-        const Matrix& t = job.t[k];
-        const double steps = (double)ceil_div(KIND == kGram ? std::max(t.rows, t.cols) : std::min(t.rows, t.cols), 32 * splits) + 2.0;
-        const int64_t n = tiles_of<KIND>(t, unit, c.b) * splits;
-        tiles += n;
-        work += (double)n * steps;
-        longest = std::max(longest, steps);
-    }
-    const int64_t rounds = ceil_div(tiles, (int64_t)c.resident * ctx->num_cu), on_each = ceil_div(tiles, ctx->num_cu);
-    return std::max(work / (double)tiles * ((double)rounds * c.once + (double)on_each * c.each), longest * (c.once + c.each));
-}
-
-// the cheapest tile of those that the unit is a multiple of, and its cost
-template <int KIND>
-int choose_tile(const gs_ctx* ctx, const Job& job, int64_t unit, int splits, double* us)
-{
-    int best = 2;
-    *us = cost_us<KIND>(ctx, job, unit, splits, kCosts[2]);
-    for (int k = 1; k >= 0 && unit % kCosts[k].b == 0; --k) {
-        const double c = cost_us<KIND>(ctx, job, unit, splits, kCosts[k]);
-        if (c >= *us) continue;
-        *us = c;
-        best = k;
-    }
-    return best;
-}
-
 template <int KIND, bool TALL>
 void launch_newton(gs_ctx* ctx, const Group& q, const float* from, float* to, const float* poly)
 {
     double us;
-    const int tile = choose_tile<KIND>(ctx, q.job, q.job.unit, KIND == kGram ? q.splits : 1, &us);
+    const int tile = choose_tile<KIND>(ctx->num_cu, q.job, q.job.unit, KIND == kGram ? q.splits : 1, &us);
     if (tile == 0) launch_tiles<KIND, TALL, Large>(ctx, q, from, to, poly);
     else if (tile == 1) launch_tiles<KIND, TALL, Medium>(ctx, q, from, to, poly);
     else launch_tiles<KIND, TALL, Small>(ctx, q, from, to, poly);
-}
-
-// The unit to which a group's sides are padded (the largest tile it may use),
-// and how often G's product is split over its long k (few tiles, a few
-// matrices of one long side each, leave the card idle otherwise).
-void choose_sizes(const gs_ctx* ctx, Group* q)
-{
-    double least = 0.0;
-    for (int unit = 64; unit <= 256; unit *= 2) {
-        double poly, next, gram;
-        choose_tile<kPoly>(ctx, q->job, unit, 1, &poly);
-        choose_tile<kNext>(ctx, q->job, unit, 1, &next);
-        int64_t s = 0;
-        for (int32_t k = 0; k < q->job.count; ++k) {
-            const int64_t side = padded(std::min(q->job.t[k].rows, q->job.t[k].cols), unit);
-            s += side * side;
-        }
-        for (int splits = 1; splits <= 32; splits *= 2) {
-            if (splits > 1 && splits * s > (1ll << 26)) break;
-            choose_tile<kGram>(ctx, q->job, unit, splits, &gram);
-            if (splits > 1) gram += 5.0 + 4.0 * (splits + 1) * s / 3e6;   // the sums' launch and bytes
-            const double us = gram + poly + next;
-            if (least > 0.0 && us >= least) continue;
-            least = us;
-            q->job.unit = unit;
-            q->splits = splits;
-        }
-    }
 }
 
 template <bool TALL>
@@ -725,7 +646,7 @@ gs_status launch_muon_list(gs_ctx* ctx, const gs_tensor* p, const gs_tensor* m, 
         }
     }
     for (Group& q : groups) {
-        choose_sizes(ctx, &q);
+        choose_sizes(ctx->num_cu, q.job, &q.job.unit, &q.splits);
         for (int32_t k = 0; k < q.job.count; ++k) {
             Matrix& t = q.job.t[k];
             const int64_t rows = padded(t.rows, q.job.unit), cols = padded(t.cols, q.job.unit), side = std::min(rows, cols);
