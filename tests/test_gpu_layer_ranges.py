@@ -133,3 +133,58 @@ def test_one_gradient_alone_and_accumulated(ctx):
     B.gs_linear_bwd(ctx, x, w, d, pre=z, act="gelu", dbias=db2)
     B.gs_linear_bwd(ctx, x, w, d, pre=z, act="gelu", dw=dw3, accumulate=True)
     assert torch.equal(dx, dx2) and torch.equal(dw, dw2) and torch.equal(db, db2) and torch.equal(dw3, 2 * dw)
+
+
+def test_graph_whose_rows_come_to_differ(ctx):
+    """Replays on values of other sizes: rows that share a scale, then rows that need their own, then masked ones."""
+    torch = _t()
+    n, k, f = 300, 264, 136
+    stream = torch.cuda.Stream()
+    c = B.Context(stream=stream)
+    x, w, z = (torch.randn(s, device="cuda").half() for s in ((n, k), (2 * f, k), (n, 2 * f)))
+    d, dx, dw = torch.randn((n, f), device="cuda"), torch.empty_like(x), torch.empty((2 * f, k), device="cuda")
+    go = lambda cc: B.gs_gated_bwd(cc, x, w, z, d, dx=dx, dw=dw)
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        go(c)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=stream):
+        go(c)
+    for rep, (some, others) in enumerate(((1.0, 1.0), (1e-9, 10.0), (1e-30, 1e-28), (0.0, 1.0), (1.0, 1e20))):
+        d.normal_()
+        d[::2] *= some
+        d[1::2] *= others
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = dx.clone(), dw.clone()
+        dx.fill_(7.0)
+        dw.fill_(7.0)
+        go(ctx)
+        torch.cuda.synchronize()
+        assert torch.equal(got[0], dx) and torch.equal(got[1], dw) and dw.isfinite().all(), rep
+    c.close()
+
+
+def test_allocation_failure_leaves_f16_gradients(ctx):
+    torch = _t()
+    from tests.test_gpu_errors import FailingContext
+    c = FailingContext()
+    x, w, z = (torch.randn(s, device="cuda").half() for s in ((300, 200), (2 * 70, 200), (300, 2 * 70)))
+    d = torch.randn((300, 70), device="cuda")
+    dx, dw = torch.full((300, 200), 7.0, device="cuda").half(), torch.full((2 * 70, 200), 7.0, device="cuda")
+    live, k = c.mem_stats()["live"], 1
+    while True:
+        c.arm(k)
+        try:
+            B.gs_gated_bwd(c, x, w, z, d, dx=dx, dw=dw)
+            break
+        except B.GsError as e:
+            assert e.status == B.GS_ERR_OOM
+            torch.cuda.synchronize()
+            assert (dx == 7).all() and (dw == 7).all() and c.mem_stats()["live"] == live
+        k += 1
+    assert k > 3
+    c.arm(0)
+    c.close()
