@@ -142,6 +142,32 @@ __device__ __forceinline__ void wave_fence()
     __builtin_amdgcn_wave_barrier();
 }
 
+// f32 in parts: an infinity, or a value above bf16's largest, has parts whose
+// products meet as NaN.  So where a result is NaN the products of its values
+// themselves are summed, which ends at the first NaN: the four of row m from
+// column n on, b's rows from `row` on.
+template <bool ACOL, bool BCOL>
+__device__ __forceinline__ f32x4 sum_again(const Operand& a, const Operand& b, int64_t m, int64_t row, int valid, int64_t k0,
+                                           int64_t k1, f32x4 z)
+{
+    const float any = (z[0] + z[1]) + (z[2] + z[3]);
+    if (any == any) return z;
+#pragma unroll 1
+    for (int j = 0; j < 4; ++j) {
+        if (z[j] == z[j] || j >= valid) continue;
+        const float* x = (const float*)a.p + (ACOL ? k0 * a.ld + m : m * a.ld + k0);
+        const float* w = (const float*)b.p + (BCOL ? k0 * b.ld + row + j : (row + j) * b.ld + k0);
+        float s = 0.0f;
+        for (int64_t k = k0; k < k1 && s == s; ++k) {
+            s = fmaf(*x, *w, s);
+            x += ACOL ? a.ld : 1;
+            w += BCOL ? b.ld : 1;
+        }
+        z[j] = s;
+    }
+    return z;
+}
+
 // Tiles of the product (DIRECT: see mm_tile); those from `full` on in `splits` ranges of k, whose sums
 // k_join adds up.
 template <typename S, int P, typename T>
@@ -204,13 +230,19 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
                 if (m >= g.m || n >= g.e.n || m < sm.own || n + 3 < sn.own) continue;
                 const int first = (int)max((int64_t)0, sn.own - n);
                 const float* v = mine + row * kRow + (GATED ? (c >> 4) * 32 + (c & 15) : c);
-                const f32x4 x = *reinterpret_cast<const f32x4*>(v);
+                f32x4 x = *reinterpret_cast<const f32x4*>(v), y = x;
+                if constexpr (GATED) y = *reinterpret_cast<const f32x4*>(v + 16);
+                if constexpr (P == 3) {
+                    const int valid = (int)min((int64_t)4, g.e.n - n);
+                    x = sum_again<ACOL, BCOL>(ga, g.b, m, n, valid, k0, k1, x);
+                    if constexpr (GATED) y = sum_again<ACOL, BCOL>(ga, g.b, m, g.e.n + n, valid, k0, k1, y);
+                }
                 if (ws) {
                     float* w = ws + (m - m0) * T::BN + (wave / T::WM) * T::NI * 16 + (v - mine - row * kRow);
                     *reinterpret_cast<f32x4*>(w) = x;
-                    if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = *reinterpret_cast<const f32x4*>(v + 16);
+                    if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = y;
                 } else if constexpr (GATED) {
-                    epilogue_gated<S>(g.e, m, n, x, *reinterpret_cast<const f32x4*>(v + 16), first);
+                    epilogue_gated<S>(g.e, m, n, x, y, first);
                 } else {
                     epilogue<S>(g.e, m, n, x, first);
                 }

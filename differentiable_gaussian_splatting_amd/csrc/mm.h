@@ -16,8 +16,9 @@
 //   P = 3: x = h + m + l in bf16, each the rounding of what the ones before
 //          leave (2^-8 of it at most, so 2^-24 |x| is left out).  Six products
 //          are kept (h h, h m, m h, m m, h l, l h); all that is left out of
-//          x y is below 2^-22 |x y|, and typically 2^-26.  Any f32 range; a
-//          value that is not finite makes its results NaN.
+//          x y is below 2^-22 |x y|, and typically 2^-26.  Any f32 range, but a
+//          value that is infinite or above bf16's largest makes its results NaN
+//          (the layers sum those again, sum_again in layer_mm.h).
 //   P = 2: x s = h + l in f16 with a power of two s that the caller knows to
 //          keep |x s| below 65504 (2^-22 |x s| is left out while |x s| >= 2^-3,
 //          2^-25 below that).  Three products (h h, h l, l h).  For the

@@ -500,10 +500,11 @@ gs_status gs_adam_tensors(gs_ctx* ctx, const gs_tensor* params, const gs_tensor*
  *
  * Types: x, w, pre and dx have one type T of GS_F32, GS_F16 and GS_BF16;
  * out, residual, bias, dout, dw and dbias are T or GS_F32 each.  Sums are f32;
- * every output is rounded once.  f32 values are multiplied exactly or as three
- * bf16 parts each (six products; what is left out of x y is below 2^-22 |x y|);
- * with parts, an f32 value of x, w or dz that is infinite, or above bf16's
- * largest, makes its results NaN. */
+ * every output is rounded once.  f32 values are multiplied exactly (few rows,
+ * narrow rows) or as three bf16 parts each (six products; what is left out of x y
+ * is below 2^-22 |x y|).  Infinities, and values above bf16's largest, are
+ * multiplied exactly wherever they meet, so that results are infinite, NaN or
+ * finite as those of f32 products are. */
 enum { GS_ACT_NONE = 0, GS_ACT_RELU = 1, GS_ACT_SILU = 2, GS_ACT_GELU = 3, GS_ACT_SIGMOID = 4 };
 
 /* out = act(z) + residual, z = x w^T + bias, with
