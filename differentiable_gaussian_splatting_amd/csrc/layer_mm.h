@@ -104,12 +104,12 @@ __device__ __forceinline__ gst::Pack<S, N> upto(const S* p, int64_t n)
     return v;
 }
 
-// columns n + first .. n + 3 of row m of the product
-template <typename S>
+// columns n + first .. n + 3 of row m of the product; DOWN: e.down may be there
+template <typename S, bool DOWN = false>
 __device__ __forceinline__ void epilogue(const Epilogue& e, int64_t m, int64_t n, f32x4 z, int first = 0)
 {
     const int valid = (int)min((int64_t)4, e.n - n);
-    if (e.down) z *= e.down[m * e.lddown];
+    if constexpr (DOWN) { if (e.down) z *= e.down[m * e.lddown]; }
     if (e.bias) z += load4<S>(e.bias, n, e.bias_type, valid, first);
     if (e.pre) store4<S>(e.pre, m * e.ldpre + n, e.pre_type, valid, z, first);
     if (e.act != GS_ACT_NONE) {
@@ -184,8 +184,11 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
     constexpr int G = GATED ? 2 : 1;
     const int64_t rest = g.tm * g.tn - g.full, total = g.full + rest * g.splits;
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    // only the gradients' products have a scaled dz; the code of the others stays without it
+    // (8192 x 4096 -> 11008 bf16 forward 880 us with it, 843 without)
+    constexpr bool kScaled = std::is_same<S, f16>::value && BCOL;
     Operand ga = g.a;
-    if (g.other && *g.other) ga.p = g.a_other;
+    if constexpr (kScaled) { if (g.other && *g.other) ga.p = g.a_other; }
     for (int64_t b = block; b < total; b += blocks) {
         int64_t tile = b, k0 = 0, k1 = g.k, i, j;
         float* ws = nullptr;
@@ -207,7 +210,7 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
 #pragma unroll
             for (int r = 0; r < T::MI; ++r) acc[q][r] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
         if (b != block) __syncthreads();   // the previous tile's reads of lds
-        mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(ga, g.b, m0, n0, k0, k1, lds.tile, acc);
+        mm_tile<S, P, ACOL, BCOL, T, false, DIRECT>(kScaled ? ga : g.a, g.b, m0, n0, k0, k1, lds.tile, acc);
         // The results go through LDS, 32 rows of each wave at a time, so that a
         // lane takes four columns next to its neighbours' (whole lines are
         // read and written) and the epilogue's code is a loop.
@@ -230,21 +233,19 @@ __device__ __forceinline__ void layer_mm(const LayerMm& g, int64_t block, int64_
                 if (m >= g.m || n >= g.e.n || m < sm.own || n + 3 < sn.own) continue;
                 const int first = (int)max((int64_t)0, sn.own - n);
                 const float* v = mine + row * kRow + (GATED ? (c >> 4) * 32 + (c & 15) : c);
-                f32x4 x = *reinterpret_cast<const f32x4*>(v), y = x;
-                if constexpr (GATED) y = *reinterpret_cast<const f32x4*>(v + 16);
-                if constexpr (P == 3) {
-                    const int valid = (int)min((int64_t)4, g.e.n - n);
-                    x = sum_again<ACOL, BCOL>(ga, g.b, m, n, valid, k0, k1, x);
-                    if constexpr (GATED) y = sum_again<ACOL, BCOL>(ga, g.b, m, g.e.n + n, valid, k0, k1, y);
-                }
+                f32x4 x = *reinterpret_cast<const f32x4*>(v), y;
+                if constexpr (P == 3) x = sum_again<ACOL, BCOL>(g.a, g.b, m, n, (int)min((int64_t)4, g.e.n - n), k0, k1, x);
+                if constexpr (GATED && P == 3)
+                    y = sum_again<ACOL, BCOL>(g.a, g.b, m, g.e.n + n, (int)min((int64_t)4, g.e.n - n), k0, k1,
+                                              *reinterpret_cast<const f32x4*>(v + 16));
                 if (ws) {
                     float* w = ws + (m - m0) * T::BN + (wave / T::WM) * T::NI * 16 + (v - mine - row * kRow);
                     *reinterpret_cast<f32x4*>(w) = x;
-                    if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = y;
+                    if constexpr (GATED) *reinterpret_cast<f32x4*>(w + 16) = P == 3 ? y : *reinterpret_cast<const f32x4*>(v + 16);
                 } else if constexpr (GATED) {
-                    epilogue_gated<S>(g.e, m, n, x, y, first);
+                    epilogue_gated<S>(g.e, m, n, x, P == 3 ? y : *reinterpret_cast<const f32x4*>(v + 16), first);
                 } else {
-                    epilogue<S>(g.e, m, n, x, first);
+                    epilogue<S, kScaled>(g.e, m, n, x, first);
                 }
             }
             wave_fence();
@@ -291,7 +292,7 @@ __global__ __launch_bounds__(256) void k_join(const LayerMm g)
         }
         const int first = (int)max((int64_t)0, sn.own - n);
         if constexpr (GATED) epilogue_gated<S>(g.e, m, n, x, y, first);
-        else epilogue<S>(g.e, m, n, x, first);
+        else epilogue<S, std::is_same<S, f16>::value>(g.e, m, n, x, first);
     }
 }
 

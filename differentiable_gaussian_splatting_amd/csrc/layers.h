@@ -69,8 +69,6 @@ __device__ __forceinline__ float larger(float most, float v)
 // in pre (each null: not there).  Types are GS_F32 or the product's own.  down:
 // what the row's sums are multiplied with first, at m lddown.
 struct Epilogue {
-    const float* down;
-    int64_t lddown;
     const void* bias;
     const void* res;
     void* pre;
@@ -79,12 +77,12 @@ struct Epilogue {
     int64_t n;                   // columns of out
     int32_t act;
     int8_t bias_type, res_type, pre_type, out_type;
+    const float* down;
+    int64_t lddown;
 };
 
 struct LayerMm {
     Operand a, b;                // rows of out, columns of out
-    const void* a_other;         // what a is instead of a.p if *other is not 0 (other null: it stays)
-    const int32_t* other;
     int64_t m, k;
     Epilogue e;
     int64_t tm, tn;              // tiles
@@ -93,6 +91,8 @@ struct LayerMm {
     int64_t kper;                // a multiple of the tile's step,
     float* ws;                   // whose sums are kept here: [splits][tiles - full][rows][columns of a tile]
     bool a_col, b_col, gated;    // a_col only with b_col
+    const void* a_other;         // what a is instead of a.p if *other is not 0 (other null: it stays)
+    const int32_t* other;
 };
 
 // Whether the tiles of a product of 16-bit operands load straight into LDS
