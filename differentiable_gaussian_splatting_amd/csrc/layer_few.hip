@@ -11,8 +11,8 @@
 // workspace or second launch is needed.  x comes out of the L2, once per block.
 // f32 uses the f32 matrix instruction: the rate does not matter here.
 //
-// One row of 4096 x 4096 bf16: 8.6 us (3.9 TB/s); four rows of 2 x 11008 x 4096
-// gated: 34 us (5.3 TB/s).  Sixteen waves a block take 9.6 us for the former;
+// One row of 4096 x 4096 bf16: 9.0 us (3.7 TB/s); four rows of 2 x 11008 x 4096
+// gated: 35 us (5.1 TB/s).  Sixteen waves a block take 9.6 us for the former;
 // without the barrier before the products the compiler keeps two loads under
 // way and the latter takes 40.
 #include <algorithm>

@@ -10,11 +10,12 @@
 // bias and residual and writes its outputs in packs of four.  Everything in it
 // is f32; each output is rounded once.
 //
-// Large products are bound by the matrix cores: 8192^3 bf16 952 us, 1155
-// TFLOP/s (the library's product 1170 to 1250); 8192 x 4096 -> 2 x 11008 gated
-// bf16 1480 (1000 TFLOP/s), where 540 MB of outputs are written after the
-// products of a tile; f32 in three parts 8192 x 2048 -> 4096 640 us (215
-// TFLOP/s, 1290 of the 16-bit products; the library's f32 product 120 to 150).
+// Large products are bound by the matrix cores: 8192^3 bf16 970 to 990 us, 1110
+// to 1130 TFLOP/s (the library's product 1530 to 1570 on the same cards); 8192 x
+// 4096 -> 2 x 11008 gated bf16 1490 to 1560 (950 to 990 TFLOP/s), where 540 MB of
+// outputs are written after the products of a tile; f32 in three parts 8192 x
+// 2048 -> 4096 680 to 790 us (175 to 200 TFLOP/s, 1050 to 1200 of the 16-bit
+// products; the library's f32 product 148).
 #pragma once
 
 #include <algorithm>

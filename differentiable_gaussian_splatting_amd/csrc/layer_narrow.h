@@ -17,8 +17,8 @@
 // is above what memory feeds it).
 //
 // 1M rows, f32: 32 -> 48 forward 86 us (3.7 TB/s), 32 -> 64 relu backward 166
-// (4.6 TB/s; 670 with dz in memory and tiles); 64 -> 64 forward 170, where the
-// f32 products take 52 and hide only in part.
+// (4.6 TB/s; 670 with dz in memory and tiles); 64 -> 64 forward 118, with a
+// bias 153, with silu too 170, where the f32 products take 52 and hide only in part.
 #pragma once
 
 #include "layer_mm.h"

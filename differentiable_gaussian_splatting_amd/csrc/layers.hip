@@ -439,7 +439,7 @@ gs_status launch_linear_bwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w,
     }
     // Small products share a launch: their tiles fill the card together, and a
     // launch costs the host 3 us (us apart / together: 148 rows of 234 -> 365
-    // gated f16 24.4 / 17.8, 2000 of 300 -> 300 f32 38.9 / 30.7; 43 of 4864 ->
+    // gated, 16-bit without f16's pass for the largest, 24.4 / 17.8, 2000 of 300 -> 300 f32 38.9 / 30.7; 43 of 4864 ->
     // 6912 bf16, where the products are long, 86 / 91).
     const bool pair = gx.m > 0 && gw.m > 0 && gx.tile == kSmall && gw.tile == kSmall &&
                       (double)m * (double)n * (double)k <= 5e8;

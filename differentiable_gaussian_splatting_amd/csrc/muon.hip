@@ -16,11 +16,12 @@
 // part each would lose 2^-9 of X per step, and the polynomial multiplies what
 // the first steps lose by up to a^5 = 485.
 //
-// The products bound it: 3 matrices of 4096 x 4096 12.8 ms, of which 12.4 are
-// products at 310 to 370 TFLOP/s (three f16 products each; G and P by half
-// their tiles); 24 of 2048 x 515 1.6 ms, where a fifth to a third of the tiles
-// is padding.  A few matrices of 64 x 48 take one launch and 23 us, fifteen
-// products that wait for each other.
+// The products bound it: 3 matrices of 4096 x 4096 12.9 to 13.6 ms, all but 0.4
+// of it products at 295 to 360 TFLOP/s (three f16 products each; G and P by half
+// their tiles); 24 of 2048 x 515 1.6 to 1.75 ms, where a fifth to a third of the
+// tiles is padding and each splits its f32 values again at every step of k.  A
+// few matrices of 64 x 48 take one launch and 24 us, fifteen products that wait
+// for each other.
 #include <algorithm>
 #include <cmath>
 
