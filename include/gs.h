@@ -526,6 +526,8 @@ gs_status gs_linear_fwd(gs_ctx* ctx, const gs_tensor* x, const gs_tensor* w, con
  * range f32 values may leave, after scaling by powers of two that are taken back
  * in f32: a finite value stays finite, and its error is at most 2^-11 of itself or,
  * for dx 2^-25 of its row's largest finite |dz|, for dw 2^-39 of the call's.
+ * Which powers these are depends on all rows of the call, so that small values of
+ * a row's dz may be rounded otherwise, within that error, beside other rows.
  * dx, dw, dbias: each may be NULL: not wanted.  Without rows, dw and dbias are
  * zero (or stay).  An output overlaps no input and no other output.  Errors: as
  * gs_linear_fwd. */
